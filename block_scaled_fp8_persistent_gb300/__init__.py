@@ -29,17 +29,23 @@ STATUS_NAMES = {
     0: "BSFP8_OK", 1: "BSFP8_ERR_NULL", 2: "BSFP8_ERR_SHAPE", 3: "BSFP8_ERR_ALIGN",
     4: "BSFP8_ERR_UNSUPPORTED_DEVICE", 5: "BSFP8_ERR_CUDA", 6: "BSFP8_ERR_DEVICE_OFFSETS",
     7: "BSFP8_ERR_DEVICE_TIMEOUT", 8: "BSFP8_ERR_DEVICE_EXPERT_IDS", 9: "BSFP8_ERR_FORMAT",
-    10: "BSFP8_ERR_DEVICE_BOUNDS",
+    10: "BSFP8_ERR_DEVICE_BOUNDS", 11: "BSFP8_ERR_DEVICE_ROWS",
 }
 
 # bsmx_format values of include/bsfp8.h
 FORMATS = {"mxfp8": 0, "mxfp4": 1, "nvfp4": 2}
+# of the operators that write a GEMM's operand (blockwise: A of bsfp8_grouped_gemm)
+QUANT_FORMATS = {**FORMATS, "blockwise": 3}
+# bsmx_type values
+TYPES = {"bf16": 0, "fp16": 1, "fp32": 2}
 
 # Every symbol include/bsfp8.h declares (the CPU test checks the library exports them).
 EXPORTED = ("bsfp8_grouped_gemm", "bsmxfp8_grouped_gemm", "bsfp8_grouped_gemm_ids",
             "bsmxfp8_grouped_gemm_ids", "bsmxfp8_pack_b_scales", "bsmxfp8_grouped_gemm_prepacked",
             "bsmxfp8_tmem_plan", "bsfp8_blockwise_plan", "bsmxfp8_plan", "bsmx_plan",
-            "bsmx_grouped_gemm", "bsfp8_get_device_error", "bsfp8_check_wait_timeout",
+            "bsmx_grouped_gemm", "bsmx_quantize", "bsmx_rmsnorm_quant", "bsmx_swiglu_quant",
+            "bsmx_moe_sort_workspace", "bsmx_moe_sort", "bsmx_moe_combine",
+            "bsmx_moe_combine_backward", "bsfp8_get_device_error", "bsfp8_check_wait_timeout",
             "bsfp8_status_string")
 
 
@@ -85,6 +91,21 @@ def load_library() -> ctypes.CDLL:
         lib.bsmxfp8_plan.restype = i32
         lib.bsmx_plan.argtypes = [ctypes.c_int64, i32, ctypes.POINTER(ctypes.c_int32)]
         lib.bsmx_plan.restype = i32
+        f32 = ctypes.c_float
+        lib.bsmx_quantize.argtypes = [i32, i32, p, p, i32, p, p, i64, i64, i32, p]
+        lib.bsmx_quantize.restype = i32
+        lib.bsmx_rmsnorm_quant.argtypes = [i32, i32, p, p, p, f32, p, p, p, p, i64, i32, p]
+        lib.bsmx_rmsnorm_quant.restype = i32
+        lib.bsmx_swiglu_quant.argtypes = [i32, p, p, p, i64, i32, p]
+        lib.bsmx_swiglu_quant.restype = i32
+        lib.bsmx_moe_sort_workspace.argtypes = [i64, i32, i32, ctypes.POINTER(ctypes.c_int64)]
+        lib.bsmx_moe_sort_workspace.restype = i32
+        lib.bsmx_moe_sort.argtypes = [p, p, p, p, p, i64, i64, i32, i32, p]
+        lib.bsmx_moe_sort.restype = i32
+        lib.bsmx_moe_combine.argtypes = [p, p, p, p, p, i64, i64, i32, i32, p]
+        lib.bsmx_moe_combine.restype = i32
+        lib.bsmx_moe_combine_backward.argtypes = [p, p, p, p, p, p, i64, i64, i32, i32, p]
+        lib.bsmx_moe_combine_backward.restype = i32
         lib.bsfp8_get_device_error.argtypes = [p, ctypes.POINTER(ctypes.c_int)]
         lib.bsfp8_get_device_error.restype = i32
         lib.bsfp8_check_wait_timeout.argtypes = [ctypes.c_int64, p]
@@ -198,6 +219,164 @@ def bsmxfp8_grouped_gemm_prepacked(A, B, a_scales, b_scales_packed, expert_offse
         _addr(C), int(M_total), int(N), int(K), int(num_experts), _stream(stream))
     if st != BSFP8_OK:
         raise BsFp8Error(st, "bsmxfp8_grouped_gemm_prepacked")
+
+
+# ---------------------------------------------------------------------------------------
+# the operators around the grouped GEMM
+# ---------------------------------------------------------------------------------------
+def _buf(x, count: int, sizes: tuple, name: str) -> int | None:
+    """Address of a buffer that must hold at least `count` elements of one of `sizes` bytes; a
+    raw address or None passes unchecked."""
+    if x is None:
+        return None
+    if isinstance(x, int):
+        return x or None
+    if not x.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor (device memory)")
+    if not x.is_contiguous():
+        raise ValueError(f"{name} must be contiguous (row-major)")
+    if x.itemsize not in sizes:
+        raise ValueError(f"{name} has elements of {x.itemsize} bytes, wanted {sizes}")
+    if x.numel() < count:
+        raise ValueError(f"{name} holds {x.numel()} elements, needs {count}")
+    return x.data_ptr() or None
+
+
+_TYPE_OF = {"torch.bfloat16": 0, "torch.float16": 1, "torch.float32": 2}
+
+
+def _type_code(x, given: str | None, allowed: tuple, name: str) -> int:
+    """bsmx_type of a tensor, or of a raw address by the name given for it."""
+    if given is not None:
+        code = TYPES[given]
+    elif isinstance(x, int):
+        raise ValueError(f"{name} is a raw address: its type has to be given")
+    else:
+        code = _TYPE_OF.get(str(x.dtype), -1)
+    if code not in allowed:
+        raise ValueError(f"{name} has an unsupported type")
+    return code
+
+
+def _bf16(x, count: int, name: str) -> int | None:
+    if x is not None and not isinstance(x, int) and str(x.dtype) != "torch.bfloat16":
+        raise ValueError(f"{name} must be bf16")
+    return _buf(x, count, (2,), name)
+
+
+def _operand(format: str, q, scales, rows: int, K: int):
+    """(address of q, address of scales) of an operand of rows x K in `format`."""
+    if format == "blockwise":
+        return _buf(q, rows * K, (1,), "q"), _buf(scales, rows * (K // 128), (4,), "scales")
+    if format == "mxfp8":
+        return _buf(q, rows * K, (1,), "q"), _buf(scales, rows * (K // 32), (1,), "scales")
+    vec = 16 if format == "nvfp4" else 32
+    return _buf(q, rows * (K // 2), (1,), "q"), _buf(scales, rows * (K // vec), (1,), "scales")
+
+
+def bsmx_quantize(format: str, x, q, scales, rows: int, K: int, row_of_slot=None, top_k: int = 1,
+                  out_rows: int | None = None, x_type: str | None = None, stream=None) -> None:
+    """Quantise x [rows, K] (bf16, fp16 or fp32) into the operand (q, scales) of `format`
+    ("mxfp8", "mxfp4", "nvfp4", "blockwise"); with row_of_slot, row t goes to each of the rows
+    row_of_slot[t, :] of an operand of out_rows rows.  See include/bsfp8.h.  Raises BsFp8Error."""
+    out_rows = rows if out_rows is None else out_rows
+    qa, sa = _operand(format, q, scales, out_rows, K)
+    st = load_library().bsmx_quantize(
+        QUANT_FORMATS[format], _type_code(x, x_type, (0, 1, 2), "x"),
+        _buf(x, rows * K, (2, 4), "x"), _buf(row_of_slot, rows * top_k, (4,), "row_of_slot"),
+        top_k, qa, sa, rows, out_rows, K, _stream(stream))
+    if st != BSFP8_OK:
+        raise BsFp8Error(st, "bsmx_quantize")
+
+
+def bsmx_rmsnorm_quant(format: str, x, weight, eps: float, rows: int, K: int, residual=None,
+                       residual_out=None, y=None, q=None, scales=None,
+                       residual_type: str | None = None, stream=None) -> None:
+    """h = x + residual, y = h / sqrt(mean(h^2) + eps) * weight; writes h to residual_out, y in
+    bf16 to y and y quantised in `format` to (q, scales), each where it is given.  See
+    include/bsfp8.h.  Raises BsFp8Error."""
+    rt = 0
+    if residual is not None or residual_out is not None:
+        rt = _type_code(residual if residual is not None else residual_out, residual_type, (0, 2),
+                        "residual")
+        if residual is not None and residual_out is not None and residual_type is None \
+                and rt != _type_code(residual_out, None, (0, 2), "residual_out"):
+            raise ValueError("residual and residual_out differ in type")
+    size = (4,) if rt == 2 else (2,)
+    qa, sa = _operand(format, q, scales, rows, K) if q is not None else (None, None)
+    st = load_library().bsmx_rmsnorm_quant(
+        QUANT_FORMATS[format], rt, _bf16(x, rows * K, "x"),
+        _buf(residual, rows * K, size, "residual"), _bf16(weight, K, "weight"), eps,
+        _buf(residual_out, rows * K, size, "residual_out"), _bf16(y, rows * K, "y"), qa, sa,
+        rows, K, _stream(stream))
+    if st != BSFP8_OK:
+        raise BsFp8Error(st, "bsmx_rmsnorm_quant")
+
+
+def bsmx_swiglu_quant(format: str, h, q, scales, rows: int, N: int, stream=None) -> None:
+    """silu(h[:, :N]) * h[:, N:] of bf16 h [rows, 2N], quantised in `format` into (q, scales).
+    See include/bsfp8.h.  Raises BsFp8Error."""
+    qa, sa = _operand(format, q, scales, rows, N)
+    st = load_library().bsmx_swiglu_quant(QUANT_FORMATS[format], _bf16(h, rows * 2 * N, "h"), qa,
+                                          sa, rows, N, _stream(stream))
+    if st != BSFP8_OK:
+        raise BsFp8Error(st, "bsmx_swiglu_quant")
+
+
+def bsmx_moe_sort_workspace(rows: int, top_k: int, num_experts: int) -> int:
+    """Bytes of workspace that bsmx_moe_sort needs (host only)."""
+    out = ctypes.c_int64(0)
+    st = load_library().bsmx_moe_sort_workspace(rows, top_k, num_experts, ctypes.byref(out))
+    if st != BSFP8_OK:
+        raise BsFp8Error(st, "bsmx_moe_sort_workspace")
+    return out.value
+
+
+def bsmx_moe_sort(topk_ids, offsets, row_of_slot, workspace, rows: int, top_k: int,
+                  num_experts: int, slot_of_row=None, workspace_bytes: int | None = None,
+                  stream=None) -> None:
+    """Sort the slots of int32 topk_ids [rows, top_k] by expert: int32 offsets [num_experts + 2],
+    row_of_slot [rows, top_k] (-1: dropped) and slot_of_row.  See include/bsfp8.h.  Raises
+    BsFp8Error."""
+    slots = rows * top_k
+    if workspace_bytes is None:
+        if isinstance(workspace, int):
+            raise ValueError("workspace is a raw address: workspace_bytes has to be given")
+        workspace_bytes = 0 if workspace is None else workspace.numel() * workspace.itemsize
+    st = load_library().bsmx_moe_sort(
+        _buf(topk_ids, slots, (4,), "topk_ids"), _buf(offsets, num_experts + 2, (4,), "offsets"),
+        _buf(row_of_slot, slots, (4,), "row_of_slot"),
+        _buf(slot_of_row, slots, (4,), "slot_of_row"), _addr(workspace), workspace_bytes, rows,
+        top_k, num_experts, _stream(stream))
+    if st != BSFP8_OK:
+        raise BsFp8Error(st, "bsmx_moe_sort")
+
+
+def bsmx_moe_combine(C, row_of_slot, out, rows: int, in_rows: int, top_k: int, N: int,
+                     weights=None, residual=None, stream=None) -> None:
+    """out[t] = residual[t] + sum_j weights[t, j] * C[row_of_slot[t, j]] over the slots that were
+    not dropped.  See include/bsfp8.h.  Raises BsFp8Error."""
+    st = load_library().bsmx_moe_combine(
+        _bf16(C, in_rows * N, "C"), _buf(row_of_slot, rows * top_k, (4,), "row_of_slot"),
+        _buf(weights, rows * top_k, (4,), "weights"), _bf16(residual, rows * N, "residual"),
+        _bf16(out, rows * N, "out"), rows, in_rows, top_k, N, _stream(stream))
+    if st != BSFP8_OK:
+        raise BsFp8Error(st, "bsmx_moe_combine")
+
+
+def bsmx_moe_combine_backward(d_out, C, row_of_slot, weights, dC, d_weights, rows: int,
+                              in_rows: int, top_k: int, N: int, stream=None) -> None:
+    """Gradient of bsmx_moe_combine: dC[row_of_slot[t, j]] = weights[t, j] * d_out[t] and
+    d_weights[t, j] = <d_out[t], C[row_of_slot[t, j]]>.  See include/bsfp8.h.  Raises
+    BsFp8Error."""
+    st = load_library().bsmx_moe_combine_backward(
+        _bf16(d_out, rows * N, "d_out"), _bf16(C, in_rows * N, "C"),
+        _buf(row_of_slot, rows * top_k, (4,), "row_of_slot"),
+        _buf(weights, rows * top_k, (4,), "weights"), _bf16(dC, in_rows * N, "dC"),
+        _buf(d_weights, rows * top_k, (4,), "d_weights"), rows, in_rows, top_k, N,
+        _stream(stream))
+    if st != BSFP8_OK:
+        raise BsFp8Error(st, "bsmx_moe_combine_backward")
 
 
 def bsmxfp8_tmem_plan(block_k: int, epilogue_n: int, vec: int, overlap: bool) -> dict:

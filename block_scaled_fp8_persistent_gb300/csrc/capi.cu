@@ -238,6 +238,13 @@ int choose_mx_token_tile(int64_t M_total, int E) {
 }  // namespace
 }  // namespace bsfp8
 
+int bsfp8::device_error_word(int** err) {
+  DeviceInfo* dev = nullptr;
+  const bsfp8_status st = device_info(&dev);
+  if (st == BSFP8_OK) *err = dev->err_word;
+  return st;
+}
+
 using namespace bsfp8;
 
 namespace bsfp8 {
@@ -578,6 +585,7 @@ extern "C" const char* bsfp8_status_string(bsfp8_status s) {
     case BSFP8_ERR_DEVICE_OFFSETS: return "device: invalid expert offsets";
     case BSFP8_ERR_DEVICE_TIMEOUT: return "device: pipeline wait timed out";
     case BSFP8_ERR_DEVICE_EXPERT_IDS: return "device: expert id out of range";
+    case BSFP8_ERR_DEVICE_ROWS: return "device: row map entry out of range";
     case BSFP8_ERR_FORMAT: return "unsupported operand format pair";
     case BSFP8_ERR_DEVICE_BOUNDS: return "device (debug build): tile outside the problem";
   }

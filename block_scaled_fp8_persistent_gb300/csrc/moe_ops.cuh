@@ -1,0 +1,86 @@
+// Launchers of the operators around the grouped GEMM (moe_quant.cu, moe_route.cu) for the
+// C-ABI layer (capi_moe.cu).  Each returns the launch error; sizes and alignment are checked
+// by the caller.
+#pragma once
+#include <cuda_runtime.h>
+#include <cstdint>
+
+namespace bsfp8 {
+
+enum ElementType : int { E_BF16 = 0, E_FP16 = 1, E_FP32 = 2 };
+
+struct QuantizeArgs {
+  const void* x;               // [rows, K]
+  const int32_t* row_of_slot;  // [rows * top_k], or nullptr: row t of q from row t of x
+  uint8_t* q;
+  void* scales;
+  int64_t rows, out_rows;
+  int top_k, K;
+  int* err;
+};
+cudaError_t launch_quantize(int format, int x_type, const QuantizeArgs& a, cudaStream_t stream);
+
+struct NormArgs {
+  const void* x;         // bf16 [rows, K]
+  const void* residual;  // bf16 or fp32 [rows, K], or nullptr
+  const void* weight;    // bf16 [K]
+  void* residual_out;    // as residual, or nullptr
+  void* y;               // bf16 [rows, K], or nullptr
+  uint8_t* q;            // or nullptr
+  void* scales;
+  int64_t rows;
+  int K;
+  float eps;
+};
+constexpr int kNormMaxK = 32768;
+cudaError_t launch_rmsnorm_quant(int format, int residual_type, const NormArgs& a,
+                                 cudaStream_t stream);
+
+struct SwigluArgs {
+  const void* h;  // bf16 [rows, 2N], gate then up
+  uint8_t* q;
+  void* scales;
+  int64_t rows;
+  int N;
+};
+cudaError_t launch_swiglu_quant(int format, const SwigluArgs& a, cudaStream_t stream);
+
+struct SortArgs {
+  const int32_t* ids;    // [slots]
+  int32_t* offsets;      // [experts + 2]
+  int32_t* row_of_slot;  // [slots]
+  int32_t* slot_of_row;  // [slots], or nullptr
+  int32_t* workspace;
+  int64_t slots;
+  int experts;
+};
+constexpr int kSortMaxExperts = 4096;
+int64_t moe_sort_workspace_bytes(int64_t slots, int experts);
+cudaError_t launch_moe_sort(const SortArgs& a, cudaStream_t stream);
+
+struct CombineArgs {
+  const void* C;               // bf16 [in_rows, N]
+  const int32_t* row_of_slot;  // [rows * top_k]
+  const float* weights;        // [rows * top_k], or nullptr: 1
+  const void* residual;        // bf16 [rows, N], or nullptr
+  void* out;                   // bf16 [rows, N]
+  int64_t rows, in_rows;
+  int top_k, N;
+  int* err;
+};
+cudaError_t launch_moe_combine(const CombineArgs& a, cudaStream_t stream);
+
+struct CombineBackwardArgs {
+  const void* d_out;           // bf16 [rows, N]
+  const void* C;               // bf16 [in_rows, N]
+  const int32_t* row_of_slot;  // [rows * top_k]
+  const float* weights;        // [rows * top_k]
+  void* dC;                    // bf16 [in_rows, N]
+  float* d_weights;            // [rows * top_k]
+  int64_t rows, in_rows;
+  int top_k, N;
+  int* err;
+};
+cudaError_t launch_moe_combine_backward(const CombineBackwardArgs& a, cudaStream_t stream);
+
+}  // namespace bsfp8

@@ -64,17 +64,24 @@ typedef enum {
   BSFP8_ERR_DEVICE_OFFSETS = 6,     /* device error word: invalid expert offsets */
   BSFP8_ERR_DEVICE_TIMEOUT = 7,     /* device error word: a pipeline wait gave up */
   BSFP8_ERR_DEVICE_EXPERT_IDS = 8,  /* device error word: an expert id outside [0, num_experts) */
-  BSFP8_ERR_FORMAT = 9,             /* bsmx_grouped_gemm: unsupported operand format pair */
-  BSFP8_ERR_DEVICE_BOUNDS = 10      /* device error word, debug builds only: a tile's rows,
+  BSFP8_ERR_FORMAT = 9,             /* bsmx_grouped_gemm: unsupported operand format pair;
+                                       the operators around it: unknown format or type */
+  BSFP8_ERR_DEVICE_BOUNDS = 10,     /* device error word, debug builds only: a tile's rows,
                                        columns or expert fell outside the problem */
+  BSFP8_ERR_DEVICE_ROWS = 11        /* device error word: a row map names a row that is not there */
 } bsfp8_status;
 
-/* Operand formats of bsmx_grouped_gemm. */
+/* Operand formats of bsmx_grouped_gemm, and of the operators that write its operands. */
 typedef enum {
   BSMX_MXFP8 = 0, /* e4m3 elements, one byte each;        UE8M0 scale per 32 elements of K */
   BSMX_MXFP4 = 1, /* e2m1 elements, two per byte along K; UE8M0 scale per 32 elements of K */
-  BSMX_NVFP4 = 2  /* e2m1 elements, two per byte along K; e4m3 scale per 16 elements of K */
+  BSMX_NVFP4 = 2, /* e2m1 elements, two per byte along K; e4m3 scale per 16 elements of K */
+  BSMX_BLOCKWISE = 3 /* e4m3 elements; fp32 scale per 128 elements of K, laid out [K/128, rows]:
+                        A and a_scales of bsfp8_grouped_gemm (not of bsmx_grouped_gemm) */
 } bsmx_format;
+
+/* Types of the unquantised inputs. */
+typedef enum { BSMX_BF16 = 0, BSMX_FP16 = 1, BSMX_FP32 = 2 } bsmx_type;
 
 /*
  * Blockwise FP8 grouped GEMM (1x128 A scales, 128x128 B scales).
@@ -265,6 +272,119 @@ bsfp8_status bsmx_grouped_gemm(int a_format, int b_format, const void* A, const 
                                int num_groups, int num_experts, cudaStream_t stream);
 
 /*
+ * The operators around the grouped GEMM: a mixture-of-experts layer is
+ *
+ *   bsmx_rmsnorm_quant   residual + norm, in bf16 for the router and / or quantised
+ *   bsmx_moe_sort        the chosen experts -> group offsets and every slot's row
+ *   bsmx_quantize        each token's row, quantised, to the rows of its slots = the GEMM's A
+ *   (grouped GEMM)       h = [gate | up]
+ *   bsmx_swiglu_quant    the second GEMM's A
+ *   (grouped GEMM)
+ *   bsmx_moe_combine     weighted sum of each token's rows
+ *
+ * on one stream with nothing read back.  The conventions above hold: device pointers, buffers
+ * of the caller's, row-major and contiguous, asynchronous, host-detectable errors return a
+ * status with nothing launched.  rows == 0 is a valid no-op (row buffers may be NULL).
+ * Sizes: rows, out_rows, in_rows and rows * top_k at most 2^31 - 1, 1 <= top_k <= 64.
+ *
+ * Quantisation (`format`, a bsmx_format).  With a the largest magnitude of a scale block,
+ *   MXFP8, MXFP4  scale 2^ceil(log2(a / 448)) or 2^ceil(log2(a / 6)), never below 2^-127
+ *   NVFP4         scale a / 6 rounded to e4m3, at least 2^-9 and at most 448
+ *   BLOCKWISE     scale a / 448 in fp32, at least 2^-126
+ * and each element is value / scale rounded to the nearest code, ties to even, saturating
+ * (BLOCKWISE multiplies by the scale's fp32 reciprocal, NVFP4 divides, MX is exact).  A block
+ * of zeros has scale 1; a block that holds a NaN or an infinity has a NaN scale (UE8M0 0xFF,
+ * e4m3 0x7F, fp32 NaN), so that what is computed of it is NaN.  q is 16-byte aligned; K and N
+ * are multiples of 128; inputs are 16-byte aligned (32-byte aligned ones are read with 32-byte
+ * loads).  BSFP8_ERR_FORMAT for a format or type that is not listed.
+ */
+
+/*
+ * Quantises x [rows, K] of type x_type (a bsmx_type) into q and scales, an operand of out_rows
+ * rows in `format`.
+ *   row_of_slot NULL  row t of q is row t of x; top_k == 1, out_rows == rows
+ *   row_of_slot       int32 [rows, top_k] (bsmx_moe_sort): row t of x, quantised once, is
+ *                     written to each row row_of_slot[t, j] of q.  Negative entries are
+ *                     skipped; an entry >= out_rows is skipped and recorded as
+ *                     BSFP8_ERR_DEVICE_ROWS.  Rows that no slot names are left as they are.
+ * The gradient of the mapped form (straight through the rounding) is bsmx_moe_combine of the
+ * gradient of q's rows without weights.
+ */
+bsfp8_status bsmx_quantize(int format, int x_type, const void* x, const int32_t* row_of_slot,
+                           int top_k, void* q, void* scales, int64_t rows, int64_t out_rows,
+                           int K, cudaStream_t stream);
+
+/*
+ * Root-mean-square norm with the residual's addition:
+ *   h = x + residual            residual NULL: h = x
+ *   y = h / sqrt(mean_k(h^2) + eps) * weight
+ * all in fp32.  x and weight are bf16 [rows, K] and [K]; residual and residual_out are of
+ * residual_type (BSMX_BF16 or BSMX_FP32).  Outputs, each optional but not all NULL:
+ * residual_out = h (may be the residual's own buffer), y in bf16, and y (unrounded) quantised
+ * into q and scales.  K <= 32768; eps positive and finite (BSFP8_ERR_SHAPE).  A row whose
+ * squares sum past fp32's range comes out as zeros.
+ */
+bsfp8_status bsmx_rmsnorm_quant(int format, int residual_type, const void* x,
+                                const void* residual, const void* weight, float eps,
+                                void* residual_out, void* y, void* q, void* scales, int64_t rows,
+                                int K, cudaStream_t stream);
+
+/*
+ * SwiGLU of the first GEMM's output, quantised as the second's A:
+ *   h bf16 [rows, 2N], gate g = h[:, :N], up u = h[:, N:];   q, scales = g / (1 + exp(-g)) * u
+ * computed in fp32 and not rounded before it is quantised.
+ */
+bsfp8_status bsmx_swiglu_quant(int format, const void* h, void* q, void* scales, int64_t rows,
+                               int N, cudaStream_t stream);
+
+/*
+ * Sorts the slots (token t's j-th choice is slot t * top_k + j) by expert; slots of one expert
+ * keep their order.
+ *   topk_ids     int32 [rows, top_k]; an id outside [0, num_experts) drops its slot (padding, or
+ *                an expert of another rank)
+ *   offsets      int32 [num_experts + 2]: expert e owns rows offsets[e] .. offsets[e+1]-1;
+ *                offsets[num_experts] = slots kept, offsets[num_experts + 1] = rows * top_k
+ *   row_of_slot  int32 [rows, top_k]: the slot's row, -1 where it was dropped
+ *   slot_of_row  int32 [rows * top_k], or NULL: its inverse, -1 for rows past the kept ones
+ *   workspace    bsmx_moe_sort_workspace bytes, 4-byte aligned (NULL where that is 0)
+ * The first num_experts + 1 offsets are a grouped GEMM's when nothing is dropped.  With dropped
+ * slots either pass the kept count as M_total, or keep M_total = rows * top_k without reading
+ * it back: all num_experts + 2 offsets are those of num_experts + 1 groups, the last being the
+ * rows of dropped slots, under any valid expert id (bsfp8_grouped_gemm_ids and its kin); what
+ * it computes for them is not read by bsmx_moe_combine.
+ * num_experts <= 4096.  BSFP8_ERR_SHAPE for a workspace that is too small.
+ */
+bsfp8_status bsmx_moe_sort_workspace(int64_t rows, int top_k, int num_experts, int64_t* bytes);
+bsfp8_status bsmx_moe_sort(const int32_t* topk_ids, int32_t* offsets, int32_t* row_of_slot,
+                           int32_t* slot_of_row, void* workspace, int64_t workspace_bytes,
+                           int64_t rows, int top_k, int num_experts, cudaStream_t stream);
+
+/*
+ * Weighted sum of each token's rows:
+ *   out[t] = bf16( residual[t] + sum_j weights[t, j] * C[row_of_slot[t, j]] )
+ * in fp32, j ascending, over the slots whose row is not negative (a row of a dropped slot is
+ * not read, whatever its weight).  C bf16 [in_rows, N]; weights fp32 [rows, top_k] or NULL for
+ * 1; residual bf16 [rows, N] or NULL; out bf16 [rows, N] (may be the residual's own buffer).
+ * N % 8 == 0, N <= 2^24.  An entry >= in_rows counts as dropped and is recorded as
+ * BSFP8_ERR_DEVICE_ROWS.
+ */
+bsfp8_status bsmx_moe_combine(const void* C, const int32_t* row_of_slot, const float* weights,
+                              const void* residual, void* out, int64_t rows, int64_t in_rows,
+                              int top_k, int N, cudaStream_t stream);
+
+/*
+ * Its gradient, d_out bf16 [rows, N] being that of out (and of the residual):
+ *   dC[row_of_slot[t, j]] = bf16( weights[t, j] * d_out[t] )
+ *   d_weights[t, j]       = sum_n d_out[t, n] * C[row_of_slot[t, j], n]      fp32
+ * d_weights is 0 for dropped slots; rows of dC that no slot names are left as they are.  dC may
+ * not overlap C or d_out.  The same result every time: each sum has one order.
+ */
+bsfp8_status bsmx_moe_combine_backward(const void* d_out, const void* C,
+                                       const int32_t* row_of_slot, const float* weights, void* dC,
+                                       float* d_weights, int64_t rows, int64_t in_rows, int top_k,
+                                       int N, cudaStream_t stream);
+
+/*
  * TMEM storage plan of double-buffered block-scaled accumulators (host only, no GPU use).
  * For a 256-column tile with 512 TMEM columns, block_k elements of K per MMA stage,
  * epilogue subtiles of epilogue_n columns and one scale per vec (16 or 32) elements of K,
@@ -323,8 +443,8 @@ bsfp8_status bsmx_plan(int64_t M_total, int num_groups, int32_t* out);
 
 /*
  * Read the device error word of the current device (after synchronising `stream`) into
- * *code (0, BSFP8_ERR_DEVICE_OFFSETS, BSFP8_ERR_DEVICE_TIMEOUT, BSFP8_ERR_DEVICE_EXPERT_IDS, or
- * in a debug build BSFP8_ERR_DEVICE_BOUNDS)
+ * *code (0, BSFP8_ERR_DEVICE_OFFSETS, BSFP8_ERR_DEVICE_TIMEOUT, BSFP8_ERR_DEVICE_EXPERT_IDS,
+ * BSFP8_ERR_DEVICE_ROWS, or in a debug build BSFP8_ERR_DEVICE_BOUNDS)
  * and reset it to 0.
  * The word is one per device, not per stream: every kernel of this library on the device
  * records its first error there, whatever stream it runs on.  Only `stream` is synchronised,
