@@ -134,8 +134,7 @@ def _addr(x) -> int | None:
 
 def _stream(stream) -> int | None:
     if stream is None:
-        import torch
-        return torch.cuda.current_stream().cuda_stream or None
+        return (_binding or load_binding()).current_stream() or None
     if isinstance(stream, int):
         return stream or None
     return stream.cuda_stream or None
@@ -224,54 +223,35 @@ def bsmxfp8_grouped_gemm_prepacked(A, B, a_scales, b_scales_packed, expert_offse
 # ---------------------------------------------------------------------------------------
 # the operators around the grouped GEMM
 # ---------------------------------------------------------------------------------------
-def _buf(x, count: int, sizes: tuple, name: str) -> int | None:
-    """Address of a buffer that must hold at least `count` elements of one of `sizes` bytes; a
-    raw address or None passes unchecked."""
-    if x is None:
-        return None
-    if isinstance(x, int):
-        return x or None
-    if not x.is_cuda:
-        raise ValueError(f"{name} must be a CUDA tensor (device memory)")
-    if not x.is_contiguous():
-        raise ValueError(f"{name} must be contiguous (row-major)")
-    if x.itemsize not in sizes:
-        raise ValueError(f"{name} has elements of {x.itemsize} bytes, wanted {sizes}")
-    if x.numel() < count:
-        raise ValueError(f"{name} holds {x.numel()} elements, needs {count}")
-    return x.data_ptr() or None
+_OPERATORS = ("bsmx_quantize", "bsmx_rmsnorm_quant", "bsmx_swiglu_quant", "bsmx_moe_sort",
+              "bsmx_moe_combine", "bsmx_moe_combine_backward")
+_binding = None
 
 
-_TYPE_OF = {"torch.bfloat16": 0, "torch.float16": 1, "torch.float32": 2}
+def load_binding():
+    """The compiled binding (csrc/binding.cpp), bound to the library's entry points (raises if
+    either has not been built)."""
+    global _binding
+    if _binding is None:
+        import importlib.machinery
+        import importlib.util
 
+        import torch  # noqa: F401  (its libraries, which the binding is linked with)
 
-def _type_code(x, given: str | None, allowed: tuple, name: str) -> int:
-    """bsmx_type of a tensor, or of a raw address by the name given for it."""
-    if given is not None:
-        code = TYPES[given]
-    elif isinstance(x, int):
-        raise ValueError(f"{name} is a raw address: its type has to be given")
-    else:
-        code = _TYPE_OF.get(str(x.dtype), -1)
-    if code not in allowed:
-        raise ValueError(f"{name} has an unsupported type")
-    return code
-
-
-def _bf16(x, count: int, name: str) -> int | None:
-    if x is not None and not isinstance(x, int) and str(x.dtype) != "torch.bfloat16":
-        raise ValueError(f"{name} must be bf16")
-    return _buf(x, count, (2,), name)
-
-
-def _operand(format: str, q, scales, rows: int, K: int):
-    """(address of q, address of scales) of an operand of rows x K in `format`."""
-    if format == "blockwise":
-        return _buf(q, rows * K, (1,), "q"), _buf(scales, rows * (K // 128), (4,), "scales")
-    if format == "mxfp8":
-        return _buf(q, rows * K, (1,), "q"), _buf(scales, rows * (K // 32), (1,), "scales")
-    vec = 16 if format == "nvfp4" else 32
-    return _buf(q, rows * (K // 2), (1,), "q"), _buf(scales, rows * (K // vec), (1,), "scales")
+        from . import build
+        path = build.binding_path()
+        if not os.path.exists(path):
+            raise ImportError(f"{path} is missing: build it with "
+                              "`python -m block_scaled_fp8_persistent_gb300.build`")
+        loader = importlib.machinery.ExtensionFileLoader("bsfp8_binding", path)
+        spec = importlib.util.spec_from_file_location("bsfp8_binding", path, loader=loader)
+        module = importlib.util.module_from_spec(spec)
+        loader.exec_module(module)
+        lib = load_library()
+        module.bind(*(ctypes.cast(getattr(lib, name), ctypes.c_void_p).value
+                      for name in _OPERATORS))
+        _binding = module
+    return _binding
 
 
 def bsmx_quantize(format: str, x, q, scales, rows: int, K: int, row_of_slot=None, top_k: int = 1,
@@ -279,13 +259,10 @@ def bsmx_quantize(format: str, x, q, scales, rows: int, K: int, row_of_slot=None
     """Quantise x [rows, K] (bf16, fp16 or fp32) into the operand (q, scales) of `format`
     ("mxfp8", "mxfp4", "nvfp4", "blockwise"); with row_of_slot, row t goes to each of the rows
     row_of_slot[t, :] of an operand of out_rows rows.  See include/bsfp8.h.  Raises BsFp8Error."""
-    out_rows = rows if out_rows is None else out_rows
-    qa, sa = _operand(format, q, scales, out_rows, K)
-    st = load_library().bsmx_quantize(
-        QUANT_FORMATS[format], _type_code(x, x_type, (0, 1, 2), "x"),
-        _buf(x, rows * K, (2, 4), "x"), _buf(row_of_slot, rows * top_k, (4,), "row_of_slot"),
-        top_k, qa, sa, rows, out_rows, K, _stream(stream))
-    if st != BSFP8_OK:
+    st = (_binding or load_binding()).quantize(
+        QUANT_FORMATS[format], -1 if x_type is None else TYPES[x_type], x, row_of_slot, top_k, q,
+        scales, rows, rows if out_rows is None else out_rows, K, stream)
+    if st:
         raise BsFp8Error(st, "bsmx_quantize")
 
 
@@ -295,31 +272,19 @@ def bsmx_rmsnorm_quant(format: str, x, weight, eps: float, rows: int, K: int, re
     """h = x + residual, y = h / sqrt(mean(h^2) + eps) * weight; writes h to residual_out, y in
     bf16 to y and y quantised in `format` to (q, scales), each where it is given.  See
     include/bsfp8.h.  Raises BsFp8Error."""
-    rt = 0
-    if residual is not None or residual_out is not None:
-        rt = _type_code(residual if residual is not None else residual_out, residual_type, (0, 2),
-                        "residual")
-        if residual is not None and residual_out is not None and residual_type is None \
-                and rt != _type_code(residual_out, None, (0, 2), "residual_out"):
-            raise ValueError("residual and residual_out differ in type")
-    size = (4,) if rt == 2 else (2,)
-    qa, sa = _operand(format, q, scales, rows, K) if q is not None else (None, None)
-    st = load_library().bsmx_rmsnorm_quant(
-        QUANT_FORMATS[format], rt, _bf16(x, rows * K, "x"),
-        _buf(residual, rows * K, size, "residual"), _bf16(weight, K, "weight"), eps,
-        _buf(residual_out, rows * K, size, "residual_out"), _bf16(y, rows * K, "y"), qa, sa,
-        rows, K, _stream(stream))
-    if st != BSFP8_OK:
+    st = (_binding or load_binding()).rmsnorm_quant(
+        QUANT_FORMATS[format], -1 if residual_type is None else TYPES[residual_type], x, residual,
+        weight, eps, residual_out, y, q, scales, rows, K, stream)
+    if st:
         raise BsFp8Error(st, "bsmx_rmsnorm_quant")
 
 
 def bsmx_swiglu_quant(format: str, h, q, scales, rows: int, N: int, stream=None) -> None:
     """silu(h[:, :N]) * h[:, N:] of bf16 h [rows, 2N], quantised in `format` into (q, scales).
     See include/bsfp8.h.  Raises BsFp8Error."""
-    qa, sa = _operand(format, q, scales, rows, N)
-    st = load_library().bsmx_swiglu_quant(QUANT_FORMATS[format], _bf16(h, rows * 2 * N, "h"), qa,
-                                          sa, rows, N, _stream(stream))
-    if st != BSFP8_OK:
+    st = (_binding or load_binding()).swiglu_quant(QUANT_FORMATS[format], h, q, scales, rows, N,
+                                                   stream)
+    if st:
         raise BsFp8Error(st, "bsmx_swiglu_quant")
 
 
@@ -338,17 +303,10 @@ def bsmx_moe_sort(topk_ids, offsets, row_of_slot, workspace, rows: int, top_k: i
     """Sort the slots of int32 topk_ids [rows, top_k] by expert: int32 offsets [num_experts + 2],
     row_of_slot [rows, top_k] (-1: dropped) and slot_of_row.  See include/bsfp8.h.  Raises
     BsFp8Error."""
-    slots = rows * top_k
-    if workspace_bytes is None:
-        if isinstance(workspace, int):
-            raise ValueError("workspace is a raw address: workspace_bytes has to be given")
-        workspace_bytes = 0 if workspace is None else workspace.numel() * workspace.itemsize
-    st = load_library().bsmx_moe_sort(
-        _buf(topk_ids, slots, (4,), "topk_ids"), _buf(offsets, num_experts + 2, (4,), "offsets"),
-        _buf(row_of_slot, slots, (4,), "row_of_slot"),
-        _buf(slot_of_row, slots, (4,), "slot_of_row"), _addr(workspace), workspace_bytes, rows,
-        top_k, num_experts, _stream(stream))
-    if st != BSFP8_OK:
+    st = (_binding or load_binding()).moe_sort(
+        topk_ids, offsets, row_of_slot, slot_of_row, workspace,
+        -1 if workspace_bytes is None else workspace_bytes, rows, top_k, num_experts, stream)
+    if st:
         raise BsFp8Error(st, "bsmx_moe_sort")
 
 
@@ -356,11 +314,9 @@ def bsmx_moe_combine(C, row_of_slot, out, rows: int, in_rows: int, top_k: int, N
                      weights=None, residual=None, stream=None) -> None:
     """out[t] = residual[t] + sum_j weights[t, j] * C[row_of_slot[t, j]] over the slots that were
     not dropped.  See include/bsfp8.h.  Raises BsFp8Error."""
-    st = load_library().bsmx_moe_combine(
-        _bf16(C, in_rows * N, "C"), _buf(row_of_slot, rows * top_k, (4,), "row_of_slot"),
-        _buf(weights, rows * top_k, (4,), "weights"), _bf16(residual, rows * N, "residual"),
-        _bf16(out, rows * N, "out"), rows, in_rows, top_k, N, _stream(stream))
-    if st != BSFP8_OK:
+    st = (_binding or load_binding()).moe_combine(C, row_of_slot, weights, residual, out, rows,
+                                                  in_rows, top_k, N, stream)
+    if st:
         raise BsFp8Error(st, "bsmx_moe_combine")
 
 
@@ -369,13 +325,9 @@ def bsmx_moe_combine_backward(d_out, C, row_of_slot, weights, dC, d_weights, row
     """Gradient of bsmx_moe_combine: dC[row_of_slot[t, j]] = weights[t, j] * d_out[t] and
     d_weights[t, j] = <d_out[t], C[row_of_slot[t, j]]>.  See include/bsfp8.h.  Raises
     BsFp8Error."""
-    st = load_library().bsmx_moe_combine_backward(
-        _bf16(d_out, rows * N, "d_out"), _bf16(C, in_rows * N, "C"),
-        _buf(row_of_slot, rows * top_k, (4,), "row_of_slot"),
-        _buf(weights, rows * top_k, (4,), "weights"), _bf16(dC, in_rows * N, "dC"),
-        _buf(d_weights, rows * top_k, (4,), "d_weights"), rows, in_rows, top_k, N,
-        _stream(stream))
-    if st != BSFP8_OK:
+    st = (_binding or load_binding()).moe_combine_backward(
+        d_out, C, row_of_slot, weights, dC, d_weights, rows, in_rows, top_k, N, stream)
+    if st:
         raise BsFp8Error(st, "bsmx_moe_combine_backward")
 
 

@@ -7,12 +7,16 @@ the CUDA runtime linked statically (the driver itself is found at run time).
 build(debug=True) makes lib/libbsfp8_debug.so instead: the same sources with
 -DBSFP8_DEBUG=1, whose kernels check every tile's coordinates against the problem and
 record BSFP8_ERR_DEVICE_BOUNDS in the device error word instead of going out of range.
+
+Both also make lib/bsfp8_binding_<torch version>.so (csrc/binding.cpp, host code only): the
+Python side of the operators around the GEMM, compiled against the torch that is installed.
 """
 from __future__ import annotations
 
 import os
 import subprocess
 import sys
+import sysconfig
 from concurrent.futures import ThreadPoolExecutor
 
 PKG = os.path.dirname(os.path.abspath(__file__))
@@ -41,6 +45,36 @@ def _deps() -> list[str]:
     return out
 
 
+def binding_path() -> str:
+    """The compiled binding of the torch that is installed."""
+    from importlib.metadata import version
+    v = "".join(c if c.isalnum() else "_" for c in version("torch"))
+    return os.path.join(LIBDIR, f"bsfp8_binding_{v}.so")
+
+
+def build_binding(force: bool = False) -> str:
+    out = binding_path()
+    if not force and up_to_date(out):
+        return out
+    from importlib.util import find_spec
+    torch = os.path.dirname(find_spec("torch").origin)
+    lib = os.path.join(torch, "lib")
+    os.makedirs(LIBDIR, exist_ok=True)
+    tmp = out + f".tmp{os.getpid()}"
+    cuda = os.path.join(os.environ.get("CUDA_HOME", "/usr/local/cuda"), "include")
+    cmd = ["g++", "-O2", "-std=c++17", "-fPIC", "-shared", "-I" + INCLUDE, "-isystem", cuda,
+           "-isystem", os.path.join(torch, "include"),
+           "-isystem", os.path.join(torch, "include", "torch", "csrc", "api", "include"),
+           "-isystem", sysconfig.get_paths()["include"], os.path.join(CSRC, "binding.cpp"),
+           "-o", tmp, "-L" + lib, "-Wl,-rpath," + lib, "-lc10", "-lc10_cuda", "-ltorch_cpu",
+           "-ltorch_python"]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"g++ failed for binding.cpp:\n{r.stdout}\n{r.stderr}")
+    os.replace(tmp, out)
+    return out
+
+
 def up_to_date(lib: str = LIB) -> bool:
     if not os.path.exists(lib):
         return False
@@ -53,6 +87,7 @@ def build(force: bool = False, verbose: bool = False, ptxas_info: bool = False,
     lib = DEBUG_LIB if debug else LIB
     objdir = OBJDIR + ("_debug" if debug else "")
     if not force and up_to_date(lib):
+        build_binding()
         return lib
     os.makedirs(objdir, exist_ok=True)
     os.makedirs(LIBDIR, exist_ok=True)
@@ -71,8 +106,10 @@ def build(force: bool = False, verbose: bool = False, ptxas_info: bool = False,
             sys.stderr.write(r.stdout + r.stderr)
         return obj
 
-    with ThreadPoolExecutor(max_workers=len(SOURCES)) as ex:
+    with ThreadPoolExecutor(max_workers=len(SOURCES) + 1) as ex:
+        binding = ex.submit(build_binding, force)
         objs = list(ex.map(compile_one, SOURCES))
+        binding.result()
     tmp = lib + f".tmp{os.getpid()}"
     cmd = [nvcc, *ARCH, "-shared", "-o", tmp, *objs]
     r = subprocess.run(cmd, capture_output=True, text=True)
