@@ -16,12 +16,13 @@ bool format_ok(int format) { return format >= BSMX_MXFP8 && format <= BSMX_BLOCK
 
 bool rows_ok(int64_t rows) { return rows >= 0 && rows <= INT32_MAX; }
 
-bool width_ok(int K) { return K >= 128 && K % 128 == 0; }
+// widths up to 2^24, so that a row's blocks fit the grid
+constexpr int kMaxWidth = 1 << 24;
+bool width_ok(int K) { return K >= 128 && K % 128 == 0 && K <= kMaxWidth; }
 
 constexpr int kMaxTopK = 64;
 
-// columns of a combine: up to 2^24, so that its grid fits
-bool columns_ok(int N) { return N >= 8 && N % 8 == 0 && N <= (1 << 24); }
+bool columns_ok(int N) { return N >= 8 && N % 8 == 0 && N <= kMaxWidth; }
 
 bool slots_ok(int64_t rows, int top_k) {
   return rows_ok(rows) && top_k >= 1 && top_k <= kMaxTopK && rows * top_k <= INT32_MAX;
@@ -84,7 +85,7 @@ extern "C" bsfp8_status bsmx_swiglu_quant(int format, const void* h, void* q, vo
                                           int64_t rows, int N, cudaStream_t stream) {
   if (!format_ok(format)) return BSFP8_ERR_FORMAT;
   if (rows > 0 && (!h || !q || !scales)) return BSFP8_ERR_NULL;
-  if (!width_ok(N) || N > INT32_MAX / 2 || !rows_ok(rows)) return BSFP8_ERR_SHAPE;
+  if (!width_ok(N) || !rows_ok(rows)) return BSFP8_ERR_SHAPE;
   if (!aligned(h, 16) || !operand_aligned(format, q, scales)) return BSFP8_ERR_ALIGN;
   int* err = nullptr;
   const bsfp8_status st = static_cast<bsfp8_status>(device_error_word(&err));

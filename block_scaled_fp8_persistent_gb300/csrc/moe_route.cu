@@ -17,7 +17,10 @@ namespace {
 //   (slots of smaller keys) + (slots of its key in earlier chunks) + (in earlier warps)
 //   + (earlier in its warp),
 // the key being the expert, or `experts` for dropped slots.  Counts only, no atomics whose
-// order could show: equal keys keep their order.
+// order could show: equal keys keep their order.  Bound by launches and round trips to L2, not
+// by bytes (12 per slot): one launch up to kSortSingle slots (128 slots of 64 experts 2.2 us,
+// 4096 slots 6.5 us), above that two, the second started before the first ends (8192 to 65536
+// slots 6.0 to 6.2 us, 524288 slots 9.4 us; one block alone takes 55 us for 65536).
 // ---------------------------------------------------------------------------------------
 constexpr int kSortThreads = 1024;
 constexpr int kSortMaxChunks = 128;
@@ -30,21 +33,35 @@ int64_t sort_chunk(int64_t slots) {
   return (c + kSortChunk - 1) / kSortChunk * kSortChunk;
 }
 
+// Words from one warp's counts to the next: odd, so that the 32 warps' counts of one key lie
+// in 32 banks.
+__host__ __device__ __forceinline__ int sort_pitch(int experts) { return (experts + 1) | 1; }
+
 int sort_warps(int64_t chunk, int experts) {
   int w = kSortThreads / 32;
-  while (w > 1 && w * (experts + 1) > kSortSmemWords) w /= 2;
+  while (w > 1 && w * sort_pitch(experts) > kSortSmemWords) w /= 2;
   while (w > 1 && (w / 2) * 32 >= chunk) w /= 2;
   return w;
+}
+
+// Programmatic launches: lets the next kernel of the stream start, and waits until the one
+// before it has completed (at once where it was not launched early).
+__device__ __forceinline__ void launch_dependents() {
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+}
+__device__ __forceinline__ void wait_for_previous() {
+  asm volatile("griddepcontrol.wait;" ::: "memory");
 }
 
 __device__ __forceinline__ int key_of(int id, int experts) {
   return (unsigned)id < (unsigned)experts ? id : experts;
 }
 
-// Counts per key of one chunk: counts[chunk * keys + key].
+// Counts per key of one chunk: counts[key * chunks + chunk].
 __global__ void __launch_bounds__(kSortThreads) sort_count_kernel(SortArgs a, int64_t chunk) {
   extern __shared__ int hist[];
   const int keys = a.experts + 1;
+  launch_dependents();
   for (int e = threadIdx.x; e < keys; e += blockDim.x) hist[e] = 0;
   __syncthreads();
   const int64_t begin = blockIdx.x * chunk;
@@ -53,7 +70,7 @@ __global__ void __launch_bounds__(kSortThreads) sort_count_kernel(SortArgs a, in
     atomicAdd(&hist[key_of(__ldg(a.ids + s), a.experts)], 1);
   __syncthreads();
   for (int e = threadIdx.x; e < keys; e += blockDim.x)
-    a.workspace[(int64_t)blockIdx.x * keys + e] = hist[e];
+    a.workspace[(int64_t)e * gridDim.x + blockIdx.x] = hist[e];
 }
 
 // Exclusive prefix sum of one value per thread over the block, and the block's total.
@@ -80,13 +97,16 @@ __device__ __forceinline__ int block_exclusive(int v, int* warp_sums, int& total
   return before + inc - v;
 }
 
-// Rows of one chunk's slots.  With one block the counts come from its own histograms,
-// otherwise from the counts of every chunk.
+// Rows of one chunk's slots.  With one block the counts come from its own histograms, added up
+// by one thread per key (1024 slots: 4.0 us, one warp per key 4.9); otherwise from the counts of
+// every chunk (at most kSortMaxChunks), which one warp per key reads and adds up side by side.
 __global__ void __launch_bounds__(kSortThreads) sort_place_kernel(SortArgs a, int64_t chunk,
                                                                   int warps) {
-  extern __shared__ int hist[];  // [warps][keys]
+  extern __shared__ int hist[];  // [warps][pitch], then [keys] first rows and [keys] totals
   __shared__ int warp_sums[32];
-  const int keys = a.experts + 1;
+  const int keys = a.experts + 1, pitch = sort_pitch(a.experts);
+  int* const base = hist + warps * pitch;
+  int* const totals = base + keys;
   const int lane = threadIdx.x % 32, warp = threadIdx.x / 32;
   const int64_t begin = blockIdx.x * chunk;
   const int64_t end = begin + chunk < a.slots ? begin + chunk : a.slots;
@@ -94,38 +114,71 @@ __global__ void __launch_bounds__(kSortThreads) sort_place_kernel(SortArgs a, in
   const int64_t lo = begin + warp * seg;
   const int64_t hi = warp < warps ? (lo + seg < end ? lo + seg : end) : lo;
 
-  for (int e = threadIdx.x; e < warps * keys; e += blockDim.x) hist[e] = 0;
+  for (int e = threadIdx.x; e < warps * pitch; e += blockDim.x) hist[e] = 0;
   __syncthreads();
   for (int64_t s = lo + lane; s < hi; s += 32)
-    atomicAdd(&hist[warp * keys + key_of(__ldg(a.ids + s), a.experts)], 1);
+    atomicAdd(&hist[warp * pitch + key_of(__ldg(a.ids + s), a.experts)], 1);
+  __syncthreads();
+  wait_for_previous();  // the chunks' counts; nothing is written before
+
+  const int chunks = gridDim.x;
+  constexpr int kKeys = 4;  // keys whose counts a warp has in flight
+  for (int e = threadIdx.x; chunks == 1 && e < keys; e += blockDim.x) {
+    int all = 0;
+    for (int w = 0; w < warps; ++w) {
+      const int c = hist[w * pitch + e];
+      hist[w * pitch + e] = all;
+      all += c;
+    }
+    totals[e] = all;
+    base[e] = 0;
+  }
+  for (int e0 = warp; chunks > 1 && e0 < keys; e0 += kKeys * (blockDim.x / 32)) {
+    int c[kKeys][kSortMaxChunks / 32] = {};
+#pragma unroll
+    for (int n = 0; n < kKeys; ++n) {
+      const int e = e0 + n * (blockDim.x / 32);
+#pragma unroll
+      for (int i = 0; i < kSortMaxChunks / 32; ++i)
+        if (e < keys && i * 32 + lane < chunks)
+          c[n][i] = a.workspace[(int64_t)e * chunks + i * 32 + lane];
+    }
+#pragma unroll
+    for (int n = 0; n < kKeys; ++n) {
+      const int e = e0 + n * (blockDim.x / 32);
+      if (e >= keys) break;
+      const int mine = lane < warps ? hist[lane * pitch + e] : 0;
+      int inc = mine;
+#pragma unroll
+      for (int d = 1; d < 32; d *= 2) {
+        const int o = __shfl_up_sync(0xffffffffu, inc, d);
+        if (lane >= d) inc += o;
+      }
+      if (lane < warps) hist[lane * pitch + e] = inc - mine;
+      int all = 0, before = 0;
+#pragma unroll
+      for (int i = 0; i < kSortMaxChunks / 32; ++i) {
+        all += c[n][i];
+        before += i * 32 + lane < (int)blockIdx.x ? c[n][i] : 0;
+      }
+      all = __reduce_add_sync(0xffffffffu, all);
+      before = __reduce_add_sync(0xffffffffu, before);
+      if (lane == 0) {
+        totals[e] = all;
+        base[e] = before;
+      }
+    }
+  }
   __syncthreads();
 
   int carry = 0;
   for (int e0 = 0; e0 < keys; e0 += blockDim.x) {
     const int e = e0 + threadIdx.x;
-    int mine = 0, before = 0, all = 0;
-    if (e < keys) {
-      for (int w = 0; w < warps; ++w) {
-        const int c = hist[w * keys + e];
-        hist[w * keys + e] = mine;
-        mine += c;
-      }
-      all = mine;
-      if (gridDim.x > 1) {
-        all = 0;
-#pragma unroll 16
-        for (int b = 0; b < (int)gridDim.x; ++b) {
-          const int c = __ldg(a.workspace + (int64_t)b * keys + e);
-          all += c;
-          if (b < (int)blockIdx.x) before += c;
-        }
-      }
-    }
     int total;
-    const int first = carry + block_exclusive(all, warp_sums, total);
+    const int first = carry + block_exclusive(e < keys ? totals[e] : 0, warp_sums, total);
     carry += total;
     if (e < keys) {
-      for (int w = 0; w < warps; ++w) hist[w * keys + e] += first + before;
+      base[e] += first;
       if (blockIdx.x == 0) a.offsets[e] = first;
     }
   }
@@ -140,11 +193,12 @@ __global__ void __launch_bounds__(kSortThreads) sort_place_kernel(SortArgs a, in
       const int key = key_of(__ldg(a.ids + s), a.experts);
       const unsigned peers = __match_any_sync(active, key);
       const int rank = __popc(peers & ((1u << lane) - 1));
-      int* h = &hist[warp * keys + key];
-      const int row = *h + rank;
+      int* h = &hist[warp * pitch + key];
+      const int place = *h + rank;
       __syncwarp(active);
-      if (rank == 0) *h = row + __popc(peers);
+      if (rank == 0) *h = place + __popc(peers);
       __syncwarp(active);
+      const int row = base[key] + place;
       a.row_of_slot[s] = key < a.experts ? row : -1;
       if (a.slot_of_row) a.slot_of_row[row] = key < a.experts ? (int)s : -1;
     }
@@ -154,8 +208,16 @@ __global__ void __launch_bounds__(kSortThreads) sort_place_kernel(SortArgs a, in
 
 // ---------------------------------------------------------------------------------------
 // weighted sum of a token's rows, and its gradient
+//
+// Bound by HBM: every named row of C is read once.  A thread takes 8 columns of a token (16-byte
+// accesses, a warp's are 512 bytes of a row) and has the rows of up to 8 slots in flight, as
+// many as top_k needs: fewer registers, more threads (top_k 2, 512 columns: 10.3 -> 7.3 us, its
+// gradient 6.2 -> 4.5).  The sum runs in small blocks, 64 threads (8192 tokens x 8 rows of 7168
+// columns 147 us, 6.6 TB/s; 128 threads 154, 256 threads 172: the last block of a row idles half
+// its threads and its rows arrive in larger lumps).  The gradient needs a token's whole row for
+// its dot products: one block of 256 threads per token (4096 tokens x 8 rows of 7168 columns
+// 148 us, 6.7 TB/s; 64 threads 153), and no partial sums to be joined in memory.
 // ---------------------------------------------------------------------------------------
-constexpr int kSlots = 8;  // rows in flight per thread
 
 __device__ __forceinline__ int checked_row(const int32_t* row_of_slot, int64_t slot,
                                            int64_t in_rows, int* err) {
@@ -172,30 +234,32 @@ __device__ __forceinline__ void unpack8(const uint32_t (&w)[4], float (&v)[8]) {
   for (int i = 0; i < 4; ++i) unpack_bf16x2(w[i], v[2 * i], v[2 * i + 1]);
 }
 
-__global__ void __launch_bounds__(256) combine_kernel(CombineArgs a) {
+// SLOTS rows of a token in flight per thread.
+template <int SLOTS>
+__global__ void __launch_bounds__(64) combine_kernel(CombineArgs a) {
   const int64_t t = blockIdx.x;
   const int col = (blockIdx.y * blockDim.x + threadIdx.x) * 8;
   if (col >= a.N) return;
   float acc[8] = {};
   if (a.residual) {
     uint32_t w[4];
-    load_stream<4, false>(static_cast<const uint16_t*>(a.residual) + t * a.N + col, w);
+    load_words(static_cast<const uint16_t*>(a.residual) + t * a.N + col, w);
     unpack8(w, acc);
   }
-  for (int j0 = 0; j0 < a.top_k; j0 += kSlots) {
-    uint32_t w[kSlots][4];
-    int row[kSlots];
+  for (int j0 = 0; j0 < a.top_k; j0 += SLOTS) {
+    uint32_t w[SLOTS][4];
+    int row[SLOTS];
 #pragma unroll
-    for (int j = 0; j < kSlots; ++j)
+    for (int j = 0; j < SLOTS; ++j)
       row[j] = j0 + j < a.top_k
                    ? checked_row(a.row_of_slot, t * a.top_k + j0 + j, a.in_rows, a.err)
                    : -1;
 #pragma unroll
-    for (int j = 0; j < kSlots; ++j)
+    for (int j = 0; j < SLOTS; ++j)
       if (row[j] >= 0)
-        load_stream<4, false>(static_cast<const uint16_t*>(a.C) + (int64_t)row[j] * a.N + col, w[j]);
+        load_words(static_cast<const uint16_t*>(a.C) + (int64_t)row[j] * a.N + col, w[j]);
 #pragma unroll
-    for (int j = 0; j < kSlots; ++j) {
+    for (int j = 0; j < SLOTS; ++j) {
       if (row[j] >= 0) {
         const float g = a.weights ? __ldg(a.weights + t * a.top_k + j0 + j) : 1.0f;
         float v[8];
@@ -210,30 +274,31 @@ __global__ void __launch_bounds__(256) combine_kernel(CombineArgs a) {
                pack_bf16x2(acc[6], acc[7]));
 }
 
+template <int SLOTS>
 __global__ void __launch_bounds__(256) combine_backward_kernel(CombineBackwardArgs a) {
-  __shared__ float part[8][kSlots];
+  __shared__ float part[8][SLOTS];
   const int64_t t = blockIdx.x;
   const int lane = threadIdx.x % 32, warp = threadIdx.x / 32;
-  for (int j0 = 0; j0 < a.top_k; j0 += kSlots) {
-    int row[kSlots];
-    float g[kSlots], dot[kSlots] = {};
+  for (int j0 = 0; j0 < a.top_k; j0 += SLOTS) {
+    int row[SLOTS];
+    float g[SLOTS], dot[SLOTS] = {};
 #pragma unroll
-    for (int j = 0; j < kSlots; ++j) {
+    for (int j = 0; j < SLOTS; ++j) {
       const bool there = j0 + j < a.top_k;
       row[j] = there ? checked_row(a.row_of_slot, t * a.top_k + j0 + j, a.in_rows, a.err) : -1;
       g[j] = there ? __ldg(a.weights + t * a.top_k + j0 + j) : 0.0f;
     }
     for (int col = threadIdx.x * 8; col < a.N; col += blockDim.x * 8) {
-      uint32_t wd[4], w[kSlots][4];
+      uint32_t wd[4], w[SLOTS][4];
       float d[8];
-      load_stream<4, false>(static_cast<const uint16_t*>(a.d_out) + t * a.N + col, wd);
+      load_words(static_cast<const uint16_t*>(a.d_out) + t * a.N + col, wd);
 #pragma unroll
-      for (int j = 0; j < kSlots; ++j)
+      for (int j = 0; j < SLOTS; ++j)
         if (row[j] >= 0)
-          load_stream<4, false>(static_cast<const uint16_t*>(a.C) + (int64_t)row[j] * a.N + col, w[j]);
+          load_words(static_cast<const uint16_t*>(a.C) + (int64_t)row[j] * a.N + col, w[j]);
       unpack8(wd, d);
 #pragma unroll
-      for (int j = 0; j < kSlots; ++j) {
+      for (int j = 0; j < SLOTS; ++j) {
         if (row[j] < 0) continue;
         float v[8];
         unpack8(w[j], v);
@@ -245,13 +310,13 @@ __global__ void __launch_bounds__(256) combine_backward_kernel(CombineBackwardAr
       }
     }
 #pragma unroll
-    for (int j = 0; j < kSlots; ++j) {
+    for (int j = 0; j < SLOTS; ++j) {
 #pragma unroll
       for (int o = 16; o > 0; o /= 2) dot[j] += __shfl_xor_sync(0xffffffffu, dot[j], o);
       if (lane == 0) part[warp][j] = dot[j];
     }
     __syncthreads();
-    if (threadIdx.x < kSlots && j0 + (int)threadIdx.x < a.top_k) {
+    if (threadIdx.x < SLOTS && j0 + (int)threadIdx.x < a.top_k) {
       float s = 0.0f;
       for (int w = 0; w < (int)blockDim.x / 32; ++w) s += part[w][threadIdx.x];
       a.d_weights[t * a.top_k + j0 + threadIdx.x] = s;
@@ -278,33 +343,58 @@ cudaError_t launch_moe_sort(const SortArgs& a, cudaStream_t stream) {
   int threads = (keys + 31) / 32 * 32;
   threads = threads < warps * 32 ? warps * 32 : threads;
   threads = threads < kSortThreads ? threads : kSortThreads;
-  const size_t smem = (size_t)warps * keys * sizeof(int);
+  const size_t smem = ((size_t)warps * sort_pitch(a.experts) + 2 * keys) * sizeof(int);
   if (smem > 48 * 1024) {
     const cudaError_t e = cudaFuncSetAttribute(
-        sort_place_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSortSmemWords * 4);
+        sort_place_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
     if (e != cudaSuccess) return e;
   }
-  if (!single) {
-    sort_count_kernel<<<chunks, kSortThreads, keys * sizeof(int), stream>>>(a, chunk);
-    const cudaError_t e = cudaGetLastError();
-    if (e != cudaSuccess) return e;
+  if (single) {
+    sort_place_kernel<<<1, threads, smem, stream>>>(a, chunk, warps);
+    return cudaGetLastError();
   }
-  sort_place_kernel<<<chunks, threads, smem, stream>>>(a, chunk, warps);
-  return cudaGetLastError();
+  sort_count_kernel<<<chunks, kSortThreads, keys * sizeof(int), stream>>>(a, chunk);
+  const cudaError_t e = cudaGetLastError();
+  if (e != cudaSuccess) return e;
+  // started while the counts are still being made: it clears and fills its own histograms
+  // before it waits for them
+  cudaLaunchConfig_t config = {};
+  config.gridDim = dim3(chunks);
+  config.blockDim = dim3(threads);
+  config.dynamicSmemBytes = smem;
+  config.stream = stream;
+  cudaLaunchAttribute early = {};
+  early.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  early.val.programmaticStreamSerializationAllowed = 1;
+  config.attrs = &early;
+  config.numAttrs = 1;
+  return cudaLaunchKernelEx(&config, sort_place_kernel, a, chunk, warps);
 }
 
 cudaError_t launch_moe_combine(const CombineArgs& a, cudaStream_t stream) {
   const int vecs = a.N / 8;
-  const int threads = vecs >= 256 ? 256 : (vecs + 31) / 32 * 32;
+  const int threads = vecs < 64 ? (vecs + 31) / 32 * 32 : 64;
   const dim3 grid((unsigned)a.rows, (unsigned)((vecs + threads - 1) / threads));
-  combine_kernel<<<grid, threads, 0, stream>>>(a);
+  if (a.top_k <= 1)
+    combine_kernel<1><<<grid, threads, 0, stream>>>(a);
+  else if (a.top_k <= 2)
+    combine_kernel<2><<<grid, threads, 0, stream>>>(a);
+  else if (a.top_k <= 4)
+    combine_kernel<4><<<grid, threads, 0, stream>>>(a);
+  else
+    combine_kernel<8><<<grid, threads, 0, stream>>>(a);
   return cudaGetLastError();
 }
 
 cudaError_t launch_moe_combine_backward(const CombineBackwardArgs& a, cudaStream_t stream) {
   const int vecs = a.N / 8;
   const int threads = vecs >= 256 ? 256 : (vecs + 31) / 32 * 32;
-  combine_backward_kernel<<<(unsigned)a.rows, threads, 0, stream>>>(a);
+  if (a.top_k <= 2)
+    combine_backward_kernel<2><<<(unsigned)a.rows, threads, 0, stream>>>(a);
+  else if (a.top_k <= 4)
+    combine_backward_kernel<4><<<(unsigned)a.rows, threads, 0, stream>>>(a);
+  else
+    combine_backward_kernel<8><<<(unsigned)a.rows, threads, 0, stream>>>(a);
   return cudaGetLastError();
 }
 

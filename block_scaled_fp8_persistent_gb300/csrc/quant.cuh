@@ -26,9 +26,24 @@ struct QuantTraits {
   static constexpr int words = fp4 ? 2 : 4;   // 32-bit words of codes per thread
 };
 
+// Two products at once.
+__device__ __forceinline__ void mul2(float a0, float a1, float b0, float b1, float& r0, float& r1) {
+  asm("{\n\t.reg .b64 a, b, r;\n\t"
+      "mov.b64 a, {%2, %3};\n\tmov.b64 b, {%4, %5};\n\t"
+      "mul.rn.f32x2 r, a, b;\n\tmov.b64 {%0, %1}, r;\n\t}"
+      : "=f"(r0), "=f"(r1)
+      : "f"(a0), "f"(a1), "f"(b0), "f"(b1));
+}
+
 __device__ __forceinline__ float max_nan(float a, float b) {
   float r;
   asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+  return r;
+}
+
+__device__ __forceinline__ float max3_nan(float a, float b, float c) {
+  float r;
+  asm("max.NaN.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
   return r;
 }
 
@@ -66,7 +81,8 @@ __device__ __forceinline__ Quantised<FMT> quantise16(const float (&v)[16]) {
   using T = QuantTraits<FMT>;
   float a = fabsf(v[0]);
 #pragma unroll
-  for (int i = 1; i < 16; ++i) a = max_nan(a, fabsf(v[i]));
+  for (int i = 1; i < 15; i += 2) a = max3_nan(a, fabsf(v[i]), fabsf(v[i + 1]));
+  a = max_nan(a, fabsf(v[15]));
 #pragma unroll
   for (int d = 1; d < T::group; d *= 2) a = max_nan(a, __shfl_xor_sync(0xffffffffu, a, d));
 
@@ -116,23 +132,27 @@ __device__ __forceinline__ Quantised<FMT> quantise16(const float (&v)[16]) {
   return out;
 }
 
-// Stores the thread's codes and, from the first thread of each block, the scale, for elements
-// 16 * item .. of row `row` of an operand with `rows` rows of K elements.
+// Stores the thread's codes of elements 16 * item .. of row `row` of an operand of K columns.
 template <int FMT>
-__device__ __forceinline__ void store_quantised(const Quantised<FMT>& o, uint8_t* q, void* scales,
-                                                int64_t row, int64_t rows, int item, int K) {
-  using T = QuantTraits<FMT>;
-  if constexpr (T::fp4)
+__device__ __forceinline__ void store_codes(const Quantised<FMT>& o, uint8_t* q, int64_t row,
+                                            int item, int K) {
+  if constexpr (QuantTraits<FMT>::fp4)
     *reinterpret_cast<uint2*>(q + row * (K / 2) + item * 8) = make_uint2(o.w[0], o.w[1]);
   else
     *reinterpret_cast<uint4*>(q + row * K + (int64_t)item * 16) =
         make_uint4(o.w[0], o.w[1], o.w[2], o.w[3]);
-  if (item % T::group == 0) {
-    if constexpr (FMT == Q_BLOCKWISE)
-      static_cast<uint32_t*>(scales)[(item / T::group) * rows + row] = o.scale;
-    else
-      static_cast<uint8_t*>(scales)[row * (K / T::vec) + item / T::group] = (uint8_t)o.scale;
-  }
+}
+
+// Stores the block's scale, from the first of its threads; the operand has `rows` rows.
+template <int FMT>
+__device__ __forceinline__ void store_scale(const Quantised<FMT>& o, void* scales, int64_t row,
+                                            int64_t rows, int item, int K) {
+  using T = QuantTraits<FMT>;
+  if (item % T::group != 0) return;
+  if constexpr (FMT == Q_BLOCKWISE)
+    static_cast<uint32_t*>(scales)[(item / T::group) * rows + row] = o.scale;
+  else
+    static_cast<uint8_t*>(scales)[row * (K / T::vec) + item / T::group] = (uint8_t)o.scale;
 }
 
 __device__ __forceinline__ void unpack_bf16x2(uint32_t w, float& lo, float& hi) {
@@ -140,11 +160,10 @@ __device__ __forceinline__ void unpack_bf16x2(uint32_t w, float& lo, float& hi) 
   hi = __uint_as_float(w & 0xffff0000u);
 }
 
-// WORDS 32-bit words from p, read once (not kept in L1): 32-byte loads where WIDE says that p
-// is 32-byte aligned, else 16-byte loads.  Not the read-only path: a caller may pass the
-// norm's residual as its output too.
-template <int WORDS, bool WIDE>
-__device__ __forceinline__ void load_stream(const void* p, uint32_t (&w)[WORDS]) {
+// WORDS 32-bit words from p, 16-byte aligned, or 32-byte aligned where WIDE.  Not the read-only
+// path: a caller may pass the norm's residual as its output too.
+template <int WORDS, bool WIDE = false>
+__device__ __forceinline__ void load_words(const void* p, uint32_t (&w)[WORDS]) {
   const char* c = static_cast<const char*>(p);
   if constexpr (WIDE) {
 #pragma unroll

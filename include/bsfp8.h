@@ -295,8 +295,8 @@ bsfp8_status bsmx_grouped_gemm(int a_format, int b_format, const void* A, const 
  * (BLOCKWISE multiplies by the scale's fp32 reciprocal, NVFP4 divides, MX is exact).  A block
  * of zeros has scale 1; a block that holds a NaN or an infinity has a NaN scale (UE8M0 0xFF,
  * e4m3 0x7F, fp32 NaN), so that what is computed of it is NaN.  q is 16-byte aligned; K and N
- * are multiples of 128; inputs are 16-byte aligned (32-byte aligned ones are read with 32-byte
- * loads).  BSFP8_ERR_FORMAT for a format or type that is not listed.
+ * are multiples of 128, at most 2^24; inputs are 16-byte aligned.  Outputs overlap inputs only
+ * where that is said.  BSFP8_ERR_FORMAT for a format or type that is not listed.
  */
 
 /*

@@ -73,7 +73,8 @@ def _no_error():
 # ------------------------------------------------------------------------------ quantise
 @pytest.mark.parametrize("fmt", FORMATS)
 @pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float16, torch.float32])
-@pytest.mark.parametrize("rows,K", [(1, 128), (3, 640), (37, 1152), (130, 7168), (2, 16512)])
+@pytest.mark.parametrize("rows,K", [(1, 128), (9, 128), (11, 256), (7, 384), (3, 640), (5, 1024), (37, 1152),
+                                    (130, 7168), (2, 16512)])
 def test_quantize(fmt, dtype, rows, K):
     x = _rand((rows, K), dtype, seed=K + rows, spread=1.0 if dtype == torch.float16 else 3.0)
     x[0, :32] = 0
@@ -137,7 +138,8 @@ def test_quantize_of_16_byte_aligned_rows(fmt):
 
 
 @pytest.mark.parametrize("fmt", FORMATS)
-@pytest.mark.parametrize("rows,top_k,E,K", [(1, 1, 1, 128), (1, 8, 8, 7168), (5, 3, 4, 640), (67, 8, 16, 1152), (40, 11, 32, 256)])
+@pytest.mark.parametrize("rows,top_k,E,K", [(1, 1, 1, 128), (1, 8, 8, 7168), (5, 3, 4, 640), (67, 8, 16, 1152), (40, 11, 32, 256),
+                                               (700, 2, 8, 1152), (513, 3, 8, 128), (520, 1, 4, 9216)])
 def test_quantize_by_row_map(fmt, rows, top_k, E, K):
     g = np.random.default_rng(rows * top_k)
     ids = g.integers(-1, E, size=(rows, top_k)).astype(np.int32)
@@ -191,7 +193,8 @@ def test_rows_out_of_range_are_recorded_and_skipped():
 # ---------------------------------------------------------------------------------- norm
 @pytest.mark.parametrize("fmt", FORMATS)
 @pytest.mark.parametrize("residual", [None, torch.bfloat16, torch.float32])
-@pytest.mark.parametrize("rows,K", [(1, 128), (7, 640), (33, 7168), (2, 16512), (1, 32768)])
+@pytest.mark.parametrize("rows,K", [(1, 128), (70, 128), (9, 256), (13, 512), (7, 640), (33, 7168), (3, 8320),
+                                    (2, 16512), (1, 32768)])
 def test_norm(fmt, residual, rows, K):
     x = _rand((rows, K), torch.bfloat16, seed=K, spread=2.0)
     w = (1 + 0.3 * torch.randn(K, generator=torch.Generator().manual_seed(5))).to(torch.bfloat16)
@@ -249,20 +252,33 @@ def test_norm_of_zero_and_non_finite_rows():
     assert torch.isfinite(y[[0, 3]]).all() and torch.all(sc[[0, 3]] < 255)
 
 
-def test_norm_of_16_byte_aligned_rows():
-    rows, K = 9, 640
-    x = _rand((rows * K + 8, 1), torch.bfloat16, seed=4, spread=0.0).reshape(-1).cuda()[8:].view(rows, K)
-    r = _rand((rows * K + 4, 1), torch.float32, seed=5, spread=0.0).reshape(-1).cuda()[4:].view(rows, K)
+@pytest.mark.parametrize("residual", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("K", [128, 640, 9216])
+def test_norm_of_16_byte_aligned_rows(residual, K):
+    rows = 9
+
+    def buffer(dtype, seed, skip):
+        flat = _rand((rows * K + 16, 1), dtype, seed=seed, spread=0.0).reshape(-1).cuda()
+        return flat[skip: skip + rows * K].view(rows, K)
+
+    step = 8 if residual == torch.bfloat16 else 4
     w = torch.ones(K, dtype=torch.bfloat16, device="cuda")
-    a, b = torch.empty_like(x), torch.empty_like(x)
-    bsfp8.bsmx_rmsnorm_quant("mxfp8", x, w, 1e-6, rows, K, residual=r, y=a)
-    bsfp8.bsmx_rmsnorm_quant("mxfp8", x.clone(), w, 1e-6, rows, K, residual=r.clone(), y=b)
-    assert torch.equal(a, b)
+    x, r = buffer(torch.bfloat16, 4, 0), buffer(residual, 5, 0)
+    want = torch.empty_like(x), torch.empty_like(r)
+    bsfp8.bsmx_rmsnorm_quant("mxfp8", x, w, 1e-6, rows, K, residual=r, y=want[0], residual_out=want[1])
+    for odd in range(4):  # each buffer in turn off a 32-byte boundary
+        bufs = [buffer(torch.bfloat16, 4, 8 * (odd == 0)), buffer(residual, 5, step * (odd == 1)),
+                buffer(torch.bfloat16, 6, 8 * (odd == 2)), buffer(residual, 7, step * (odd == 3))]
+        bufs[0].copy_(x)
+        bufs[1].copy_(r)
+        assert bufs[odd].data_ptr() % 32 == 16
+        bsfp8.bsmx_rmsnorm_quant("mxfp8", bufs[0], w, 1e-6, rows, K, residual=bufs[1], y=bufs[2], residual_out=bufs[3])
+        assert torch.equal(bufs[2], want[0]) and torch.equal(bufs[3], want[1])
 
 
 # -------------------------------------------------------------------------------- SwiGLU
 @pytest.mark.parametrize("fmt", FORMATS)
-@pytest.mark.parametrize("rows,N", [(1, 128), (5, 640), (131, 2048), (3, 9216)])
+@pytest.mark.parametrize("rows,N", [(1, 128), (17, 128), (3, 384), (5, 640), (131, 2048), (3, 9216)])
 def test_swiglu(fmt, rows, N):
     h = _rand((rows, 2 * N), torch.bfloat16, seed=N, spread=1.0)
     h[0, :64] = 30.0
@@ -284,12 +300,14 @@ def test_swiglu_of_extreme_gates():
     h[1, :N] = 300.0
     h[2, 3] = float("inf")
     h[3, N + 130] = float("nan")
+    h[3, 0], h[3, N] = -1e20, 1e20  # 0 although gate times up is past fp32
     q, s = _operand("mxfp8", 4, N)
     bsfp8.bsmx_swiglu_quant("mxfp8", h.cuda(), q, s, 4, N)
     v, sc = ref.decode(q[: 4 * N], s[: 4 * N // 32], "mxfp8", 4, N)
     assert np.all(v[0] == 0) and np.all(sc[0] == 1)
     assert np.all(v[1] * sc[1][0] == 288.0)  # 300 = 300 / 1 in e4m3's grid of 32
     assert np.isnan(sc[2, 0]) and np.isfinite(sc[2, 1:]).all()
+    assert v[3, 0] == 0
     assert np.isnan(sc[3, 130 // 32]) and np.isfinite(np.delete(sc[3], 130 // 32)).all()
 
 
@@ -311,7 +329,7 @@ def _sort(ids, E, with_slot=True):
 
 @pytest.mark.parametrize("E", [1, 8, 60, 256, 1500, 4096])
 @pytest.mark.parametrize("rows,top_k", [(0, 8), (1, 1), (1, 8), (31, 1), (33, 2), (129, 6), (512, 8), (513, 8), (700, 11),
-                                        (5000, 1), (16384, 8), (20011, 9)])
+                                        (5000, 1), (16384, 8), (20011, 9), (70001, 8)])
 def test_sort(rows, top_k, E):
     g = np.random.default_rng(rows + E)
     ids = np.minimum(g.zipf(1.3, size=(rows, top_k)) - 1, 1 << 20).astype(np.int32)
@@ -347,7 +365,7 @@ def _routed(rows, top_k, E, seed, dropped=0.2):
     return row, g.random((rows, top_k)).astype(np.float32)
 
 
-SHAPES = [(1, 1, 8), (1, 8, 7168), (3, 2, 136), (50, 8, 2048), (17, 13, 4104), (9, 64, 256), (2, 4, 20000)]
+SHAPES = [(1, 1, 8), (1, 8, 7168), (6, 1, 520), (7, 3, 264), (5, 4, 2048), (600, 5, 512), (3, 2, 136), (50, 8, 2048), (17, 13, 4104), (9, 64, 256), (2, 4, 20000)]
 
 
 @pytest.mark.parametrize("weighted", [False, True])

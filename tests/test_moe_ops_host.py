@@ -29,7 +29,7 @@ def _quantize(lib, **kw):
     (dict(fmt=4), FORMAT), (dict(fmt=-1), FORMAT), (dict(xt=3), FORMAT),
     (dict(x=None), NULL), (dict(q=None), NULL), (dict(s=None), NULL),
     (dict(K=0), SHAPE), (dict(K=64), SHAPE), (dict(K=200), SHAPE), (dict(rows=-1), SHAPE),
-    (dict(rows=1 << 31, out=1 << 31), SHAPE), (dict(out=6), SHAPE), (dict(k=2), SHAPE),
+    (dict(K=(1 << 24) + 128), SHAPE), (dict(rows=1 << 31, out=1 << 31), SHAPE), (dict(out=6), SHAPE), (dict(k=2), SHAPE),
     (dict(map=FAKE, k=0), SHAPE), (dict(map=FAKE, k=65), SHAPE),
     (dict(map=FAKE, k=64, rows=1 << 26), SHAPE), (dict(map=FAKE, k=2, out=-1), SHAPE),
     (dict(x=FAKE + 8), ALIGN), (dict(q=FAKE + 8), ALIGN), (dict(fmt=3, s=FAKE + 2), ALIGN),
