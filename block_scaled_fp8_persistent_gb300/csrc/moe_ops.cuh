@@ -7,6 +7,44 @@
 
 namespace bsfp8 {
 
+// Programmatic launches.  A small kernel of these operators starts while the one before it on
+// the stream is still running: it lets the next one do so, and touches memory only once the
+// kernel before has completed and its writes are visible (at once where that one was not
+// overlapped).  Kernels take `early` as an argument: the two instructions cost a block
+// more than they gain in grids of many blocks (8192 x 2 rows of 512 columns summed 7.4 us
+// without, 9.4 with), while decode-sized grids gain 0.3 us of 2 to 3.
+__device__ __forceinline__ void launch_dependents() {
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+}
+__device__ __forceinline__ void wait_for_previous() {
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+}
+__device__ __forceinline__ void begin_early(bool early) {
+  if (early) {
+    launch_dependents();
+    wait_for_previous();
+  }
+}
+
+constexpr uint64_t kEarlyBlocks = 1024;  // most blocks of a grid that starts early
+inline bool starts_early(dim3 grid) { return (uint64_t)grid.x * grid.y <= kEarlyBlocks; }
+
+template <typename... P, typename... A>
+cudaError_t launch(void (*kernel)(P...), dim3 grid, dim3 block, size_t smem, bool early,
+                   cudaStream_t stream, A... args) {
+  cudaLaunchConfig_t config = {};
+  config.gridDim = grid;
+  config.blockDim = block;
+  config.dynamicSmemBytes = smem;
+  config.stream = stream;
+  cudaLaunchAttribute serial = {};
+  serial.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  serial.val.programmaticStreamSerializationAllowed = 1;
+  config.attrs = &serial;
+  config.numAttrs = early ? 1 : 0;
+  return cudaLaunchKernelEx(&config, kernel, args...);
+}
+
 enum ElementType : int { E_BF16 = 0, E_FP16 = 1, E_FP32 = 2 };
 
 struct QuantizeArgs {

@@ -74,7 +74,8 @@ struct PieceGrid {
 // and hands it to store(o, row, item).
 template <int FMT, bool NARROW, typename Load, typename Store>
 __device__ __forceinline__ void quantise_piece(int64_t rows, int items, int side,
-                                               const Load& load, const Store& store) {
+                                               bool early, const Load& load, const Store& store) {
+  begin_early(early);
   int64_t row = blockIdx.x;
   int i = blockIdx.y * blockDim.x + threadIdx.x;
   bool live = i < items;
@@ -95,9 +96,9 @@ __device__ __forceinline__ void quantise_piece(int64_t rows, int items, int side
 // ---------------------------------------------------------------------------------------
 template <int FMT, int XT, bool MAP, bool NARROW>
 __global__ void __launch_bounds__(MAP ? kMapThreads : kPieceThreads, MAP ? 3 : kPieceBlocks)
-    quantize_kernel(QuantizeArgs a, int side) {
+    quantize_kernel(QuantizeArgs a, int side, bool early) {
   quantise_piece<FMT, NARROW>(
-      a.rows, a.K / 16, side,
+      a.rows, a.K / 16, side, early,
       [&](int64_t t, int i, float (&v)[16]) { load16<XT>(a.x, t * a.K + (int64_t)i * 16, v); },
       [&](const Quantised<FMT>& o, int64_t t, int i) {
         if constexpr (!MAP) {
@@ -161,13 +162,14 @@ __device__ __forceinline__ void store16_fp32(float* p, const float (&v)[16]) {
 // threads per SM (16384 rows of 7168 with y, mxfp8: 152 us, 7.0 TB/s, against 161 with 1536);
 // fp32 ones take 42 (209 against 214).
 template <int FMT, bool Q, int RT, int ITEMS, bool WIDE, int LANES, int THREADS, int BLOCKS>
-__global__ void __launch_bounds__(THREADS, BLOCKS) rmsnorm_kernel(NormArgs a) {
+__global__ void __launch_bounds__(THREADS, BLOCKS) rmsnorm_kernel(NormArgs a, bool early) {
   const int64_t t = LANES ? (int64_t)blockIdx.x * (blockDim.x / (LANES ? LANES : 1)) +
                                 threadIdx.x / (LANES ? LANES : 1)
                           : blockIdx.x;
   const int first = LANES ? threadIdx.x % (LANES ? LANES : 1) : threadIdx.x;
   const int stride = LANES ? LANES : blockDim.x;
   const int items = t < a.rows ? a.K / 16 : 0;
+  begin_early(early);
   float h[ITEMS][16];
   float sum = 0.0f;
 #pragma unroll
@@ -262,10 +264,10 @@ __device__ __forceinline__ void swiglu2(float& g0, float& g1, float u0, float u1
 }
 
 template <int FMT, bool NARROW>
-__global__ void __launch_bounds__(kPieceThreads, kPieceBlocks) swiglu_kernel(SwigluArgs a,
-                                                                             int side) {
+__global__ void __launch_bounds__(kPieceThreads, kPieceBlocks) swiglu_kernel(SwigluArgs a, int side,
+                                                                             bool early) {
   quantise_piece<FMT, NARROW>(
-      a.rows, a.N / 16, side,
+      a.rows, a.N / 16, side, early,
       [&](int64_t t, int i, float (&v)[16]) {
         float u[16];
         const int64_t at = t * 2 * a.N + (int64_t)i * 16;
@@ -282,27 +284,19 @@ __global__ void __launch_bounds__(kPieceThreads, kPieceBlocks) swiglu_kernel(Swi
 
 bool aligned_32(const void* p) { return (reinterpret_cast<uintptr_t>(p) % 32) == 0; }
 
-int block_for(int items, int most) {
-  const int t = (items + 31) / 32 * 32;
-  return t < most ? t : most;
-}
-
 template <int FMT, int XT>
 cudaError_t quantize_as(const QuantizeArgs& a, cudaStream_t stream) {
-  if (a.row_of_slot) {
-    const PieceGrid g(a.rows, a.K, a.rows < kMapFewRows ? kMapThreadsFewRows : kMapThreads);
-    if (g.side > 1)
-      quantize_kernel<FMT, XT, true, true><<<g.grid, g.threads, 0, stream>>>(a, g.side);
-    else
-      quantize_kernel<FMT, XT, true, false><<<g.grid, g.threads, 0, stream>>>(a, g.side);
-  } else {
-    const PieceGrid g(a.rows, a.K, kPieceThreads);
-    if (g.side > 1)
-      quantize_kernel<FMT, XT, false, true><<<g.grid, g.threads, 0, stream>>>(a, g.side);
-    else
-      quantize_kernel<FMT, XT, false, false><<<g.grid, g.threads, 0, stream>>>(a, g.side);
-  }
-  return cudaGetLastError();
+  const bool map = a.row_of_slot != nullptr;
+  const PieceGrid g(a.rows, a.K,
+                    !map                     ? kPieceThreads
+                    : a.rows < kMapFewRows ? kMapThreadsFewRows
+                                             : kMapThreads);
+  const auto kernel = map ? (g.side > 1 ? quantize_kernel<FMT, XT, true, true>
+                                        : quantize_kernel<FMT, XT, true, false>)
+                          : (g.side > 1 ? quantize_kernel<FMT, XT, false, true>
+                                        : quantize_kernel<FMT, XT, false, false>);
+  const bool early = starts_early(g.grid);
+  return launch(kernel, g.grid, g.threads, 0, early, stream, a, g.side, early);
 }
 
 template <int FMT>
@@ -318,21 +312,18 @@ template <int FMT, bool Q, int RT, bool WIDE>
 cudaError_t norm_as(const NormArgs& a, cudaStream_t stream) {
   const int items = a.K / 16;
   const unsigned rows = (unsigned)a.rows;
-  const auto packed = [&](int each) { return (unsigned)((a.rows + each - 1) / each); };
+  const auto go = [&](void (*kernel)(NormArgs, bool), unsigned blocks, int threads) {
+    const bool early = starts_early(blocks);
+    return launch(kernel, blocks, (threads + 31) / 32 * 32, 0, early, stream, a, early);
+  };
   if (items <= 8)
-    rmsnorm_kernel<FMT, Q, RT, 1, WIDE, 8, 256, 8><<<packed(32), 256, 0, stream>>>(a);
-  else if (items <= 32)
-    rmsnorm_kernel<FMT, Q, RT, 1, WIDE, 32, 256, 8><<<packed(8), 256, 0, stream>>>(a);
-  else if (items <= 512)
-    rmsnorm_kernel<FMT, Q, RT, 1, WIDE, 0, 512, RT == E_FP32 ? 3 : 4>
-        <<<rows, block_for(items, 512), 0, stream>>>(a);
-  else if (items <= 1024)
-    rmsnorm_kernel<FMT, Q, RT, 1, WIDE, 0, 1024, 2>
-        <<<rows, block_for(items, 1024), 0, stream>>>(a);
-  else
-    rmsnorm_kernel<FMT, Q, RT, 2, WIDE, 0, 1024, 1>
-        <<<rows, block_for((items + 1) / 2, 1024), 0, stream>>>(a);
-  return cudaGetLastError();
+    return go(rmsnorm_kernel<FMT, Q, RT, 1, WIDE, 8, 256, 8>, (unsigned)((a.rows + 31) / 32), 256);
+  if (items <= 32)
+    return go(rmsnorm_kernel<FMT, Q, RT, 1, WIDE, 32, 256, 8>, (unsigned)((a.rows + 7) / 8), 256);
+  if (items <= 512)
+    return go(rmsnorm_kernel<FMT, Q, RT, 1, WIDE, 0, 512, RT == E_FP32 ? 3 : 4>, rows, items);
+  if (items <= 1024) return go(rmsnorm_kernel<FMT, Q, RT, 1, WIDE, 0, 1024, 2>, rows, items);
+  return go(rmsnorm_kernel<FMT, Q, RT, 2, WIDE, 0, 1024, 1>, rows, (items + 1) / 2);
 }
 
 template <int FMT, bool Q>
@@ -346,11 +337,9 @@ cudaError_t norm_format(int residual_type, const NormArgs& a, cudaStream_t strea
 template <int FMT>
 cudaError_t swiglu_format(const SwigluArgs& a, cudaStream_t stream) {
   const PieceGrid g(a.rows, a.N, kPieceThreads);
-  if (g.side > 1)
-    swiglu_kernel<FMT, true><<<g.grid, g.threads, 0, stream>>>(a, g.side);
-  else
-    swiglu_kernel<FMT, false><<<g.grid, g.threads, 0, stream>>>(a, g.side);
-  return cudaGetLastError();
+  const bool early = starts_early(g.grid);
+  return launch(g.side > 1 ? swiglu_kernel<FMT, true> : swiglu_kernel<FMT, false>, g.grid,
+                g.threads, 0, early, stream, a, g.side, early);
 }
 
 }  // namespace

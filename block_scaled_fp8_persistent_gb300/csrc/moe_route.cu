@@ -18,8 +18,8 @@ namespace {
 //   + (earlier in its warp),
 // the key being the expert, or `experts` for dropped slots.  Counts only, no atomics whose
 // order could show: equal keys keep their order.  Bound by launches and round trips to L2, not
-// by bytes (12 per slot): one launch up to kSortSingle slots (128 slots of 64 experts 2.2 us,
-// 4096 slots 6.5 us), above that two, the second started before the first ends (8192 to 65536
+// by bytes (12 per slot): one launch up to kSortSingle slots (128 slots of 64 experts 1.8 us,
+// 4096 slots 6.2 us), above that two, the second started before the first ends (8192 to 65536
 // slots 6.0 to 6.2 us, 524288 slots 9.4 us; one block alone takes 55 us for 65536).
 // ---------------------------------------------------------------------------------------
 constexpr int kSortThreads = 1024;
@@ -44,15 +44,6 @@ int sort_warps(int64_t chunk, int experts) {
   return w;
 }
 
-// Programmatic launches: lets the next kernel of the stream start, and waits until the one
-// before it has completed (at once where it was not launched early).
-__device__ __forceinline__ void launch_dependents() {
-  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-}
-__device__ __forceinline__ void wait_for_previous() {
-  asm volatile("griddepcontrol.wait;" ::: "memory");
-}
-
 __device__ __forceinline__ int key_of(int id, int experts) {
   return (unsigned)id < (unsigned)experts ? id : experts;
 }
@@ -61,6 +52,8 @@ __device__ __forceinline__ int key_of(int id, int experts) {
 __global__ void __launch_bounds__(kSortThreads) sort_count_kernel(SortArgs a, int64_t chunk) {
   extern __shared__ int hist[];
   const int keys = a.experts + 1;
+  // The place kernel reads the ids before its own wait.  This kernel does not start early, so
+  // whatever wrote them has completed.
   launch_dependents();
   for (int e = threadIdx.x; e < keys; e += blockDim.x) hist[e] = 0;
   __syncthreads();
@@ -98,7 +91,7 @@ __device__ __forceinline__ int block_exclusive(int v, int* warp_sums, int& total
 }
 
 // Rows of one chunk's slots.  With one block the counts come from its own histograms, added up
-// by one thread per key (1024 slots: 4.0 us, one warp per key 4.9); otherwise from the counts of
+// by one thread per key (1024 slots: 3.4 us; with one warp per key 0.9 us more); otherwise from the counts of
 // every chunk (at most kSortMaxChunks), which one warp per key reads and adds up side by side.
 __global__ void __launch_bounds__(kSortThreads) sort_place_kernel(SortArgs a, int64_t chunk,
                                                                   int warps) {
@@ -115,11 +108,13 @@ __global__ void __launch_bounds__(kSortThreads) sort_place_kernel(SortArgs a, in
   const int64_t hi = warp < warps ? (lo + seg < end ? lo + seg : end) : lo;
 
   for (int e = threadIdx.x; e < warps * pitch; e += blockDim.x) hist[e] = 0;
+  if (gridDim.x == 1) wait_for_previous();  // otherwise the count kernel has waited for the ids
   __syncthreads();
   for (int64_t s = lo + lane; s < hi; s += 32)
     atomicAdd(&hist[warp * pitch + key_of(__ldg(a.ids + s), a.experts)], 1);
   __syncthreads();
   wait_for_previous();  // the chunks' counts; nothing is written before
+  launch_dependents();
 
   const int chunks = gridDim.x;
   constexpr int kKeys = 4;  // keys whose counts a warp has in flight
@@ -236,9 +231,10 @@ __device__ __forceinline__ void unpack8(const uint32_t (&w)[4], float (&v)[8]) {
 
 // SLOTS rows of a token in flight per thread.
 template <int SLOTS>
-__global__ void __launch_bounds__(64) combine_kernel(CombineArgs a) {
+__global__ void __launch_bounds__(64) combine_kernel(CombineArgs a, bool early) {
   const int64_t t = blockIdx.x;
   const int col = (blockIdx.y * blockDim.x + threadIdx.x) * 8;
+  begin_early(early);
   if (col >= a.N) return;
   float acc[8] = {};
   if (a.residual) {
@@ -275,10 +271,12 @@ __global__ void __launch_bounds__(64) combine_kernel(CombineArgs a) {
 }
 
 template <int SLOTS>
-__global__ void __launch_bounds__(256) combine_backward_kernel(CombineBackwardArgs a) {
+__global__ void __launch_bounds__(256) combine_backward_kernel(CombineBackwardArgs a,
+                                                                       bool early) {
   __shared__ float part[8][SLOTS];
   const int64_t t = blockIdx.x;
   const int lane = threadIdx.x % 32, warp = threadIdx.x / 32;
+  begin_early(early);
   for (int j0 = 0; j0 < a.top_k; j0 += SLOTS) {
     int row[SLOTS];
     float g[SLOTS], dot[SLOTS] = {};
@@ -349,53 +347,34 @@ cudaError_t launch_moe_sort(const SortArgs& a, cudaStream_t stream) {
         sort_place_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
     if (e != cudaSuccess) return e;
   }
-  if (single) {
-    sort_place_kernel<<<1, threads, smem, stream>>>(a, chunk, warps);
-    return cudaGetLastError();
-  }
-  sort_count_kernel<<<chunks, kSortThreads, keys * sizeof(int), stream>>>(a, chunk);
-  const cudaError_t e = cudaGetLastError();
+  if (single) return launch(sort_place_kernel, 1, threads, smem, true, stream, a, chunk, warps);
+  const cudaError_t e = launch(sort_count_kernel, chunks, kSortThreads, keys * sizeof(int), false,
+                               stream, a, chunk);
   if (e != cudaSuccess) return e;
-  // started while the counts are still being made: it clears and fills its own histograms
-  // before it waits for them
-  cudaLaunchConfig_t config = {};
-  config.gridDim = dim3(chunks);
-  config.blockDim = dim3(threads);
-  config.dynamicSmemBytes = smem;
-  config.stream = stream;
-  cudaLaunchAttribute early = {};
-  early.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  early.val.programmaticStreamSerializationAllowed = 1;
-  config.attrs = &early;
-  config.numAttrs = 1;
-  return cudaLaunchKernelEx(&config, sort_place_kernel, a, chunk, warps);
+  // its own histograms are cleared and filled while the counts are still being made
+  return launch(sort_place_kernel, chunks, threads, smem, true, stream, a, chunk, warps);
 }
 
 cudaError_t launch_moe_combine(const CombineArgs& a, cudaStream_t stream) {
   const int vecs = a.N / 8;
   const int threads = vecs < 64 ? (vecs + 31) / 32 * 32 : 64;
   const dim3 grid((unsigned)a.rows, (unsigned)((vecs + threads - 1) / threads));
-  if (a.top_k <= 1)
-    combine_kernel<1><<<grid, threads, 0, stream>>>(a);
-  else if (a.top_k <= 2)
-    combine_kernel<2><<<grid, threads, 0, stream>>>(a);
-  else if (a.top_k <= 4)
-    combine_kernel<4><<<grid, threads, 0, stream>>>(a);
-  else
-    combine_kernel<8><<<grid, threads, 0, stream>>>(a);
-  return cudaGetLastError();
+  const auto kernel = a.top_k <= 1   ? combine_kernel<1>
+                      : a.top_k <= 2 ? combine_kernel<2>
+                      : a.top_k <= 4 ? combine_kernel<4>
+                                     : combine_kernel<8>;
+  const bool early = starts_early(grid);
+  return launch(kernel, grid, threads, 0, early, stream, a, early);
 }
 
 cudaError_t launch_moe_combine_backward(const CombineBackwardArgs& a, cudaStream_t stream) {
   const int vecs = a.N / 8;
   const int threads = vecs >= 256 ? 256 : (vecs + 31) / 32 * 32;
-  if (a.top_k <= 2)
-    combine_backward_kernel<2><<<(unsigned)a.rows, threads, 0, stream>>>(a);
-  else if (a.top_k <= 4)
-    combine_backward_kernel<4><<<(unsigned)a.rows, threads, 0, stream>>>(a);
-  else
-    combine_backward_kernel<8><<<(unsigned)a.rows, threads, 0, stream>>>(a);
-  return cudaGetLastError();
+  const auto kernel = a.top_k <= 2   ? combine_backward_kernel<2>
+                      : a.top_k <= 4 ? combine_backward_kernel<4>
+                                     : combine_backward_kernel<8>;
+  const bool early = starts_early((unsigned)a.rows);
+  return launch(kernel, (unsigned)a.rows, threads, 0, early, stream, a, early);
 }
 
 }  // namespace bsfp8
