@@ -8,6 +8,7 @@
 
 #include "bsfp8.h"
 #include "common.cuh"
+#include "moe_ops.cuh"
 #include "ptx.cuh"
 
 namespace bsfp8 {

@@ -3,7 +3,6 @@
 #include <cmath>
 
 #include "bsfp8.h"
-#include "common.cuh"
 #include "moe_ops.cuh"
 
 using namespace bsfp8;

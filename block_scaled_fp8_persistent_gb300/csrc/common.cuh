@@ -15,7 +15,6 @@ enum DeviceError : int {
   DEV_TIMEOUT = 7,      // a pipeline wait gave up (the kernel wound down cleanly)
   DEV_BAD_EXPERT_IDS = 8,  // an expert id outside [0, num_experts)
   DEV_BOUNDS = 10,  // debug builds: a tile's rows, columns or expert fell outside the problem
-  DEV_BAD_ROWS = 11,  // a row map's entry at or past the number of rows it may name
 };
 
 // Debug builds (-DBSFP8_DEBUG=1) check every tile's coordinates against the problem before
@@ -114,8 +113,5 @@ TmemPlan mx_pair_tmem_plan();
 // a 128-row block keeps its 4 codes of the 128-K block at byte (r % 32) * 16 + (r / 32) * 4.
 cudaError_t launch_pack_mx_b_scales(const uint8_t* src, uint8_t* dst, int E, int N, int K,
                                     int num_sms, cudaStream_t stream);
-
-// The current device's error word (a bsfp8_status: BSFP8_OK, or why there is none).
-int device_error_word(int** err);
 
 }  // namespace bsfp8

@@ -45,6 +45,12 @@ cudaError_t launch(void (*kernel)(P...), dim3 grid, dim3 block, size_t smem, boo
   return cudaLaunchKernelEx(&config, kernel, args...);
 }
 
+// Device error code beside those of common.cuh: a row map's entry names a row that is not there.
+constexpr int DEV_BAD_ROWS = 11;
+
+// The current device's error word (a bsfp8_status: BSFP8_OK, or why there is none); capi.cu.
+int device_error_word(int** err);
+
 enum ElementType : int { E_BF16 = 0, E_FP16 = 1, E_FP32 = 2 };
 
 struct QuantizeArgs {

@@ -9,7 +9,6 @@
 // tiles of 8 rows x 128 columns per warp 122.
 #include <cuda_fp16.h>
 
-#include "common.cuh"
 #include "moe_ops.cuh"
 #include "ptx.cuh"
 #include "quant.cuh"

@@ -1,7 +1,6 @@
 // Tokens sorted by expert, and the way back: the stable counting sort that gives every slot
 // (token t's j-th choice, slot t * top_k + j) its row in the grouped GEMM's operand, the
 // weighted sum of a token's rows, and that sum's gradient.
-#include "common.cuh"
 #include "moe_ops.cuh"
 #include "ptx.cuh"
 #include "quant.cuh"
