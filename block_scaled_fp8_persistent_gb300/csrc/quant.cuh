@@ -14,6 +14,8 @@
 #include <cuda_runtime.h>
 #include <cstdint>
 
+#include "ptx.cuh"
+
 namespace bsfp8 {
 
 enum QuantFormat : int { Q_MXFP8 = 0, Q_MXFP4 = 1, Q_NVFP4 = 2, Q_BLOCKWISE = 3 };
@@ -149,10 +151,17 @@ __device__ __forceinline__ void store_scale(const Quantised<FMT>& o, void* scale
                                             int64_t rows, int item, int K) {
   using T = QuantTraits<FMT>;
   if (item % T::group != 0) return;
-  if constexpr (FMT == Q_BLOCKWISE)
-    static_cast<uint32_t*>(scales)[(item / T::group) * rows + row] = o.scale;
-  else
+  if constexpr (FMT == Q_BLOCKWISE) {
+    // Rows next to each other fill a sector from several blocks: it is to stay in L2 until they
+    // have, or it goes to memory in parts (8192 rows of 7168 to 8 places with their sort 98.7 us
+    // at the default priority, 92.7 so, 86.9 without any scales).
+    asm volatile("st.global.L2::cache_hint.b32 [%0], %1, %2;" ::"l"(
+                     static_cast<uint32_t*>(scales) + (item / T::group) * rows + row),
+                 "r"(o.scale), "l"(l2_policy_evict_last())
+                 : "memory");
+  } else {
     static_cast<uint8_t*>(scales)[row * (K / T::vec) + item / T::group] = (uint8_t)o.scale;
+  }
 }
 
 __device__ __forceinline__ void unpack_bf16x2(uint32_t w, float& lo, float& hi) {
