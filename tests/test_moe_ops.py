@@ -471,7 +471,75 @@ def test_dispatch_gradient_is_the_unweighted_combine():
     assert np.all(np.abs(dx.cpu().double().numpy() - x) <= HALF_BF16 * np.abs(x) + 1e-5)
 
 
+# ------------------------------------------------------------------------------ refusals
+def test_binding_refuses_wrong_tensors():
+    T, K = 4, 256
+    bf = lambda *shape: torch.zeros(*shape, dtype=torch.bfloat16, device="cuda")  # noqa: E731
+    q, s = _operand("mxfp8", T, K)
+    ids = torch.zeros(T, 2, dtype=torch.int32, device="cuda")
+    w = torch.zeros(T, 2, device="cuda")
+    for bad in (lambda: bsfp8.bsmx_quantize("mxfp8", bf(K, T).t(), q, s, T, K),
+                lambda: bsfp8.bsmx_quantize("mxfp8", bf(T, K).cpu(), q, s, T, K),
+                lambda: bsfp8.bsmx_quantize("mxfp8", bf(T - 1, K), q, s, T, K),
+                lambda: bsfp8.bsmx_quantize("mxfp8", bf(T, K).double(), q, s, T, K),
+                lambda: bsfp8.bsmx_quantize("mxfp8", bf(T, K), q[: T * K - 1], s, T, K),
+                lambda: bsfp8.bsmx_quantize("mxfp8", bf(T, K), q, s[: T * K // 32 - 1], T, K),
+                lambda: bsfp8.bsmx_quantize("blockwise", bf(T, K), q, s, T, K),
+                lambda: bsfp8.bsmx_quantize("mxfp8", bf(T, K), q, s, T, K, x_type="fp32"),
+                lambda: bsfp8.bsmx_quantize("mxfp8", bf(T, K), q, s, T, K, row_of_slot=ids.long(), top_k=2, out_rows=8),
+                lambda: bsfp8.bsmx_quantize("mxfp8", bf(T, K), q, s, T, K, row_of_slot=ids, top_k=2, out_rows=8),
+                lambda: bsfp8.bsmx_rmsnorm_quant("mxfp8", bf(T, K), bf(K - 1), 1e-6, T, K, y=bf(T, K)),
+                lambda: bsfp8.bsmx_rmsnorm_quant("mxfp8", bf(T, K), bf(K).float(), 1e-6, T, K, y=bf(T, K)),
+                lambda: bsfp8.bsmx_rmsnorm_quant("mxfp8", bf(T, K), bf(K), 1e-6, T, K, residual=bf(T, K),
+                                                 residual_out=bf(T, K).float()),
+                lambda: bsfp8.bsmx_swiglu_quant("mxfp8", bf(T, K), q, s, T, K),
+                lambda: bsfp8.bsmx_moe_sort(ids, ids.reshape(-1)[:5], ids, None, T, 2, 8),
+                lambda: bsfp8.bsmx_moe_combine(bf(8, K), ids, bf(T, K), T, 9, 2, K, weights=w),
+                lambda: bsfp8.bsmx_moe_combine(bf(8, K), ids, bf(T, K), T, 8, 2, K, weights=w.to(torch.bfloat16)),
+                lambda: bsfp8.bsmx_moe_combine_backward(bf(T, K), bf(8, K), ids, w, bf(8, K), w[:3], T, 8, 2, K)):
+        with pytest.raises(ValueError):
+            bad()
+    with pytest.raises(bsfp8.BsFp8Error):
+        bsfp8.bsmx_moe_sort(torch.zeros(5000, 2, dtype=torch.int32, device="cuda"), torch.zeros(10, dtype=torch.int32, device="cuda"),
+                            torch.zeros(10000, dtype=torch.int32, device="cuda"), None, 5000, 2, 8)
+    _no_error()
+
+
 # ------------------------------------------------------------- streams, graphs, empty, large
+def test_chain_of_small_calls_back_to_back():
+    # each small kernel may start before the one before it ends: the chain's values show whether
+    # each waited for it
+    rows, K, top_k, E = 24, 2048, 4, 8
+    g = np.random.default_rng(1)
+    ids = torch.from_numpy(g.integers(0, E, size=(rows, top_k)).astype(np.int32)).cuda()
+    w = torch.ones(K, dtype=torch.bfloat16, device="cuda")
+    half = torch.full((rows, top_k), 0.25, device="cuda")
+    n = rows * top_k
+    ones = torch.ones(n, K, dtype=torch.bfloat16, device="cuda")
+    row, off = torch.empty(n, dtype=torch.int32, device="cuda"), torch.empty(E + 2, dtype=torch.int32, device="cuda")
+
+    def chain(x, steps, sync):
+        for _ in range(steps):
+            y, C = torch.empty_like(x), torch.zeros(n, K, dtype=torch.bfloat16, device="cuda")
+            q, s = _operand("mxfp8", rows, K)
+            dw = torch.empty(rows, top_k, device="cuda")
+            out = torch.empty_like(x)
+            for call in (lambda: bsfp8.bsmx_rmsnorm_quant("mxfp8", x, w, 1e-6, rows, K, y=y),
+                         lambda: bsfp8.bsmx_moe_sort(ids, off, row, None, rows, top_k, E),
+                         lambda: bsfp8.bsmx_moe_combine_backward(y, ones, row, half, C, dw, rows, n, top_k, K),
+                         lambda: bsfp8.bsmx_moe_combine(C, row, out, rows, n, top_k, K),
+                         lambda: bsfp8.bsmx_quantize("mxfp8", out, q, s, rows, K)):
+                call()
+                if sync:
+                    torch.cuda.synchronize()
+            x = out
+        return x, q, s
+
+    x = _rand((rows, K), torch.bfloat16, seed=4, spread=0.5).cuda()
+    for a, b in zip(chain(x, 12, False), chain(x, 12, True)):
+        assert torch.equal(a, b)
+
+
 def test_empty_calls():
     bsfp8.bsmx_quantize("mxfp8", None, None, None, 0, 256, x_type="bf16")
     bsfp8.bsmx_swiglu_quant("mxfp8", None, None, None, 0, 256)
