@@ -29,19 +29,29 @@ __device__ __forceinline__ void begin_early(bool early) {
 constexpr uint64_t kEarlyBlocks = 1024;  // most blocks of a grid that starts early
 inline bool starts_early(dim3 grid) { return (uint64_t)grid.x * grid.y <= kEarlyBlocks; }
 
+// cluster: blocks of one, all of a grid's where it is above 1
 template <typename... P, typename... A>
 cudaError_t launch(void (*kernel)(P...), dim3 grid, dim3 block, size_t smem, bool early,
-                   cudaStream_t stream, A... args) {
+                   cudaStream_t stream, int cluster, A... args) {
+  cudaLaunchAttribute attrs[2] = {};
+  unsigned n = 0;
+  if (early) {
+    attrs[n].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attrs[n++].val.programmaticStreamSerializationAllowed = 1;
+  }
+  if (cluster > 1) {
+    attrs[n].id = cudaLaunchAttributeClusterDimension;
+    attrs[n].val.clusterDim.x = cluster;
+    attrs[n].val.clusterDim.y = attrs[n].val.clusterDim.z = 1;
+    ++n;
+  }
   cudaLaunchConfig_t config = {};
   config.gridDim = grid;
   config.blockDim = block;
   config.dynamicSmemBytes = smem;
   config.stream = stream;
-  cudaLaunchAttribute serial = {};
-  serial.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  serial.val.programmaticStreamSerializationAllowed = 1;
-  config.attrs = &serial;
-  config.numAttrs = early ? 1 : 0;
+  config.attrs = attrs;
+  config.numAttrs = n;
   return cudaLaunchKernelEx(&config, kernel, args...);
 }
 

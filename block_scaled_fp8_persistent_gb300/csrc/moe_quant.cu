@@ -295,7 +295,7 @@ cudaError_t quantize_as(const QuantizeArgs& a, cudaStream_t stream) {
                           : (g.side > 1 ? quantize_kernel<FMT, XT, false, true>
                                         : quantize_kernel<FMT, XT, false, false>);
   const bool early = starts_early(g.grid);
-  return launch(kernel, g.grid, g.threads, 0, early, stream, a, g.side, early);
+  return launch(kernel, g.grid, g.threads, 0, early, stream, 1, a, g.side, early);
 }
 
 template <int FMT>
@@ -313,7 +313,7 @@ cudaError_t norm_as(const NormArgs& a, cudaStream_t stream) {
   const unsigned rows = (unsigned)a.rows;
   const auto go = [&](void (*kernel)(NormArgs, bool), unsigned blocks, int threads) {
     const bool early = starts_early(blocks);
-    return launch(kernel, blocks, (threads + 31) / 32 * 32, 0, early, stream, a, early);
+    return launch(kernel, blocks, (threads + 31) / 32 * 32, 0, early, stream, 1, a, early);
   };
   if (items <= 8)
     return go(rmsnorm_kernel<FMT, Q, RT, 1, WIDE, 8, 256, 8>, (unsigned)((a.rows + 31) / 32), 256);
@@ -338,7 +338,7 @@ cudaError_t swiglu_format(const SwigluArgs& a, cudaStream_t stream) {
   const PieceGrid g(a.rows, a.N, kPieceThreads);
   const bool early = starts_early(g.grid);
   return launch(g.side > 1 ? swiglu_kernel<FMT, true> : swiglu_kernel<FMT, false>, g.grid,
-                g.threads, 0, early, stream, a, g.side, early);
+                g.threads, 0, early, stream, 1, a, g.side, early);
 }
 
 }  // namespace

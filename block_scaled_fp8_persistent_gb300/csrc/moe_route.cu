@@ -17,14 +17,19 @@ namespace {
 //   + (earlier in its warp),
 // the key being the expert, or `experts` for dropped slots.  Counts only, no atomics whose
 // order could show: equal keys keep their order.  Bound by launches and round trips to L2, not
-// by bytes (12 per slot): one launch up to kSortSingle slots (128 slots of 64 experts 1.8 us,
-// 4096 slots 6.2 us), above that two, the second started before the first ends (8192 to 65536
-// slots 6.0 to 6.2 us, 524288 slots 9.4 us; one block alone takes 55 us for 65536).
+// by bytes (12 per slot).  64 / 256 experts: one block up to kSortSingle slots (128 slots 1.9 us,
+// 512 slots 2.4; 1024 would take 3.3 / 3.7); a cluster of eight, whose blocks read each other's
+// counts from shared memory, up to kSortCluster (1024 slots 2.8 / 3.1 us, 4096 slots 3.5 / 3.8,
+// 16384 slots 5.9 / 6.7; 65536 would take 11.1 / 12.4); above that many blocks and two launches,
+// the second started before the first ends (8192 would take 6.0 / 8.4, 65536 slots 6.2 / 8.6,
+// 524288 slots 9.4 / 12.0).
 // ---------------------------------------------------------------------------------------
 constexpr int kSortThreads = 1024;
 constexpr int kSortMaxChunks = 128;
-constexpr int kSortChunk = 1024;       // smallest chunk: one 32-slot step per warp
-constexpr int64_t kSortSingle = 4096;  // up to here one block sorts alone
+constexpr int kSortChunk = 1024;  // smallest chunk: one 32-slot step per warp
+constexpr int64_t kSortSingle = 512;     // up to here one block sorts alone
+constexpr int64_t kSortCluster = 16384;   // up to here one cluster
+constexpr int kSortClusterBlocks = 8;
 constexpr int kSortSmemWords = 40 * 1024;
 
 int64_t sort_chunk(int64_t slots) {
@@ -41,6 +46,12 @@ int sort_warps(int64_t chunk, int experts) {
   while (w > 1 && w * sort_pitch(experts) > kSortSmemWords) w /= 2;
   while (w > 1 && (w / 2) * 32 >= chunk) w /= 2;
   return w;
+}
+
+__device__ __forceinline__ int ld_shared_cluster(uint32_t addr) {
+  int v;
+  asm volatile("ld.shared::cluster.s32 %0, [%1];" : "=r"(v) : "r"(addr) : "memory");
+  return v;
 }
 
 __device__ __forceinline__ int key_of(int id, int experts) {
@@ -89,9 +100,49 @@ __device__ __forceinline__ int block_exclusive(int v, int* warp_sums, int& total
   return before + inc - v;
 }
 
-// Rows of one chunk's slots.  With one block the counts come from its own histograms, added up
-// by one thread per key (1024 slots: 3.4 us; with one warp per key 0.9 us more); otherwise from the counts of
-// every chunk (at most kSortMaxChunks), which one warp per key reads and adds up side by side.
+// Exclusive prefix of one key's counts over the warps, in place; returns their sum.
+__device__ __forceinline__ int prefix_over_warps(int* count, int warps, int pitch) {
+  int sum = 0;
+  for (int w0 = 0; w0 < warps; w0 += 8) {
+    int c[8];
+#pragma unroll
+    for (int w = 0; w < 8; ++w) c[w] = w0 + w < warps ? count[(w0 + w) * pitch] : 0;
+#pragma unroll
+    for (int w = 0; w < 8; ++w) {
+      if (w0 + w < warps) count[(w0 + w) * pitch] = sum;
+      sum += c[w];
+    }
+  }
+  return sum;
+}
+
+// Writes the rows of a warp's slots lo .. hi-1; `seen` counts its slots of each key.
+__device__ __forceinline__ void place_segment(const SortArgs& a, int64_t lo, int64_t hi, int* seen,
+                                              const int* base) {
+  const int lane = threadIdx.x % 32;
+  for (int64_t s0 = lo; s0 < hi; s0 += 32) {
+    const int64_t s = s0 + lane;
+    const bool live = s < hi;
+    const unsigned active = __ballot_sync(0xffffffffu, live);
+    if (live) {
+      const int key = key_of(__ldg(a.ids + s), a.experts);
+      const unsigned peers = __match_any_sync(active, key);
+      const int rank = __popc(peers & ((1u << lane) - 1));
+      int* h = &seen[key];
+      const int place = *h + rank;
+      __syncwarp(active);
+      if (rank == 0) *h = place + __popc(peers);
+      __syncwarp(active);
+      const int row = base[key] + place;
+      a.row_of_slot[s] = key < a.experts ? row : -1;
+      if (a.slot_of_row) a.slot_of_row[row] = key < a.experts ? (int)s : -1;
+    }
+    __syncwarp();
+  }
+}
+
+// Rows of one chunk's slots, from the counts of every chunk (at most kSortMaxChunks): one warp
+// per key reads and adds up both those and its own warps' side by side.
 __global__ void __launch_bounds__(kSortThreads) sort_place_kernel(SortArgs a, int64_t chunk,
                                                                   int warps) {
   extern __shared__ int hist[];  // [warps][pitch], then [keys] first rows and [keys] totals
@@ -107,7 +158,6 @@ __global__ void __launch_bounds__(kSortThreads) sort_place_kernel(SortArgs a, in
   const int64_t hi = warp < warps ? (lo + seg < end ? lo + seg : end) : lo;
 
   for (int e = threadIdx.x; e < warps * pitch; e += blockDim.x) hist[e] = 0;
-  if (gridDim.x == 1) wait_for_previous();  // otherwise the count kernel has waited for the ids
   __syncthreads();
   for (int64_t s = lo + lane; s < hi; s += 32)
     atomicAdd(&hist[warp * pitch + key_of(__ldg(a.ids + s), a.experts)], 1);
@@ -117,17 +167,7 @@ __global__ void __launch_bounds__(kSortThreads) sort_place_kernel(SortArgs a, in
 
   const int chunks = gridDim.x;
   constexpr int kKeys = 4;  // keys whose counts a warp has in flight
-  for (int e = threadIdx.x; chunks == 1 && e < keys; e += blockDim.x) {
-    int all = 0;
-    for (int w = 0; w < warps; ++w) {
-      const int c = hist[w * pitch + e];
-      hist[w * pitch + e] = all;
-      all += c;
-    }
-    totals[e] = all;
-    base[e] = 0;
-  }
-  for (int e0 = warp; chunks > 1 && e0 < keys; e0 += kKeys * (blockDim.x / 32)) {
+  for (int e0 = warp; e0 < keys; e0 += kKeys * (blockDim.x / 32)) {
     int c[kKeys][kSortMaxChunks / 32] = {};
 #pragma unroll
     for (int n = 0; n < kKeys; ++n) {
@@ -179,25 +219,60 @@ __global__ void __launch_bounds__(kSortThreads) sort_place_kernel(SortArgs a, in
   if (blockIdx.x == 0 && threadIdx.x == 0) a.offsets[keys] = (int)a.slots;
   __syncthreads();
 
-  for (int64_t s0 = lo; s0 < hi; s0 += 32) {
-    const int64_t s = s0 + lane;
-    const bool live = s < hi;
-    const unsigned active = __ballot_sync(0xffffffffu, live);
-    if (live) {
-      const int key = key_of(__ldg(a.ids + s), a.experts);
-      const unsigned peers = __match_any_sync(active, key);
-      const int rank = __popc(peers & ((1u << lane) - 1));
-      int* h = &hist[warp * pitch + key];
-      const int place = *h + rank;
-      __syncwarp(active);
-      if (rank == 0) *h = place + __popc(peers);
-      __syncwarp(active);
-      const int row = base[key] + place;
-      a.row_of_slot[s] = key < a.experts ? row : -1;
-      if (a.slot_of_row) a.slot_of_row[row] = key < a.experts ? (int)s : -1;
+  place_segment(a, lo, hi, hist + warp * pitch, base);
+}
+
+// The same in one launch for fewer slots: the chunks' blocks are one cluster (or a single block),
+// each adds up its warps' counts, one thread per key, and reads the others' from their shared
+// memory.
+__global__ void __launch_bounds__(kSortThreads) sort_cluster_kernel(SortArgs a, int64_t chunk,
+                                                                    int warps) {
+  extern __shared__ int hist[];  // [warps][pitch], [keys] first rows, [keys] this block's counts
+  __shared__ int warp_sums[32];
+  const int keys = a.experts + 1, pitch = sort_pitch(a.experts);
+  int* const base = hist + warps * pitch;
+  int* const counts = base + keys;
+  const int lane = threadIdx.x % 32, warp = threadIdx.x / 32;
+  const int64_t begin = blockIdx.x * chunk;
+  const int64_t end = begin + chunk < a.slots ? begin + chunk : a.slots;
+  const int64_t seg = ((end - begin + warps - 1) / warps + 31) / 32 * 32;
+  const int64_t lo = begin + warp * seg;
+  const int64_t hi = warp < warps ? (lo + seg < end ? lo + seg : end) : lo;
+
+  for (int e = threadIdx.x; e < warps * pitch; e += blockDim.x) hist[e] = 0;
+  __syncthreads();
+  begin_early(true);
+  for (int64_t s = lo + lane; s < hi; s += 32)
+    atomicAdd(&hist[warp * pitch + key_of(__ldg(a.ids + s), a.experts)], 1);
+  __syncthreads();
+  for (int e = threadIdx.x; e < keys; e += blockDim.x)
+    counts[e] = prefix_over_warps(hist + e, warps, pitch);
+  if (gridDim.x > 1) cluster_sync();
+  // (block_exclusive's barriers order a single block's counts: each is read by its writer)
+
+  int carry = 0;
+  for (int e0 = 0; e0 < keys; e0 += blockDim.x) {
+    const int e = e0 + threadIdx.x;
+    int all = 0, before = 0, total;
+    if (e < keys) {
+      const uint32_t at = smem_u32(counts + e);
+      for (int b = 0; b < (int)gridDim.x; ++b) {
+        const int c = ld_shared_cluster(mapa_shared(at, b));
+        all += c;
+        before += b < (int)blockIdx.x ? c : 0;
+      }
     }
-    __syncwarp();
+    const int first = carry + block_exclusive(all, warp_sums, total);
+    carry += total;
+    if (e < keys) {
+      base[e] = first + before;
+      if (blockIdx.x == 0) a.offsets[e] = first;
+    }
   }
+  if (blockIdx.x == 0 && threadIdx.x == 0) a.offsets[keys] = (int)a.slots;
+  __syncthreads();
+  place_segment(a, lo, hi, hist + warp * pitch, base);
+  if (gridDim.x > 1) cluster_sync();  // no block's counts go away while another reads them
 }
 
 // ---------------------------------------------------------------------------------------
@@ -325,33 +400,39 @@ __global__ void __launch_bounds__(256) combine_backward_kernel(CombineBackwardAr
 }  // namespace
 
 int64_t moe_sort_workspace_bytes(int64_t slots, int experts) {
-  if (slots <= kSortSingle) return 0;
+  if (slots <= kSortCluster) return 0;
   const int64_t chunk = sort_chunk(slots);
   return (slots + chunk - 1) / chunk * (experts + 1) * (int64_t)sizeof(int32_t);
 }
 
 cudaError_t launch_moe_sort(const SortArgs& a, cudaStream_t stream) {
   const int keys = a.experts + 1;
-  const bool single = a.slots <= kSortSingle;
-  const int64_t chunk = single ? a.slots : sort_chunk(a.slots);
-  const int chunks = single ? 1 : (int)((a.slots + chunk - 1) / chunk);
+  const int blocks = a.slots <= kSortSingle ? 1 : a.slots <= kSortCluster ? kSortClusterBlocks : 0;
+  const int64_t chunk = blocks ? (a.slots + blocks - 1) / blocks : sort_chunk(a.slots);
   const int warps = sort_warps(chunk, a.experts);
   // one thread per key in the scan, as far as a block goes
   int threads = (keys + 31) / 32 * 32;
   threads = threads < warps * 32 ? warps * 32 : threads;
   threads = threads < kSortThreads ? threads : kSortThreads;
   const size_t smem = ((size_t)warps * sort_pitch(a.experts) + 2 * keys) * sizeof(int);
-  if (smem > 48 * 1024) {
-    const cudaError_t e = cudaFuncSetAttribute(
-        sort_place_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+  const auto allow = [&](const void* kernel) {
+    return smem <= 48 * 1024 ? cudaSuccess
+                             : cudaFuncSetAttribute(
+                                   kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+  };
+  if (blocks) {
+    const cudaError_t e = allow(reinterpret_cast<const void*>(sort_cluster_kernel));
     if (e != cudaSuccess) return e;
+    return launch(sort_cluster_kernel, blocks, threads, smem, true, stream, blocks, a, chunk, warps);
   }
-  if (single) return launch(sort_place_kernel, 1, threads, smem, true, stream, a, chunk, warps);
-  const cudaError_t e = launch(sort_count_kernel, chunks, kSortThreads, keys * sizeof(int), false,
-                               stream, a, chunk);
+  const cudaError_t e = allow(reinterpret_cast<const void*>(sort_place_kernel));
   if (e != cudaSuccess) return e;
+  const int chunks = (int)((a.slots + chunk - 1) / chunk);
+  const cudaError_t c = launch(sort_count_kernel, chunks, kSortThreads, keys * sizeof(int), false,
+                               stream, 1, a, chunk);
+  if (c != cudaSuccess) return c;
   // its own histograms are cleared and filled while the counts are still being made
-  return launch(sort_place_kernel, chunks, threads, smem, true, stream, a, chunk, warps);
+  return launch(sort_place_kernel, chunks, threads, smem, true, stream, 1, a, chunk, warps);
 }
 
 cudaError_t launch_moe_combine(const CombineArgs& a, cudaStream_t stream) {
@@ -363,7 +444,7 @@ cudaError_t launch_moe_combine(const CombineArgs& a, cudaStream_t stream) {
                       : a.top_k <= 4 ? combine_kernel<4>
                                      : combine_kernel<8>;
   const bool early = starts_early(grid);
-  return launch(kernel, grid, threads, 0, early, stream, a, early);
+  return launch(kernel, grid, threads, 0, early, stream, 1, a, early);
 }
 
 cudaError_t launch_moe_combine_backward(const CombineBackwardArgs& a, cudaStream_t stream) {
@@ -373,7 +454,7 @@ cudaError_t launch_moe_combine_backward(const CombineBackwardArgs& a, cudaStream
                       : a.top_k <= 4 ? combine_backward_kernel<4>
                                      : combine_backward_kernel<8>;
   const bool early = starts_early((unsigned)a.rows);
-  return launch(kernel, (unsigned)a.rows, threads, 0, early, stream, a, early);
+  return launch(kernel, (unsigned)a.rows, threads, 0, early, stream, 1, a, early);
 }
 
 }  // namespace bsfp8

@@ -346,7 +346,8 @@ bsfp8_status bsmx_swiglu_quant(int format, const void* h, void* q, void* scales,
  *                offsets[num_experts] = slots kept, offsets[num_experts + 1] = rows * top_k
  *   row_of_slot  int32 [rows, top_k]: the slot's row, -1 where it was dropped
  *   slot_of_row  int32 [rows * top_k], or NULL: its inverse, -1 for rows past the kept ones
- *   workspace    bsmx_moe_sort_workspace bytes, 4-byte aligned (NULL where that is 0)
+ *   workspace    bsmx_moe_sort_workspace bytes, 4-byte aligned (NULL where that is 0: up to
+ *                16384 slots)
  * The first num_experts + 1 offsets are a grouped GEMM's when nothing is dropped.  With dropped
  * slots either pass the kept count as M_total, or keep M_total = rows * top_k without reading
  * it back: all num_experts + 2 offsets are those of num_experts + 1 groups, the last being the

@@ -328,7 +328,7 @@ def _sort(ids, E, with_slot=True):
 
 
 @pytest.mark.parametrize("E", [1, 8, 60, 256, 1500, 4096])
-@pytest.mark.parametrize("rows,top_k", [(0, 8), (1, 1), (1, 8), (31, 1), (33, 2), (129, 6), (512, 8), (513, 8), (700, 11),
+@pytest.mark.parametrize("rows,top_k", [(0, 8), (1, 1), (1, 8), (31, 1), (33, 2), (129, 6), (512, 8), (513, 8), (512, 2), (1025, 1), (1024, 4), (700, 11), (2048, 8), (2049, 8),
                                         (5000, 1), (16384, 8), (20011, 9), (70001, 8)])
 def test_sort(rows, top_k, E):
     g = np.random.default_rng(rows + E)
@@ -340,7 +340,7 @@ def test_sort(rows, top_k, E):
         assert np.array_equal(a, b)
 
 
-@pytest.mark.parametrize("rows", [100, 9000])
+@pytest.mark.parametrize("rows", [100, 3000, 9000])
 @pytest.mark.parametrize("kind", ["dropped", "one", "last", "wild", "sorted", "reversed"])
 def test_sort_extremes(rows, kind):
     E, k = 64, 2
@@ -500,8 +500,8 @@ def test_binding_refuses_wrong_tensors():
         with pytest.raises(ValueError):
             bad()
     with pytest.raises(bsfp8.BsFp8Error):
-        bsfp8.bsmx_moe_sort(torch.zeros(5000, 2, dtype=torch.int32, device="cuda"), torch.zeros(10, dtype=torch.int32, device="cuda"),
-                            torch.zeros(10000, dtype=torch.int32, device="cuda"), None, 5000, 2, 8)
+        bsfp8.bsmx_moe_sort(torch.zeros(50000, 2, dtype=torch.int32, device="cuda"), torch.zeros(10, dtype=torch.int32, device="cuda"),
+                            torch.zeros(100000, dtype=torch.int32, device="cuda"), None, 50000, 2, 8)
     _no_error()
 
 

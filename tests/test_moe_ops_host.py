@@ -74,7 +74,7 @@ def test_swiglu_refusals(lib, kw, status):
 
 @pytest.mark.parametrize("kw,status", [
     (dict(ids=None), NULL), (dict(off=None), NULL), (dict(row=None), NULL),
-    (dict(rows=5000, ws=None), NULL), (dict(rows=5000, wsb=16), SHAPE),
+    (dict(rows=50000, ws=None), NULL), (dict(rows=50000, wsb=16), SHAPE),
     (dict(rows=-1), SHAPE), (dict(k=0), SHAPE), (dict(k=65), SHAPE), (dict(E=0), SHAPE),
     (dict(E=4097), SHAPE), (dict(rows=1 << 30, k=2), SHAPE),
     (dict(ids=FAKE + 2), ALIGN), (dict(off=FAKE + 2), ALIGN), (dict(row=FAKE + 1), ALIGN),
