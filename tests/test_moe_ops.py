@@ -193,7 +193,7 @@ def test_rows_out_of_range_are_recorded_and_skipped():
 # ---------------------------------------------------------------------------------- norm
 @pytest.mark.parametrize("fmt", FORMATS)
 @pytest.mark.parametrize("residual", [None, torch.bfloat16, torch.float32])
-@pytest.mark.parametrize("rows,K", [(1, 128), (70, 128), (9, 256), (13, 512), (7, 640), (33, 7168), (3, 8320),
+@pytest.mark.parametrize("rows,K", [(1, 128), (70, 128), (9, 256), (13, 512), (7, 640), (5, 1024), (33, 7168), (3, 8320),
                                     (2, 16512), (1, 32768)])
 def test_norm(fmt, residual, rows, K):
     x = _rand((rows, K), torch.bfloat16, seed=K, spread=2.0)
