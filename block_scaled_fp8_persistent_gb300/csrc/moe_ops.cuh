@@ -10,7 +10,8 @@ namespace bsfp8 {
 // Programmatic launches.  A small kernel of these operators starts while the one before it on
 // the stream is still running: it lets the next one do so, and touches memory only once the
 // kernel before has completed and its writes are visible (at once where that one was not
-// overlapped).  Kernels take `early` as an argument: the two instructions cost a block
+// overlapped).  No load of these kernels takes the read-only path: what they read may be written
+// by a kernel that runs after they were launched.  Kernels take `early` as an argument: the two instructions cost a block
 // more than they gain in grids of many blocks (8192 x 2 rows of 512 columns summed 7.4 us
 // without, 9.4 with), while decode-sized grids gain 0.3 us of 2 to 3.
 __device__ __forceinline__ void launch_dependents() {

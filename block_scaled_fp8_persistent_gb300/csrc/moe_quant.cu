@@ -1,5 +1,5 @@
-// Operators that write a grouped GEMM's operand: quantisation of rows (in place, or sorted by
-// expert), RMS norm with the residual's addition, SwiGLU.  All are bound by HBM: each element
+// Operators that write a grouped GEMM's operand: quantisation of rows (as they lie, or into
+// expert order), RMS norm with the residual's addition, SwiGLU.  All are bound by HBM: each element
 // is read once, its block quantised in registers (quant.cuh) and written once.
 //
 // What carries them is many threads with one straight piece of work each: 16 elements of a row
@@ -51,7 +51,7 @@ constexpr int kPieceBlocks = 6;  // per SM: at most 42 registers
 // Blocks that follow a row map.  With many rows a block takes a whole row (up to 8192 elements),
 // so that each copy is written in one go: 8192 rows of 7168 to 8 places in mxfp8, with their
 // sort, 91 us against 97 with 224 threads.  With few rows smaller blocks reach more SMs: 16
-// rows 4.1 us against 4.8.
+// rows with their sort 4.1 us against 4.8.
 constexpr int kMapThreads = 512;
 constexpr int kMapThreadsFewRows = 128;
 constexpr int64_t kMapFewRows = 512;
@@ -72,8 +72,8 @@ struct PieceGrid {
 // Quantises the thread's piece (all lanes of a warp together), which load(row, item, v) fetches,
 // and hands it to store(o, row, item).
 template <int FMT, bool NARROW, typename Load, typename Store>
-__device__ __forceinline__ void quantise_piece(int64_t rows, int items, int side,
-                                               bool early, const Load& load, const Store& store) {
+__device__ __forceinline__ void quantise_piece(int64_t rows, int items, int side, bool early,
+                                               const Load& load, const Store& store) {
   begin_early(early);
   int64_t row = blockIdx.x;
   int i = blockIdx.y * blockDim.x + threadIdx.x;
@@ -104,12 +104,19 @@ __global__ void __launch_bounds__(MAP ? kMapThreads : kPieceThreads, MAP ? 3 : k
           store_codes<FMT>(o, a.q, t, i, a.K);
           store_scale<FMT>(o, a.scales, t, a.rows, i, a.K);
         } else {
-          for (int j = 0; j < a.top_k; ++j) {
-            const int row = __ldg(a.row_of_slot + t * a.top_k + j);
-            if (row >= a.out_rows) atomicCAS(a.err, 0, DEV_BAD_ROWS);
-            if (row >= 0 && row < a.out_rows) {
-              store_codes<FMT>(o, a.q, row, i, a.K);
-              store_scale<FMT>(o, a.scales, row, a.out_rows, i, a.K);
+          constexpr int kRows = 8;  // looked up before the stores of their copies
+          for (int j0 = 0; j0 < a.top_k; j0 += kRows) {
+            int row[kRows];
+#pragma unroll
+            for (int j = 0; j < kRows; ++j)
+              row[j] = j0 + j < a.top_k ? a.row_of_slot[t * a.top_k + j0 + j] : -1;
+#pragma unroll
+            for (int j = 0; j < kRows; ++j) {
+              if (row[j] >= a.out_rows) atomicCAS(a.err, 0, DEV_BAD_ROWS);
+              if (row[j] >= 0 && row[j] < a.out_rows) {
+                store_codes<FMT>(o, a.q, row[j], i, a.K);
+                store_scale<FMT>(o, a.scales, row[j], a.out_rows, i, a.K);
+              }
             }
           }
         }
@@ -213,7 +220,7 @@ __global__ void __launch_bounds__(THREADS, BLOCKS) rmsnorm_kernel(NormArgs a, bo
     if (i < items) {
       const uint4* wp =
           reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(a.weight) + i * 16);
-      const uint4 w0 = __ldg(wp), w1 = __ldg(wp + 1);
+      const uint4 w0 = wp[0], w1 = wp[1];
       const uint32_t w[8] = {w0.x, w0.y, w0.z, w0.w, w1.x, w1.y, w1.z, w1.w};
 #pragma unroll
       for (int e = 0; e < 8; ++e) {
@@ -287,9 +294,9 @@ template <int FMT, int XT>
 cudaError_t quantize_as(const QuantizeArgs& a, cudaStream_t stream) {
   const bool map = a.row_of_slot != nullptr;
   const PieceGrid g(a.rows, a.K,
-                    !map                     ? kPieceThreads
+                    !map                   ? kPieceThreads
                     : a.rows < kMapFewRows ? kMapThreadsFewRows
-                                             : kMapThreads);
+                                           : kMapThreads);
   const auto kernel = map ? (g.side > 1 ? quantize_kernel<FMT, XT, true, true>
                                         : quantize_kernel<FMT, XT, true, false>)
                           : (g.side > 1 ? quantize_kernel<FMT, XT, false, true>

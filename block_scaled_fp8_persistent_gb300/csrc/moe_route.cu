@@ -20,15 +20,15 @@ namespace {
 // by bytes (12 per slot).  64 / 256 experts: one block up to kSortSingle slots (128 slots 1.9 us,
 // 512 slots 2.4; 1024 would take 3.3 / 3.7); a cluster of eight, whose blocks read each other's
 // counts from shared memory, up to kSortCluster (1024 slots 2.8 / 3.1 us, 4096 slots 3.5 / 3.8,
-// 16384 slots 5.9 / 6.7; 65536 would take 11.1 / 12.4); above that many blocks and two launches,
-// the second started before the first ends (8192 would take 6.0 / 8.4, 65536 slots 6.2 / 8.6,
-// 524288 slots 9.4 / 12.0).
+// 16384 slots 5.4 / 6.2; 65536 would take 11.1 / 12.4); above that many blocks and two launches,
+// the second started before the first ends (8192 would take 6.0 / 8.4, 65536 slots 6.2 / 8.7,
+// 524288 slots 8.8 / 11.6).
 // ---------------------------------------------------------------------------------------
 constexpr int kSortThreads = 1024;
 constexpr int kSortMaxChunks = 128;
-constexpr int kSortChunk = 1024;  // smallest chunk: one 32-slot step per warp
+constexpr int kSortChunk = 1024;         // smallest chunk: one 32-slot step per warp
 constexpr int64_t kSortSingle = 512;     // up to here one block sorts alone
-constexpr int64_t kSortCluster = 16384;   // up to here one cluster
+constexpr int64_t kSortCluster = 16384;  // up to here one cluster
 constexpr int kSortClusterBlocks = 8;
 constexpr int kSortSmemWords = 40 * 1024;
 
@@ -70,7 +70,7 @@ __global__ void __launch_bounds__(kSortThreads) sort_count_kernel(SortArgs a, in
   const int64_t begin = blockIdx.x * chunk;
   const int64_t end = begin + chunk < a.slots ? begin + chunk : a.slots;
   for (int64_t s = begin + threadIdx.x; s < end; s += blockDim.x)
-    atomicAdd(&hist[key_of(__ldg(a.ids + s), a.experts)], 1);
+    atomicAdd(&hist[key_of(a.ids[s], a.experts)], 1);
   __syncthreads();
   for (int e = threadIdx.x; e < keys; e += blockDim.x)
     a.workspace[(int64_t)e * gridDim.x + blockIdx.x] = hist[e];
@@ -120,12 +120,14 @@ __device__ __forceinline__ int prefix_over_warps(int* count, int warps, int pitc
 __device__ __forceinline__ void place_segment(const SortArgs& a, int64_t lo, int64_t hi, int* seen,
                                               const int* base) {
   const int lane = threadIdx.x % 32;
+  int next = lo + lane < hi ? a.ids[lo + lane] : 0;
   for (int64_t s0 = lo; s0 < hi; s0 += 32) {
     const int64_t s = s0 + lane;
     const bool live = s < hi;
+    const int key = key_of(next, a.experts);
+    if (s + 32 < hi) next = a.ids[s + 32];
     const unsigned active = __ballot_sync(0xffffffffu, live);
     if (live) {
-      const int key = key_of(__ldg(a.ids + s), a.experts);
       const unsigned peers = __match_any_sync(active, key);
       const int rank = __popc(peers & ((1u << lane) - 1));
       int* h = &seen[key];
@@ -160,7 +162,7 @@ __global__ void __launch_bounds__(kSortThreads) sort_place_kernel(SortArgs a, in
   for (int e = threadIdx.x; e < warps * pitch; e += blockDim.x) hist[e] = 0;
   __syncthreads();
   for (int64_t s = lo + lane; s < hi; s += 32)
-    atomicAdd(&hist[warp * pitch + key_of(__ldg(a.ids + s), a.experts)], 1);
+    atomicAdd(&hist[warp * pitch + key_of(a.ids[s], a.experts)], 1);
   __syncthreads();
   wait_for_previous();  // the chunks' counts; nothing is written before
   launch_dependents();
@@ -243,7 +245,7 @@ __global__ void __launch_bounds__(kSortThreads) sort_cluster_kernel(SortArgs a, 
   __syncthreads();
   begin_early(true);
   for (int64_t s = lo + lane; s < hi; s += 32)
-    atomicAdd(&hist[warp * pitch + key_of(__ldg(a.ids + s), a.experts)], 1);
+    atomicAdd(&hist[warp * pitch + key_of(a.ids[s], a.experts)], 1);
   __syncthreads();
   for (int e = threadIdx.x; e < keys; e += blockDim.x)
     counts[e] = prefix_over_warps(hist + e, warps, pitch);
@@ -290,7 +292,7 @@ __global__ void __launch_bounds__(kSortThreads) sort_cluster_kernel(SortArgs a, 
 
 __device__ __forceinline__ int checked_row(const int32_t* row_of_slot, int64_t slot,
                                            int64_t in_rows, int* err) {
-  const int row = __ldg(row_of_slot + slot);
+  const int row = row_of_slot[slot];
   if (row >= in_rows) {
     atomicCAS(err, 0, DEV_BAD_ROWS);
     return -1;
@@ -331,7 +333,7 @@ __global__ void __launch_bounds__(64) combine_kernel(CombineArgs a, bool early) 
 #pragma unroll
     for (int j = 0; j < SLOTS; ++j) {
       if (row[j] >= 0) {
-        const float g = a.weights ? __ldg(a.weights + t * a.top_k + j0 + j) : 1.0f;
+        const float g = a.weights ? a.weights[t * a.top_k + j0 + j] : 1.0f;
         float v[8];
         unpack8(w[j], v);
 #pragma unroll
@@ -346,7 +348,7 @@ __global__ void __launch_bounds__(64) combine_kernel(CombineArgs a, bool early) 
 
 template <int SLOTS>
 __global__ void __launch_bounds__(256) combine_backward_kernel(CombineBackwardArgs a,
-                                                                       bool early) {
+                                                               bool early) {
   __shared__ float part[8][SLOTS];
   const int64_t t = blockIdx.x;
   const int lane = threadIdx.x % 32, warp = threadIdx.x / 32;
@@ -358,7 +360,7 @@ __global__ void __launch_bounds__(256) combine_backward_kernel(CombineBackwardAr
     for (int j = 0; j < SLOTS; ++j) {
       const bool there = j0 + j < a.top_k;
       row[j] = there ? checked_row(a.row_of_slot, t * a.top_k + j0 + j, a.in_rows, a.err) : -1;
-      g[j] = there ? __ldg(a.weights + t * a.top_k + j0 + j) : 0.0f;
+      g[j] = there ? a.weights[t * a.top_k + j0 + j] : 0.0f;
     }
     for (int col = threadIdx.x * 8; col < a.N; col += blockDim.x * 8) {
       uint32_t wd[4], w[SLOTS][4];
