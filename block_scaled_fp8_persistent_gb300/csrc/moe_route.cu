@@ -282,12 +282,17 @@ __global__ void __launch_bounds__(kSortThreads) sort_cluster_kernel(SortArgs a, 
 //
 // Bound by HBM: every named row of C is read once.  A thread takes 8 columns of a token (16-byte
 // accesses, a warp's are 512 bytes of a row) and has the rows of up to 8 slots in flight, as
-// many as top_k needs: fewer registers, more threads (top_k 2, 512 columns: 10.3 -> 7.3 us, its
-// gradient 6.2 -> 4.5).  The sum runs in small blocks, 64 threads (8192 tokens x 8 rows of 7168
-// columns 147 us, 6.6 TB/s; 128 threads 154, 256 threads 172: the last block of a row idles half
-// its threads and its rows arrive in larger lumps).  The gradient needs a token's whole row for
-// its dot products: one block of 256 threads per token (4096 tokens x 8 rows of 7168 columns
-// 148 us, 6.7 TB/s; 64 threads 153), and no partial sums to be joined in memory.
+// many as top_k needs; the registers are held to what leaves 1000 to 2000 threads per SM.
+//   sum, 8 rows     blocks of 64 threads, 64 registers: 8192 tokens of 7168 columns 140 us,
+//                   6.9 TB/s (70 registers 146, 128 threads 145, 256 threads with 70 172)
+//   4 / 2 rows      128 threads: 8192 tokens of 4096 columns 61.4 / 41.5 us (64 threads 61.9 /
+//                   41.7; left to itself the compiler took 63.3 us for 4)
+//   1 row           128 threads and two vectors of columns per thread, else a block ends before
+//                   enough loads are out: 16384 tokens of 4096 columns 45 us (one vector 48, 64
+//                   threads 68)
+//   gradient        a token's whole row for its dot products, one block of 256 threads, no
+//                   partial sums to be joined in memory: 4096 tokens x 8 rows of 7168 columns
+//                   149 us, 6.7 TB/s (64 threads 153)
 // ---------------------------------------------------------------------------------------
 
 __device__ __forceinline__ int checked_row(const int32_t* row_of_slot, int64_t slot,
@@ -305,21 +310,35 @@ __device__ __forceinline__ void unpack8(const uint32_t (&w)[4], float (&v)[8]) {
   for (int i = 0; i < 4; ++i) unpack_bf16x2(w[i], v[2 * i], v[2 * i + 1]);
 }
 
-// SLOTS rows of a token in flight per thread.
+// SLOTS rows of a token in flight per thread, each in kCombineVecs vectors of 8 columns.
 template <int SLOTS>
-__global__ void __launch_bounds__(64) combine_kernel(CombineArgs a, bool early) {
+constexpr int kCombineThreads = SLOTS == 8 ? 64 : 128;
+template <int SLOTS>
+constexpr int kCombineBlocks = SLOTS == 4 ? 12 : 16;  // per SM
+template <int SLOTS>
+constexpr int kCombineVecs = SLOTS == 1 ? 2 : 1;
+
+template <int SLOTS>
+__global__ void __launch_bounds__(kCombineThreads<SLOTS>, kCombineBlocks<SLOTS>)
+    combine_kernel(CombineArgs a, bool early) {
+  constexpr int VECS = kCombineVecs<SLOTS>;
   const int64_t t = blockIdx.x;
-  const int col = (blockIdx.y * blockDim.x + threadIdx.x) * 8;
+  const int first = (blockIdx.y * VECS * blockDim.x + threadIdx.x) * 8;
+  const int step = blockDim.x * 8;
   begin_early(early);
-  if (col >= a.N) return;
-  float acc[8] = {};
+  float acc[VECS][8] = {};
   if (a.residual) {
-    uint32_t w[4];
-    load_words(static_cast<const uint16_t*>(a.residual) + t * a.N + col, w);
-    unpack8(w, acc);
+#pragma unroll
+    for (int v = 0; v < VECS; ++v) {
+      uint32_t w[4];
+      if (first + v * step < a.N) {
+        load_words(static_cast<const uint16_t*>(a.residual) + t * a.N + first + v * step, w);
+        unpack8(w, acc[v]);
+      }
+    }
   }
   for (int j0 = 0; j0 < a.top_k; j0 += SLOTS) {
-    uint32_t w[SLOTS][4];
+    uint32_t w[SLOTS][VECS][4];
     int row[SLOTS];
 #pragma unroll
     for (int j = 0; j < SLOTS; ++j)
@@ -328,27 +347,35 @@ __global__ void __launch_bounds__(64) combine_kernel(CombineArgs a, bool early) 
                    : -1;
 #pragma unroll
     for (int j = 0; j < SLOTS; ++j)
-      if (row[j] >= 0)
-        load_words(static_cast<const uint16_t*>(a.C) + (int64_t)row[j] * a.N + col, w[j]);
+#pragma unroll
+      for (int v = 0; v < VECS; ++v)
+        if (row[j] >= 0 && first + v * step < a.N)
+          load_words(static_cast<const uint16_t*>(a.C) + (int64_t)row[j] * a.N + first + v * step,
+                     w[j][v]);
 #pragma unroll
     for (int j = 0; j < SLOTS; ++j) {
-      if (row[j] >= 0) {
-        const float g = a.weights ? a.weights[t * a.top_k + j0 + j] : 1.0f;
-        float v[8];
-        unpack8(w[j], v);
+      if (row[j] < 0) continue;
+      const float g = a.weights ? a.weights[t * a.top_k + j0 + j] : 1.0f;
 #pragma unroll
-        for (int e = 0; e < 8; ++e) acc[e] = fmaf(g, v[e], acc[e]);
+      for (int v = 0; v < VECS; ++v) {
+        float c[8];
+        unpack8(w[j][v], c);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) acc[v][e] = fmaf(g, c[e], acc[v][e]);
       }
     }
   }
-  st_global_v4(static_cast<uint16_t*>(a.out) + t * a.N + col, pack_bf16x2(acc[0], acc[1]),
-               pack_bf16x2(acc[2], acc[3]), pack_bf16x2(acc[4], acc[5]),
-               pack_bf16x2(acc[6], acc[7]));
+#pragma unroll
+  for (int v = 0; v < VECS; ++v)
+    if (first + v * step < a.N)
+      st_global_v4(static_cast<uint16_t*>(a.out) + t * a.N + first + v * step,
+                   pack_bf16x2(acc[v][0], acc[v][1]), pack_bf16x2(acc[v][2], acc[v][3]),
+                   pack_bf16x2(acc[v][4], acc[v][5]), pack_bf16x2(acc[v][6], acc[v][7]));
 }
 
 template <int SLOTS>
-__global__ void __launch_bounds__(256) combine_backward_kernel(CombineBackwardArgs a,
-                                                               bool early) {
+__global__ void __launch_bounds__(256, SLOTS == 8 ? 3 : SLOTS == 4 ? 4 : 6)
+    combine_backward_kernel(CombineBackwardArgs a, bool early) {
   __shared__ float part[8][SLOTS];
   const int64_t t = blockIdx.x;
   const int lane = threadIdx.x % 32, warp = threadIdx.x / 32;
@@ -437,16 +464,22 @@ cudaError_t launch_moe_sort(const SortArgs& a, cudaStream_t stream) {
   return launch(sort_place_kernel, chunks, threads, smem, true, stream, 1, a, chunk, warps);
 }
 
-cudaError_t launch_moe_combine(const CombineArgs& a, cudaStream_t stream) {
-  const int vecs = a.N / 8;
-  const int threads = vecs < 64 ? (vecs + 31) / 32 * 32 : 64;
-  const dim3 grid((unsigned)a.rows, (unsigned)((vecs + threads - 1) / threads));
-  const auto kernel = a.top_k <= 1   ? combine_kernel<1>
-                      : a.top_k <= 2 ? combine_kernel<2>
-                      : a.top_k <= 4 ? combine_kernel<4>
-                                     : combine_kernel<8>;
+template <int SLOTS>
+cudaError_t combine_as(const CombineArgs& a, cudaStream_t stream) {
+  constexpr int kMost = kCombineThreads<SLOTS>, kVecs = kCombineVecs<SLOTS>;
+  const int pieces = (a.N / 8 + kVecs - 1) / kVecs;  // threads to a row
+  const int parts = (pieces + kMost - 1) / kMost;    // blocks to a row
+  const int threads = ((pieces + parts - 1) / parts + 31) / 32 * 32;
+  const dim3 grid((unsigned)a.rows, (unsigned)parts);
   const bool early = starts_early(grid);
-  return launch(kernel, grid, threads, 0, early, stream, 1, a, early);
+  return launch(combine_kernel<SLOTS>, grid, threads, 0, early, stream, 1, a, early);
+}
+
+cudaError_t launch_moe_combine(const CombineArgs& a, cudaStream_t stream) {
+  return a.top_k <= 1   ? combine_as<1>(a, stream)
+         : a.top_k <= 2 ? combine_as<2>(a, stream)
+         : a.top_k <= 4 ? combine_as<4>(a, stream)
+                        : combine_as<8>(a, stream);
 }
 
 cudaError_t launch_moe_combine_backward(const CombineBackwardArgs& a, cudaStream_t stream) {

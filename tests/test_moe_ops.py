@@ -365,7 +365,7 @@ def _routed(rows, top_k, E, seed, dropped=0.2):
     return row, g.random((rows, top_k)).astype(np.float32)
 
 
-SHAPES = [(1, 1, 8), (1, 8, 7168), (6, 1, 520), (7, 3, 264), (5, 4, 2048), (600, 5, 512), (3, 2, 136), (50, 8, 2048), (17, 13, 4104), (9, 64, 256), (2, 4, 20000)]
+SHAPES = [(1, 1, 8), (1, 8, 7168), (6, 1, 520), (9, 1, 4096), (3, 1, 2056), (7, 3, 264), (5, 4, 2048), (600, 5, 512), (3, 2, 136), (50, 8, 2048), (17, 13, 4104), (9, 64, 256), (2, 4, 20000)]
 
 
 @pytest.mark.parametrize("weighted", [False, True])
