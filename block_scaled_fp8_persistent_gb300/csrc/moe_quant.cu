@@ -301,7 +301,8 @@ cudaError_t quantize_as(const QuantizeArgs& a, cudaStream_t stream) {
                                         : quantize_kernel<FMT, XT, true, false>)
                           : (g.side > 1 ? quantize_kernel<FMT, XT, false, true>
                                         : quantize_kernel<FMT, XT, false, false>);
-  const bool early = starts_early(g.grid);
+  const int each = 16 * ((XT == E_FP32 ? 4 : 2) + a.top_k);  // bytes a thread moves
+  const bool early = starts_early(g.grid, (int64_t)g.threads * each);
   return launch(kernel, g.grid, g.threads, 0, early, stream, 1, a, g.side, early);
 }
 
@@ -317,19 +318,18 @@ cudaError_t quantize_format(int x_type, const QuantizeArgs& a, cudaStream_t stre
 template <int FMT, bool Q, int RT, bool WIDE>
 cudaError_t norm_as(const NormArgs& a, cudaStream_t stream) {
   const int items = a.K / 16;
-  const unsigned rows = (unsigned)a.rows;
-  const auto go = [&](void (*kernel)(NormArgs, bool), unsigned blocks, int threads) {
-    const bool early = starts_early(blocks);
+  const int64_t row_bytes = (int64_t)a.K * (RT == E_FP32 ? 11 : 7);  // x, residual twice, q
+  const auto go = [&](void (*kernel)(NormArgs, bool), int side, int threads) {
+    const unsigned blocks = (unsigned)((a.rows + side - 1) / side);
+    const bool early = starts_early(blocks, side * row_bytes);
     return launch(kernel, blocks, (threads + 31) / 32 * 32, 0, early, stream, 1, a, early);
   };
-  if (items <= 8)
-    return go(rmsnorm_kernel<FMT, Q, RT, 1, WIDE, 8, 256, 8>, (unsigned)((a.rows + 31) / 32), 256);
-  if (items <= 32)
-    return go(rmsnorm_kernel<FMT, Q, RT, 1, WIDE, 32, 256, 8>, (unsigned)((a.rows + 7) / 8), 256);
+  if (items <= 8) return go(rmsnorm_kernel<FMT, Q, RT, 1, WIDE, 8, 256, 8>, 32, 256);
+  if (items <= 32) return go(rmsnorm_kernel<FMT, Q, RT, 1, WIDE, 32, 256, 8>, 8, 256);
   if (items <= 512)
-    return go(rmsnorm_kernel<FMT, Q, RT, 1, WIDE, 0, 512, RT == E_FP32 ? 3 : 4>, rows, items);
-  if (items <= 1024) return go(rmsnorm_kernel<FMT, Q, RT, 1, WIDE, 0, 1024, 2>, rows, items);
-  return go(rmsnorm_kernel<FMT, Q, RT, 2, WIDE, 0, 1024, 1>, rows, (items + 1) / 2);
+    return go(rmsnorm_kernel<FMT, Q, RT, 1, WIDE, 0, 512, RT == E_FP32 ? 3 : 4>, 1, items);
+  if (items <= 1024) return go(rmsnorm_kernel<FMT, Q, RT, 1, WIDE, 0, 1024, 2>, 1, items);
+  return go(rmsnorm_kernel<FMT, Q, RT, 2, WIDE, 0, 1024, 1>, 1, (items + 1) / 2);
 }
 
 template <int FMT, bool Q>
@@ -343,7 +343,7 @@ cudaError_t norm_format(int residual_type, const NormArgs& a, cudaStream_t strea
 template <int FMT>
 cudaError_t swiglu_format(const SwigluArgs& a, cudaStream_t stream) {
   const PieceGrid g(a.rows, a.N, kPieceThreads);
-  const bool early = starts_early(g.grid);
+  const bool early = starts_early(g.grid, (int64_t)g.threads * 16 * 5);
   return launch(g.side > 1 ? swiglu_kernel<FMT, true> : swiglu_kernel<FMT, false>, g.grid,
                 g.threads, 0, early, stream, 1, a, g.side, early);
 }

@@ -471,7 +471,8 @@ cudaError_t combine_as(const CombineArgs& a, cudaStream_t stream) {
   const int parts = (pieces + kMost - 1) / kMost;    // blocks to a row
   const int threads = ((pieces + parts - 1) / parts + 31) / 32 * 32;
   const dim3 grid((unsigned)a.rows, (unsigned)parts);
-  const bool early = starts_early(grid);
+  const bool early =
+      starts_early(grid, (int64_t)threads * kVecs * 16 * (a.top_k + 1 + (a.residual ? 1 : 0)));
   return launch(combine_kernel<SLOTS>, grid, threads, 0, early, stream, 1, a, early);
 }
 
@@ -488,7 +489,7 @@ cudaError_t launch_moe_combine_backward(const CombineBackwardArgs& a, cudaStream
   const auto kernel = a.top_k <= 2   ? combine_backward_kernel<2>
                       : a.top_k <= 4 ? combine_backward_kernel<4>
                                      : combine_backward_kernel<8>;
-  const bool early = starts_early((unsigned)a.rows);
+  const bool early = starts_early((unsigned)a.rows, (int64_t)a.N * 2 * (2 * a.top_k + 1));
   return launch(kernel, (unsigned)a.rows, threads, 0, early, stream, 1, a, early);
 }
 
