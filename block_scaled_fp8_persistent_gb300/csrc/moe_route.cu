@@ -21,8 +21,8 @@ namespace {
 // 512 slots 2.4; 1024 would take 3.3 / 3.7); a cluster of eight, whose blocks read each other's
 // counts from shared memory, up to kSortCluster (1024 slots 2.8 / 3.1 us, 4096 slots 3.5 / 3.8,
 // 16384 slots 5.4 / 6.2; 65536 would take 11.1 / 12.4); above that many blocks and two launches,
-// the second started before the first ends (8192 would take 6.0 / 8.4, 65536 slots 6.2 / 8.7,
-// 524288 slots 8.8 / 11.6).
+// the second started before the first ends (8192 would take 5.8 / 8.1, 65536 slots 5.9 / 8.3,
+// 524288 slots 9.2 / 12.0; back to back in a graph).
 // ---------------------------------------------------------------------------------------
 constexpr int kSortThreads = 1024;
 constexpr int kSortMaxChunks = 128;
@@ -62,8 +62,9 @@ __device__ __forceinline__ int key_of(int id, int experts) {
 __global__ void __launch_bounds__(kSortThreads) sort_count_kernel(SortArgs a, int64_t chunk) {
   extern __shared__ int hist[];
   const int keys = a.experts + 1;
-  // The place kernel reads the ids before its own wait.  This kernel does not start early, so
-  // whatever wrote them has completed.
+  // In this order: the place kernel reads the ids before its own wait, so whatever wrote them has
+  // to be complete before it may start.
+  wait_for_previous();
   launch_dependents();
   for (int e = threadIdx.x; e < keys; e += blockDim.x) hist[e] = 0;
   __syncthreads();
@@ -457,7 +458,7 @@ cudaError_t launch_moe_sort(const SortArgs& a, cudaStream_t stream) {
   const cudaError_t e = allow(reinterpret_cast<const void*>(sort_place_kernel));
   if (e != cudaSuccess) return e;
   const int chunks = (int)((a.slots + chunk - 1) / chunk);
-  const cudaError_t c = launch(sort_count_kernel, chunks, kSortThreads, keys * sizeof(int), false,
+  const cudaError_t c = launch(sort_count_kernel, chunks, kSortThreads, keys * sizeof(int), true,
                                stream, 1, a, chunk);
   if (c != cudaSuccess) return c;
   // its own histograms are cleared and filled while the counts are still being made
