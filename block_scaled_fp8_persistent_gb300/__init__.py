@@ -10,6 +10,12 @@ not a GB300 (compute capability 10.3) the calls raise.
     bsfp8.bsmxfp8_grouped_gemm(...)   # MXFP8: UE8M0 scales per 32 K
     bsfp8.bsmx_grouped_gemm("mxfp8", "mxfp4", ...)   # a format per operand
 
+and the operators around it, which go through the compiled module csrc/binding.cpp (checks of
+device, layout, type and size of every tensor, then the C entry point):
+
+    bsfp8.bsmx_rmsnorm_quant(...), bsfp8.bsmx_moe_sort(...), bsfp8.bsmx_quantize(...),
+    bsfp8.bsmx_swiglu_quant(...), bsfp8.bsmx_moe_combine(...), bsfp8.bsmx_moe_combine_backward(...)
+
 Tensors are torch CUDA tensors (or raw device addresses as ints) in the layouts of
 include/bsfp8.h; ``stream`` is a torch.cuda.Stream, a raw cudaStream_t int, or None for
 torch's current stream.

@@ -294,9 +294,9 @@ bsfp8_status bsmx_grouped_gemm(int a_format, int b_format, const void* A, const 
  * and each element is value / scale rounded to the nearest code, ties to even, saturating
  * (BLOCKWISE multiplies by the scale's fp32 reciprocal, NVFP4 divides, MX is exact).  A block
  * of zeros has scale 1; a block that holds a NaN or an infinity has a NaN scale (UE8M0 0xFF,
- * e4m3 0x7F, fp32 NaN), so that what is computed of it is NaN.  q is 16-byte aligned; K and N
- * are multiples of 128, at most 2^24; inputs are 16-byte aligned.  Outputs overlap inputs only
- * where that is said.  BSFP8_ERR_FORMAT for a format or type that is not listed.
+ * e4m3 0x7F, fp32 NaN), so that what is computed of it is NaN.  q is 16-byte aligned, BLOCKWISE
+ * scales 4-byte (the GEMM wants that of all scales); K and N are multiples of 128, at most 2^24;
+ * inputs are 16-byte aligned.  Outputs overlap inputs only where that is said.  BSFP8_ERR_FORMAT for a format or type that is not listed.
  */
 
 /*
@@ -306,7 +306,8 @@ bsfp8_status bsmx_grouped_gemm(int a_format, int b_format, const void* A, const 
  *   row_of_slot       int32 [rows, top_k] (bsmx_moe_sort): row t of x, quantised once, is
  *                     written to each row row_of_slot[t, j] of q.  Negative entries are
  *                     skipped; an entry >= out_rows is skipped and recorded as
- *                     BSFP8_ERR_DEVICE_ROWS.  Rows that no slot names are left as they are.
+ *                     BSFP8_ERR_DEVICE_ROWS.  Rows that no slot names are left as they are; no
+ *                     row is to be named twice.
  * The gradient of the mapped form (straight through the rounding) is bsmx_moe_combine of the
  * gradient of q's rows without weights.
  */
