@@ -21,8 +21,8 @@ namespace {
 // 512 slots 2.4; 1024 would take 3.3 / 3.7); a cluster of eight, whose blocks read each other's
 // counts from shared memory, up to kSortCluster (1024 slots 2.8 / 3.1 us, 4096 slots 3.5 / 3.8,
 // 16384 slots 5.4 / 6.2; 65536 would take 11.1 / 12.4); above that many blocks and two launches,
-// the second started before the first ends (8192 would take 5.8 / 8.1, 65536 slots 5.9 / 8.3,
-// 524288 slots 9.2 / 12.0; back to back in a graph).
+// the second started before the first ends (8192 would take 5.5 / 7.0, 65536 slots 5.7 / 7.4,
+// 524288 slots 9.1 / 11.4; back to back in a graph).
 // ---------------------------------------------------------------------------------------
 constexpr int kSortThreads = 1024;
 constexpr int kSortMaxChunks = 128;
@@ -144,8 +144,10 @@ __device__ __forceinline__ void place_segment(const SortArgs& a, int64_t lo, int
   }
 }
 
-// Rows of one chunk's slots, from the counts of every chunk (at most kSortMaxChunks): one warp
-// per key reads and adds up both those and its own warps' side by side.
+// Rows of one chunk's slots, from the counts of every chunk (at most 32 * LOADS), which one warp
+// per key reads side by side.  What needs the block's own slots only is done before the counts are
+// waited for.
+template <int LOADS>
 __global__ void __launch_bounds__(kSortThreads) sort_place_kernel(SortArgs a, int64_t chunk,
                                                                   int warps) {
   extern __shared__ int hist[];  // [warps][pitch], then [keys] first rows and [keys] totals
@@ -165,36 +167,30 @@ __global__ void __launch_bounds__(kSortThreads) sort_place_kernel(SortArgs a, in
   for (int64_t s = lo + lane; s < hi; s += 32)
     atomicAdd(&hist[warp * pitch + key_of(a.ids[s], a.experts)], 1);
   __syncthreads();
-  wait_for_previous();  // the chunks' counts; nothing is written before
+  for (int e = threadIdx.x; e < keys; e += blockDim.x) prefix_over_warps(hist + e, warps, pitch);
+  wait_for_previous();  // the chunks' counts; nothing is written to memory before
   launch_dependents();
 
   const int chunks = gridDim.x;
   constexpr int kKeys = 4;  // keys whose counts a warp has in flight
   for (int e0 = warp; e0 < keys; e0 += kKeys * (blockDim.x / 32)) {
-    int c[kKeys][kSortMaxChunks / 32] = {};
+    int c[kKeys][LOADS];
 #pragma unroll
     for (int n = 0; n < kKeys; ++n) {
       const int e = e0 + n * (blockDim.x / 32);
 #pragma unroll
-      for (int i = 0; i < kSortMaxChunks / 32; ++i)
-        if (e < keys && i * 32 + lane < chunks)
-          c[n][i] = a.workspace[(int64_t)e * chunks + i * 32 + lane];
+      for (int i = 0; i < LOADS; ++i)
+        c[n][i] = e < keys && i * 32 + lane < chunks
+                      ? a.workspace[(int64_t)e * chunks + i * 32 + lane]
+                      : 0;
     }
 #pragma unroll
     for (int n = 0; n < kKeys; ++n) {
       const int e = e0 + n * (blockDim.x / 32);
       if (e >= keys) break;
-      const int mine = lane < warps ? hist[lane * pitch + e] : 0;
-      int inc = mine;
-#pragma unroll
-      for (int d = 1; d < 32; d *= 2) {
-        const int o = __shfl_up_sync(0xffffffffu, inc, d);
-        if (lane >= d) inc += o;
-      }
-      if (lane < warps) hist[lane * pitch + e] = inc - mine;
       int all = 0, before = 0;
 #pragma unroll
-      for (int i = 0; i < kSortMaxChunks / 32; ++i) {
+      for (int i = 0; i < LOADS; ++i) {
         all += c[n][i];
         before += i * 32 + lane < (int)blockIdx.x ? c[n][i] : 0;
       }
@@ -455,14 +451,15 @@ cudaError_t launch_moe_sort(const SortArgs& a, cudaStream_t stream) {
     if (e != cudaSuccess) return e;
     return launch(sort_cluster_kernel, blocks, threads, smem, true, stream, blocks, a, chunk, warps);
   }
-  const cudaError_t e = allow(reinterpret_cast<const void*>(sort_place_kernel));
-  if (e != cudaSuccess) return e;
   const int chunks = (int)((a.slots + chunk - 1) / chunk);
+  const auto place = chunks <= 64 ? sort_place_kernel<2> : sort_place_kernel<kSortMaxChunks / 32>;
+  const cudaError_t e = allow(reinterpret_cast<const void*>(place));
+  if (e != cudaSuccess) return e;
   const cudaError_t c = launch(sort_count_kernel, chunks, kSortThreads, keys * sizeof(int), true,
                                stream, 1, a, chunk);
   if (c != cudaSuccess) return c;
   // its own histograms are cleared and filled while the counts are still being made
-  return launch(sort_place_kernel, chunks, threads, smem, true, stream, 1, a, chunk, warps);
+  return launch(place, chunks, threads, smem, true, stream, 1, a, chunk, warps);
 }
 
 template <int SLOTS>
