@@ -457,6 +457,24 @@ def test_combine_backward_against_differences():
     assert abs(want - exact) <= HALF_BF16 * float(w[t, j]) * float((d[t].double() * delta).abs().sum())
 
 
+def test_combine_backward_of_rows_against_differences():
+    # weights that are powers of two leave w * C, one row at a time, unrounded: the change of
+    # <d_out, out> as a row goes from 0 to a change is exact, and so is dC
+    rows, top_k, N = 5, 2, 256
+    row = torch.arange(rows * top_k, dtype=torch.int32, device="cuda").flip(0).contiguous()
+    w = torch.tensor([0.5, 2.0], device="cuda").repeat(rows, 1)
+    d = _rand((rows, N), torch.bfloat16, seed=2, spread=0.5).cuda()
+    change = _rand((rows * top_k, N), torch.bfloat16, seed=3, spread=0.5).cuda()
+    dC, dw = torch.zeros_like(change), torch.empty(rows, top_k, device="cuda")
+    bsfp8.bsmx_moe_combine_backward(d, change, row, w, dC, dw, rows, rows * top_k, top_k, N)
+    for r in range(rows * top_k):
+        C, out = torch.zeros_like(change), torch.empty_like(d)
+        C[r] = change[r]
+        bsfp8.bsmx_moe_combine(C, row, out, rows, rows * top_k, top_k, N, weights=w)
+        moved = (d.double() * out.double()).sum()
+        assert moved == (dC[r].double() * change[r].double()).sum()
+
+
 def test_dispatch_gradient_is_the_unweighted_combine():
     rows, top_k, K = 30, 4, 384
     row, _ = _routed(rows, top_k, 8, seed=3)
