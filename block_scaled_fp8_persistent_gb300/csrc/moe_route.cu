@@ -1,6 +1,8 @@
 // Tokens sorted by expert, and the way back: the stable counting sort that gives every slot
 // (token t's j-th choice, slot t * top_k + j) its row in the grouped GEMM's operand, the
 // weighted sum of a token's rows, and that sum's gradient.
+#include <atomic>
+
 #include "moe_ops.cuh"
 #include "ptx.cuh"
 #include "quant.cuh"
@@ -423,6 +425,27 @@ __global__ void __launch_bounds__(256, SLOTS == 8 ? 3 : SLOTS == 4 ? 4 : 6)
   }
 }
 
+// Once per device the kernels are allowed the most that any sort asks for.  What a launch may
+// use belongs to the kernel, not to the call: several host threads may sort at once, and no call
+// may take away what another is about to launch with.
+cudaError_t allow_sort_smem() {
+  constexpr size_t kMost = (kSortSmemWords + 2 * (kSortMaxExperts + 1)) * sizeof(int);
+  static_assert(kMost + 1024 <= 227 * 1024, "shared memory per block");
+  static std::atomic<bool> done[64];
+  int dev = 0;
+  cudaGetDevice(&dev);
+  if (dev < 64 && done[dev].load(std::memory_order_acquire)) return cudaSuccess;
+  for (const void* kernel : {reinterpret_cast<const void*>(sort_cluster_kernel),
+                             reinterpret_cast<const void*>(sort_place_kernel<2>),
+                             reinterpret_cast<const void*>(sort_place_kernel<kSortMaxChunks / 32>)}) {
+    const cudaError_t e =
+        cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kMost);
+    if (e != cudaSuccess) return e;
+  }
+  if (dev < 64) done[dev].store(true, std::memory_order_release);
+  return cudaSuccess;
+}
+
 }  // namespace
 
 int64_t moe_sort_workspace_bytes(int64_t slots, int experts) {
@@ -441,20 +464,14 @@ cudaError_t launch_moe_sort(const SortArgs& a, cudaStream_t stream) {
   threads = threads < warps * 32 ? warps * 32 : threads;
   threads = threads < kSortThreads ? threads : kSortThreads;
   const size_t smem = ((size_t)warps * sort_pitch(a.experts) + 2 * keys) * sizeof(int);
-  const auto allow = [&](const void* kernel) {
-    return smem <= 48 * 1024 ? cudaSuccess
-                             : cudaFuncSetAttribute(
-                                   kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
-  };
-  if (blocks) {
-    const cudaError_t e = allow(reinterpret_cast<const void*>(sort_cluster_kernel));
+  if (smem > 48 * 1024) {
+    const cudaError_t e = allow_sort_smem();
     if (e != cudaSuccess) return e;
-    return launch(sort_cluster_kernel, blocks, threads, smem, true, stream, blocks, a, chunk, warps);
   }
+  if (blocks)
+    return launch(sort_cluster_kernel, blocks, threads, smem, true, stream, blocks, a, chunk, warps);
   const int chunks = (int)((a.slots + chunk - 1) / chunk);
   const auto place = chunks <= 64 ? sort_place_kernel<2> : sort_place_kernel<kSortMaxChunks / 32>;
-  const cudaError_t e = allow(reinterpret_cast<const void*>(place));
-  if (e != cudaSuccess) return e;
   const cudaError_t c = launch(sort_count_kernel, chunks, kSortThreads, keys * sizeof(int), true,
                                stream, 1, a, chunk);
   if (c != cudaSuccess) return c;

@@ -11,6 +11,8 @@ Tolerances, each from the arithmetic and set before the first run (2^-24 = one f
   combine         (top_k + 1) * 2^-24 of the sum of magnitudes and half a bf16 ulp
   its gradient    d_weights: 8 terms per 2048 columns in a thread, 5 shuffles, 8 warps, doubled
 """
+import threading
+
 import numpy as np
 import pytest
 import torch
@@ -352,6 +354,54 @@ def test_sort_extremes(rows, kind):
     got = _sort(ids, E, with_slot=kind != "one")
     for a, b in zip(got, ref.sort_slots(ids, E)):
         assert a is None or np.array_equal(a, b)
+
+
+def test_sorts_of_different_sizes_on_two_threads():
+    # 512 and 4096 experts want 68 and 160 KB of shared memory: what one call asks for must not
+    # take away what the other is about to launch with.  The C entry point directly, which runs
+    # without the interpreter lock.
+    lib = bsfp8.load_library()
+    rows, top_k, steps = 2048, 8, 3000
+    n = rows * top_k
+    ids = np.random.default_rng(5).integers(0, 512, size=(rows, top_k)).astype(np.int32)
+    d = torch.from_numpy(ids).cuda()
+    torch.cuda.synchronize()
+    refused, rows_of = {}, {}
+
+    def sort(E):
+        off = torch.empty(E + 2, dtype=torch.int32, device="cuda")
+        rows_of[E] = torch.empty(n, dtype=torch.int32, device="cuda")
+        stream = torch.cuda.Stream()
+        args = (d.data_ptr(), off.data_ptr(), rows_of[E].data_ptr(), None, None, 0, rows, top_k, E, stream.cuda_stream)
+        refused[E] = sum(lib.bsmx_moe_sort(*args) != 0 for _ in range(steps))
+        stream.synchronize()
+
+    threads = [threading.Thread(target=sort, args=(E,)) for E in (512, 4096)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert refused == {512: 0, 4096: 0}
+    for E in (512, 4096):
+        assert np.array_equal(rows_of[E].cpu().numpy(), ref.sort_slots(ids, E)[1])
+
+
+def test_a_captured_sort_replays_after_a_smaller_one():
+    rows, top_k, E = 2048, 8, 4096
+    n = rows * top_k
+    ids = np.random.default_rng(6).integers(-1, E, size=(rows, top_k)).astype(np.int32)
+    d = torch.from_numpy(ids).cuda()
+    off, row = torch.empty(E + 2, dtype=torch.int32, device="cuda"), torch.empty(n, dtype=torch.int32, device="cuda")
+    bsfp8.bsmx_moe_sort(d, off, row, None, rows, top_k, E)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        bsfp8.bsmx_moe_sort(d, off, row, None, rows, top_k, E)
+    _sort(ids, 512)
+    off.fill_(-7)
+    row.fill_(-7)
+    graph.replay()
+    want = ref.sort_slots(ids, E)
+    assert np.array_equal(off.cpu().numpy(), want[0]) and np.array_equal(row.cpu().numpy(), want[1])
 
 
 # ------------------------------------------------------------------- combine and gradient
