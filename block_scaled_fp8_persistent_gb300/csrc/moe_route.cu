@@ -23,7 +23,7 @@ namespace {
 // 512 slots 2.4; 1024 would take 3.3 / 3.7); a cluster of eight, whose blocks read each other's
 // counts from shared memory, up to kSortCluster (1024 slots 2.8 / 3.1 us, 4096 slots 3.5 / 3.8,
 // 16384 slots 5.4 / 6.2; 65536 would take 11.1 / 12.4); above that many blocks and two launches,
-// the second started before the first ends (8192 would take 5.5 / 7.0, 65536 slots 5.7 / 7.4,
+// the second started before the first ends (8192 would take 5.5 / 7.0, 65536 slots 5.9 / 7.7,
 // 524288 slots 9.1 / 11.4; back to back in a graph).
 // ---------------------------------------------------------------------------------------
 constexpr int kSortThreads = 1024;
@@ -64,10 +64,7 @@ __device__ __forceinline__ int key_of(int id, int experts) {
 __global__ void __launch_bounds__(kSortThreads) sort_count_kernel(SortArgs a, int64_t chunk) {
   extern __shared__ int hist[];
   const int keys = a.experts + 1;
-  // In this order: the place kernel reads the ids before its own wait, so whatever wrote them has
-  // to be complete before it may start.
-  wait_for_previous();
-  launch_dependents();
+  begin_early(true);
   for (int e = threadIdx.x; e < keys; e += blockDim.x) hist[e] = 0;
   __syncthreads();
   const int64_t begin = blockIdx.x * chunk;
@@ -147,8 +144,8 @@ __device__ __forceinline__ void place_segment(const SortArgs& a, int64_t lo, int
 }
 
 // Rows of one chunk's slots, from the counts of every chunk (at most 32 * LOADS), which one warp
-// per key reads side by side.  What needs the block's own slots only is done before the counts are
-// waited for.
+// per key reads side by side.  The ids are read after the wait too, although the counting kernel
+// has waited for whoever wrote them: what a kernel wrote is visible to those that wait.
 template <int LOADS>
 __global__ void __launch_bounds__(kSortThreads) sort_place_kernel(SortArgs a, int64_t chunk,
                                                                   int warps) {
@@ -166,12 +163,11 @@ __global__ void __launch_bounds__(kSortThreads) sort_place_kernel(SortArgs a, in
 
   for (int e = threadIdx.x; e < warps * pitch; e += blockDim.x) hist[e] = 0;
   __syncthreads();
+  begin_early(true);
   for (int64_t s = lo + lane; s < hi; s += 32)
     atomicAdd(&hist[warp * pitch + key_of(a.ids[s], a.experts)], 1);
   __syncthreads();
   for (int e = threadIdx.x; e < keys; e += blockDim.x) prefix_over_warps(hist + e, warps, pitch);
-  wait_for_previous();  // the chunks' counts; nothing is written to memory before
-  launch_dependents();
 
   const int chunks = gridDim.x;
   constexpr int kKeys = 4;  // keys whose counts a warp has in flight
@@ -475,7 +471,7 @@ cudaError_t launch_moe_sort(const SortArgs& a, cudaStream_t stream) {
   const cudaError_t c = launch(sort_count_kernel, chunks, kSortThreads, keys * sizeof(int), true,
                                stream, 1, a, chunk);
   if (c != cudaSuccess) return c;
-  // its own histograms are cleared and filled while the counts are still being made
+  // starts, and clears its histograms, while the counts are still being made
   return launch(place, chunks, threads, smem, true, stream, 1, a, chunk, warps);
 }
 

@@ -404,6 +404,22 @@ def test_a_captured_sort_replays_after_a_smaller_one():
     assert np.array_equal(off.cpu().numpy(), want[0]) and np.array_equal(row.cpu().numpy(), want[1])
 
 
+@pytest.mark.parametrize("rows,top_k", [(300, 2), (1500, 4), (2500, 8), (16500, 8)])
+def test_chained_sorts(rows, top_k):
+    # each sort's ids are the rows that the one before it writes, nothing in between
+    E, steps, n = 4096, 6, rows * top_k
+    ids = np.random.default_rng(rows).integers(0, E, size=n).astype(np.int32)
+    bufs = [torch.from_numpy(ids).cuda()] + [torch.empty(n, dtype=torch.int32, device="cuda") for _ in range(steps)]
+    off = torch.empty(steps, E + 2, dtype=torch.int32, device="cuda")
+    ws = torch.empty(max(4, bsfp8.bsmx_moe_sort_workspace(rows, top_k, E)), dtype=torch.uint8, device="cuda")
+    torch.cuda.synchronize()
+    for i in range(steps):
+        bsfp8.bsmx_moe_sort(bufs[i], off[i], bufs[i + 1], ws, rows, top_k, E)
+    for i in range(steps):
+        want_off, ids, _ = ref.sort_slots(ids, E)
+        assert np.array_equal(off[i].cpu().numpy(), want_off) and np.array_equal(bufs[i + 1].cpu().numpy(), ids)
+
+
 # ------------------------------------------------------------------- combine and gradient
 def _routed(rows, top_k, E, seed, dropped=0.2):
     g = np.random.default_rng(seed)

@@ -1,5 +1,8 @@
 """The operators around the grouped GEMM on the host: arguments that are refused before any GPU
 work, the sort's workspace, and the 64-bit definitions the GPU tests compare with."""
+import os
+import re
+
 import numpy as np
 import pytest
 import torch
@@ -146,6 +149,24 @@ def test_binding_refuses_host_and_raw_arguments():
     with pytest.raises(bsfp8.BsFp8Error) as e:
         bsfp8.bsmx_quantize("mxfp8", FAKE, FAKE, FAKE, 2, 100, x_type="bf16", stream=0)
     assert e.value.status == SHAPE
+
+
+def test_kernels_wait_before_they_touch_what_others_wrote():
+    # a kernel that starts before the one before it has ended may touch its arguments' memory
+    # only after its own wait
+    csrc = os.path.join(os.path.dirname(bsfp8.__file__), "csrc")
+    kernels = 0
+    for name in ("moe_route.cu", "moe_quant.cu"):
+        text = re.sub(r"//[^\n]*", "", open(os.path.join(csrc, name)).read())
+        for head in re.finditer(r"__global__ void[^;{]*?(\w+_kernel)\((\w+Args) a\b[^{]*\{", text):
+            body = text[head.end():]
+            body = body[:body.index("\n}\n")]
+            waits = [m.start() for m in re.finditer(r"begin_early\(|wait_for_previous\(|quantise_piece<", body)]
+            fields = r"\ba\.(ids|offsets|row_of_slot|slot_of_row|workspace|C|weights?|residual\w*|out|d_\w+|dC|x|h|y|q|scales)\b"
+            first = re.search(fields + r"|\bplace_segment\(|\bchecked_row\(", body)
+            assert waits and waits[0] < first.start(), head.group(1)
+            kernels += 1
+    assert kernels == 8
 
 
 # ------------------------------------------------------------------- the 64-bit definitions
