@@ -329,8 +329,8 @@ def bsmx_moe_combine(C, row_of_slot, out, rows: int, in_rows: int, top_k: int, N
 def bsmx_moe_combine_backward(d_out, C, row_of_slot, weights, dC, d_weights, rows: int,
                               in_rows: int, top_k: int, N: int, stream=None) -> None:
     """Gradient of bsmx_moe_combine: dC[row_of_slot[t, j]] = weights[t, j] * d_out[t] and
-    d_weights[t, j] = <d_out[t], C[row_of_slot[t, j]]>.  See include/bsfp8.h.  Raises
-    BsFp8Error."""
+    d_weights[t, j] = <d_out[t], C[row_of_slot[t, j]]>, for row maps that name no row twice (as
+    bsmx_moe_sort's).  See include/bsfp8.h.  Raises BsFp8Error."""
     st = (_binding or load_binding()).moe_combine_backward(
         d_out, C, row_of_slot, weights, dC, d_weights, rows, in_rows, top_k, N, stream)
     if st:

@@ -378,8 +378,11 @@ bsfp8_status bsmx_moe_combine(const void* C, const int32_t* row_of_slot, const f
  * Its gradient, d_out bf16 [rows, N] being that of out (and of the residual):
  *   dC[row_of_slot[t, j]] = bf16( weights[t, j] * d_out[t] )
  *   d_weights[t, j]       = sum_n d_out[t, n] * C[row_of_slot[t, j], n]      fp32
- * d_weights is 0 for dropped slots; rows of dC that no slot names are left as they are.  dC may
- * not overlap C or d_out.  The same result every time: each sum has one order.
+ * d_weights is 0 for dropped slots; rows of dC that no slot names are left as they are.  No row
+ * is to be named twice, as in the maps of bsmx_moe_sort: each slot stores its row of dC whole, so
+ * of two slots with the same row one would be lost, and which one is not defined (the forward sum
+ * takes such maps).  dC may not overlap C or d_out.  With distinct rows the result is the same
+ * every time: each sum has one order.
  */
 bsfp8_status bsmx_moe_combine_backward(const void* d_out, const void* C,
                                        const int32_t* row_of_slot, const float* weights, void* dC,

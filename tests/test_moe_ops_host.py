@@ -169,6 +169,21 @@ def test_kernels_wait_before_they_touch_what_others_wrote():
     assert kernels == 8
 
 
+def test_operators_that_store_by_row_say_that_rows_are_distinct():
+    # the mapped quantisation and the combine's gradient write each named row whole
+    header = open(os.path.join(libbuild.INCLUDE, "bsfp8.h")).read()
+    flat = re.sub(r"\s*\n \* *", " ", header)
+    for name in ("bsmx_quantize", "bsmx_moe_combine_backward"):
+        comment = flat[: flat.index(f"bsfp8_status {name}(")].rsplit("/*", 1)[1]
+        assert re.search("[Nn]o row is to be named twice", comment), name
+
+
+def test_sorted_slots_have_distinct_rows():
+    ids = np.random.default_rng(2).integers(-1, 9, size=(40, 5))
+    row = ref.sort_slots(ids, 8)[1]
+    assert len(np.unique(row[row >= 0])) == (row >= 0).sum()
+
+
 # ------------------------------------------------------------------- the 64-bit definitions
 def test_nearest_against_torch_float8():
     v = np.concatenate([np.linspace(-460, 460, 4001), np.linspace(-0.02, 0.02, 4001)])
