@@ -138,9 +138,25 @@ def _addr(x) -> int | None:
     return x.data_ptr() or None
 
 
+_current_stream = None
+
+
+def _find_current_stream():
+    """The query of torch's current stream: the binding's, which takes 0.1 us where torch's own
+    takes 3, or torch's where there is none for the torch that is installed (the GEMMs need the
+    library only).  Settled at the first call."""
+    global _current_stream
+    try:
+        _current_stream = load_binding().current_stream
+    except ImportError:
+        import torch
+        _current_stream = lambda: torch.cuda.current_stream().cuda_stream  # noqa: E731
+    return _current_stream
+
+
 def _stream(stream) -> int | None:
     if stream is None:
-        return (_binding or load_binding()).current_stream() or None
+        return (_current_stream or _find_current_stream())() or None
     if isinstance(stream, int):
         return stream or None
     return stream.cuda_stream or None

@@ -168,3 +168,21 @@ def test_nvfp4_host_rules(lib):
     assert _call_fmt(lib, 2, 2, sb=FAKE + 4) == 3
     assert _call_fmt(lib, 2, 2, N=192) == 2
     assert _call_fmt(lib, 2, 2, B=None) == 1
+
+
+def test_streams_without_the_compiled_binding(monkeypatch, lib):
+    # a GEMM on torch's current stream needs the library only
+    import types
+
+    import torch
+    monkeypatch.setattr(libbuild, "binding_path", lambda: "/nowhere/bsfp8_binding.so")
+    monkeypatch.setattr(bsfp8, "_binding", None)
+    monkeypatch.setattr(bsfp8, "_current_stream", None, raising=False)
+    monkeypatch.setattr(torch.cuda, "current_stream", lambda: types.SimpleNamespace(cuda_stream=1 << 12))
+    for _ in range(2):
+        assert bsfp8._stream(None) == 1 << 12
+    with pytest.raises(bsfp8.BsFp8Error) as e:  # reaches the library's own checks
+        bsfp8.bsfp8_grouped_gemm(None, None, None, None, None, None, 1, 128, 128, 1)
+    assert e.value.status == 1
+    with pytest.raises(ImportError):  # the operators around it say what is missing
+        bsfp8.bsmx_swiglu_quant("mxfp8", None, None, None, 0, 128)
