@@ -9,7 +9,9 @@ build(debug=True) makes lib/libbsfp8_debug.so instead: the same sources with
 record BSFP8_ERR_DEVICE_BOUNDS in the device error word instead of going out of range.
 
 Both also make lib/bsfp8_binding_<torch version>.so (csrc/binding.cpp, host code only): the
-Python side of the operators around the GEMM, compiled against the torch that is installed.
+Python side of the operators around the GEMM, compiled against the torch that is installed.  The
+library does not depend on it: where it cannot be built (no torch, no C++ compiler) there is a
+warning, and only the Python calls of those operators are missing.
 """
 from __future__ import annotations
 
@@ -17,6 +19,7 @@ import os
 import subprocess
 import sys
 import sysconfig
+import warnings
 from concurrent.futures import ThreadPoolExecutor
 
 PKG = os.path.dirname(os.path.abspath(__file__))
@@ -53,6 +56,7 @@ def binding_path() -> str:
 
 
 def build_binding(force: bool = False) -> str:
+    """Builds the compiled binding (raises if that fails)."""
     out = binding_path()
     if not force and up_to_date(out):
         return out
@@ -75,6 +79,13 @@ def build_binding(force: bool = False) -> str:
     return out
 
 
+def _try_binding(force: bool = False) -> None:
+    try:
+        build_binding(force)
+    except Exception as e:  # whatever is missing: the library does not need it
+        warnings.warn(f"the compiled binding was not built: {e}", RuntimeWarning, stacklevel=3)
+
+
 def up_to_date(lib: str = LIB) -> bool:
     if not os.path.exists(lib):
         return False
@@ -87,7 +98,7 @@ def build(force: bool = False, verbose: bool = False, ptxas_info: bool = False,
     lib = DEBUG_LIB if debug else LIB
     objdir = OBJDIR + ("_debug" if debug else "")
     if not force and up_to_date(lib):
-        build_binding()
+        _try_binding()
         return lib
     os.makedirs(objdir, exist_ok=True)
     os.makedirs(LIBDIR, exist_ok=True)
@@ -107,7 +118,7 @@ def build(force: bool = False, verbose: bool = False, ptxas_info: bool = False,
         return obj
 
     with ThreadPoolExecutor(max_workers=len(SOURCES) + 1) as ex:
-        binding = ex.submit(build_binding, force)
+        binding = ex.submit(_try_binding, force)
         objs = list(ex.map(compile_one, SOURCES))
         binding.result()
     tmp = lib + f".tmp{os.getpid()}"

@@ -186,3 +186,26 @@ def test_streams_without_the_compiled_binding(monkeypatch, lib):
     assert e.value.status == 1
     with pytest.raises(ImportError):  # the operators around it say what is missing
         bsfp8.bsmx_swiglu_quant("mxfp8", None, None, None, 0, 128)
+
+
+def test_the_library_is_built_without_the_binding(monkeypatch, tmp_path):
+    # no torch: the library that is there is up to date, and one that is not gets linked
+    from importlib.metadata import PackageNotFoundError
+
+    def missing(*_):
+        raise PackageNotFoundError("torch")
+
+    monkeypatch.setattr(libbuild, "binding_path", missing)
+    with pytest.warns(RuntimeWarning, match="binding"):
+        assert libbuild.build() == libbuild.LIB
+    compiler = tmp_path / "nvcc"  # stands for the compiler: makes what -o names
+    compiler.write_text('#!/bin/sh\nwhile [ "$1" != -o ]; do shift; done\n: > "$2"\n')
+    compiler.chmod(0o755)
+    monkeypatch.setattr(libbuild, "_nvcc", lambda: str(compiler))
+    monkeypatch.setattr(libbuild, "OBJDIR", str(tmp_path / "obj"))
+    monkeypatch.setattr(libbuild, "LIBDIR", str(tmp_path))
+    monkeypatch.setattr(libbuild, "LIB", str(tmp_path / "lib.so"))
+    with pytest.warns(RuntimeWarning, match="binding"):
+        assert os.path.exists(libbuild.build(force=True))
+    with pytest.raises(PackageNotFoundError):
+        libbuild.build_binding()
