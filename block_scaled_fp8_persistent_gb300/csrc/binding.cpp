@@ -147,11 +147,30 @@ void check_operand(Args& a, int format, Buffer& q, Buffer& scales, int64_t rows,
     a.check(scales, "scales", rows * (K / (format == BSMX_NVFP4 ? 16 : 32)), 0, 1);
 }
 
+// Gives the interpreter lock away while it lives: a launch may wait for room in the stream's
+// queue, which a host callback that wants the lock may have to make.
+class Unlocked {
+ public:
+  Unlocked() : state_(PyEval_SaveThread()) {}
+  ~Unlocked() { PyEval_RestoreThread(state_); }
+  Unlocked(const Unlocked&) = delete;
+  Unlocked& operator=(const Unlocked&) = delete;
+
+ private:
+  PyThreadState* const state_;
+};
+
 template <typename F>
 PyObject* status(Args& a, F&& call) {
   if (!a.ok()) return nullptr;
   const cudaStream_t stream = a.resolve();
-  return a.ok() ? PyLong_FromLong(call(stream)) : nullptr;
+  if (!a.ok()) return nullptr;
+  bsfp8_status st;
+  {
+    Unlocked unlocked;
+    st = call(stream);
+  }
+  return PyLong_FromLong(st);
 }
 
 // quantize(format, x_type, x, row_of_slot, top_k, q, scales, rows, out_rows, K, stream)

@@ -1,7 +1,14 @@
 """The operators around the grouped GEMM on the host: arguments that are refused before any GPU
 work, the sort's workspace, and the 64-bit definitions the GPU tests compare with."""
+import ctypes
+import importlib.machinery
+import importlib.util
 import os
 import re
+import shutil
+import subprocess
+import threading
+import time
 
 import numpy as np
 import pytest
@@ -182,6 +189,41 @@ def test_sorted_slots_have_distinct_rows():
     ids = np.random.default_rng(2).integers(-1, 9, size=(40, 5))
     row = ref.sort_slots(ids, 8)[1]
     assert len(np.unique(row[row >= 0])) == (row >= 0).sum()
+
+
+STUB = r"""
+#include <unistd.h>
+extern "C" {
+volatile int entered = 0, go_on = 0;
+int wait_for_python(int, const void*, void*, void*, long, int, void*) {
+  entered = 1;
+  for (int i = 0; i < 2000 && !go_on; ++i) usleep(1000);
+  return go_on ? 0 : 5;
+}
+}
+"""
+
+
+def test_calls_run_without_the_interpreter_lock(tmp_path):
+    # an entry point that returns once another Python thread has run, or gives up after 2 s
+    libbuild.build()
+    (tmp_path / "stub.cpp").write_text(STUB)
+    subprocess.run(["g++", "-O1", "-shared", "-fPIC", str(tmp_path / "stub.cpp"), "-o", str(tmp_path / "stub.so")], check=True)
+    stub = ctypes.CDLL(str(tmp_path / "stub.so"))
+    path = shutil.copy(libbuild.binding_path(), tmp_path / "binding.so")  # an instance of its own
+    loader = importlib.machinery.ExtensionFileLoader("bsfp8_binding", str(path))
+    module = importlib.util.module_from_spec(importlib.util.spec_from_file_location("bsfp8_binding", path, loader=loader))
+    loader.exec_module(module)
+    module.bind(*[ctypes.cast(stub.wait_for_python, ctypes.c_void_p).value] * 6)
+    got = []
+    call = threading.Thread(target=lambda: got.append(module.swiglu_quant(0, FAKE, FAKE, FAKE, 1, 128, 0)))
+    call.start()
+    entered, go_on = ctypes.c_int.in_dll(stub, "entered"), ctypes.c_int.in_dll(stub, "go_on")
+    while not entered.value:
+        time.sleep(0.001)
+    go_on.value = 1
+    call.join()
+    assert got == [0]
 
 
 # ------------------------------------------------------------------- the 64-bit definitions
