@@ -280,10 +280,11 @@ def bsmx_quantize(format: str, x, q, scales, rows: int, K: int, row_of_slot=None
                   out_rows: int | None = None, x_type: str | None = None, stream=None) -> None:
     """Quantise x [rows, K] (bf16, fp16 or fp32) into the operand (q, scales) of `format`
     ("mxfp8", "mxfp4", "nvfp4", "blockwise"); with row_of_slot, row t goes to each of the rows
-    row_of_slot[t, :] of an operand of out_rows rows.  See include/bsfp8.h.  Raises BsFp8Error."""
+    row_of_slot[t, :] of an operand of out_rows rows (None: rows * top_k, one for every slot);
+    rows that no slot names are left as they are.  See include/bsfp8.h.  Raises BsFp8Error."""
     st = (_binding or load_binding()).quantize(
         QUANT_FORMATS[format], -1 if x_type is None else TYPES[x_type], x, row_of_slot, top_k, q,
-        scales, rows, rows if out_rows is None else out_rows, K, stream)
+        scales, rows, rows * top_k if out_rows is None else out_rows, K, stream)
     if st:
         raise BsFp8Error(st, "bsmx_quantize")
 

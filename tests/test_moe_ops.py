@@ -169,6 +169,18 @@ def test_quantize_by_row_map(fmt, rows, top_k, E, K):
     _check_guards(fmt, q, s, n, K, 9)
 
 
+def test_row_map_of_every_slot_by_default():
+    rows, top_k, K = 6, 3, 256
+    x = _rand((rows, K), torch.bfloat16, seed=4, spread=0.5).cuda()
+    row = torch.randperm(rows * top_k, generator=torch.Generator().manual_seed(1)).to(torch.int32).cuda()
+    q, s = _operand("mxfp8", rows * top_k, K)
+    bsfp8.bsmx_quantize("mxfp8", x, q, s, rows, K, row_of_slot=row, top_k=top_k)
+    _no_error()
+    want_q, want_s = _operand("mxfp8", rows * top_k, K)
+    bsfp8.bsmx_quantize("mxfp8", x, want_q, want_s, rows, K, row_of_slot=row, top_k=top_k, out_rows=rows * top_k)
+    assert torch.equal(q, want_q) and torch.equal(s, want_s) and torch.all(s[: rows * top_k * K // 32] > 0)
+
+
 def test_rows_out_of_range_are_recorded_and_skipped():
     rows, K, top_k = 6, 256, 2
     x = _rand((rows, K), torch.bfloat16, seed=1, spread=0.5).cuda()

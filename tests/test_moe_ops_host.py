@@ -9,6 +9,7 @@ import shutil
 import subprocess
 import threading
 import time
+import types
 
 import numpy as np
 import pytest
@@ -189,6 +190,16 @@ def test_sorted_slots_have_distinct_rows():
     ids = np.random.default_rng(2).integers(-1, 9, size=(40, 5))
     row = ref.sort_slots(ids, 8)[1]
     assert len(np.unique(row[row >= 0])) == (row >= 0).sum()
+
+
+def test_a_row_map_has_a_row_for_every_slot_unless_told_otherwise(monkeypatch):
+    seen = []
+    fake = types.SimpleNamespace(quantize=lambda *args: seen.append(args[8]) or 0)  # out_rows
+    monkeypatch.setattr(bsfp8, "_binding", fake)
+    bsfp8.bsmx_quantize("mxfp8", FAKE, FAKE, FAKE, 5, 128, x_type="bf16")
+    bsfp8.bsmx_quantize("mxfp8", FAKE, FAKE, FAKE, 5, 128, x_type="bf16", row_of_slot=FAKE, top_k=8)
+    bsfp8.bsmx_quantize("mxfp8", FAKE, FAKE, FAKE, 5, 128, x_type="bf16", row_of_slot=FAKE, top_k=8, out_rows=17)
+    assert seen == [5, 40, 17]
 
 
 STUB = r"""
