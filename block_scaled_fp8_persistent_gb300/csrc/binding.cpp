@@ -4,6 +4,7 @@
 // from the library the package loaded, so any build of it can be called.
 //
 // Every buffer is a CUDA tensor, a raw device address (int, unchecked) or None.
+#include <c10/cuda/CUDAFunctions.h>
 #include <c10/cuda/CUDAStream.h>
 #include <torch/csrc/autograd/python_variable.h>
 
@@ -84,6 +85,9 @@ class Args {
       return fail("%s has an unsupported type%s", name,
                   types == kBf16 ? ": it must be bf16" : "");
     if (!t.is_cuda()) return fail("%s must be a CUDA tensor (device memory)", name);
+    if (t.get_device() != device())
+      return fail("%s is on GPU %d, not on the current device (%d)", name, (int)t.get_device(),
+                  device());
     if (!t.is_contiguous()) return fail("%s must be contiguous (row-major)", name);
     if (t.numel() < count)
       return fail("%s holds %lld elements, needs %lld", name, (long long)t.numel(),
@@ -128,10 +132,18 @@ class Args {
   }
 
  private:
+  // The current device, which the call runs on; -1 where there is none.
+  int device() {
+    c10::DeviceIndex d = -1;
+    if (device_ == kUnasked) device_ = c10::cuda::GetDevice(&d) == cudaSuccess ? d : -1;
+    return device_;
+  }
   PyObject* take() { return failed_ ? nullptr : *next_++; }
 
   PyObject* const* next_;
   PyObject* stream_ = Py_None;
+  static constexpr int kUnasked = -2;
+  int device_ = kUnasked;
   bool failed_ = false;
 };
 

@@ -202,6 +202,25 @@ def test_a_row_map_has_a_row_for_every_slot_unless_told_otherwise(monkeypatch):
     assert seen == [5, 40, 17]
 
 
+def test_binding_refuses_tensors_of_another_gpu():
+    # tensors without memory, said to be on a GPU that is not the current one
+    libbuild.build()
+    class Elsewhere(torch.Tensor):
+        @classmethod
+        def __torch_dispatch__(cls, func, types, args=(), kwargs=None):
+            raise AssertionError("no operation is asked for")
+
+    x, h, ids = (torch.Tensor._make_wrapper_subclass(Elsewhere, (2, n), dtype=t, device="cuda:7")
+                 for n, t in ((128, torch.bfloat16), (256, torch.bfloat16), (2, torch.int32)))
+    for call in (lambda: bsfp8.bsmx_quantize("mxfp8", x, FAKE, FAKE, 2, 128),
+                 lambda: bsfp8.bsmx_swiglu_quant("mxfp8", h, FAKE, FAKE, 2, 128),
+                 lambda: bsfp8.bsmx_rmsnorm_quant("mxfp8", x, FAKE, 1e-6, 2, 128, y=FAKE),
+                 lambda: bsfp8.bsmx_moe_sort(ids, FAKE, FAKE, None, 2, 2, 8),
+                 lambda: bsfp8.bsmx_moe_combine(FAKE, ids, FAKE, 2, 4, 2, 128)):
+        with pytest.raises(ValueError, match="GPU 7"):
+            call()
+
+
 STUB = r"""
 #include <unistd.h>
 extern "C" {
