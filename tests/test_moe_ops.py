@@ -704,6 +704,57 @@ def test_offsets_past_32_bits():
     _no_error()
 
 
+def test_mapped_rows_and_gradient_past_32_bits():
+    rows, K = 300_001, 7168  # of q, C and dC: more than 2^31 elements
+    place = torch.tensor([[rows - 1, 0], [rows - 3, -1]], dtype=torch.int32, device="cuda")
+    x = _rand((2, K), torch.bfloat16, seed=6, spread=0.5).cuda()
+    for fmt in ("mxfp8", "blockwise"):
+        want_q, want_s = _operand(fmt, 2, K)
+        bsfp8.bsmx_quantize(fmt, x, want_q, want_s, 2, K)
+        q = torch.zeros(rows, K, dtype=torch.uint8, device="cuda")
+        s = torch.zeros(K // 128, rows, device="cuda") if fmt == "blockwise" else torch.zeros(rows, K // 32, dtype=torch.uint8, device="cuda")
+        bsfp8.bsmx_quantize(fmt, x, q, s, 2, K, row_of_slot=place, top_k=2, out_rows=rows)
+        _no_error()
+        want_q = want_q[: 2 * K].view(2, K)
+        want_s = want_s[: K // 64].view(-1, 2).t() if fmt == "blockwise" else want_s[: K // 16].view(2, -1)
+        for row, t in ((rows - 1, 0), (0, 0), (rows - 3, 1)):
+            assert torch.equal(q[row], want_q[t]) and torch.equal(s[:, row] if fmt == "blockwise" else s[row], want_s[t])
+        assert not q[1: rows - 3].any() and not q[rows - 2].any()
+        del q, s
+    C = torch.zeros(rows, K, dtype=torch.bfloat16, device="cuda")
+    C[-1], C[-3], C[0] = x[0], x[1], 1
+    dC, w = torch.zeros_like(C), torch.tensor([[0.5, 2.0], [4.0, 1.0]], device="cuda")
+    d = _rand((2, K), torch.bfloat16, seed=7, spread=0.0).cuda()
+    dw = torch.empty(2, 2, device="cuda")
+    bsfp8.bsmx_moe_combine_backward(d, C, place, w, dC, dw, 2, rows, 2, K)
+    _no_error()
+    # weights that are powers of two leave the products unrounded
+    assert torch.equal(dC[-1], d[0] * 0.5) and torch.equal(dC[0], d[0] * 2) and torch.equal(dC[-3], d[1] * 4)
+    assert not dC[1: rows - 3].any() and not dC[-2].any()
+    want, mag = torch.zeros(2, 2, dtype=torch.float64), torch.zeros(2, 2, dtype=torch.float64)
+    for t, j, v in ((0, 0, x[0]), (0, 1, torch.ones_like(x[0])), (1, 0, x[1])):
+        p = (d[t].double() * v.double()).cpu()
+        want[t, j], mag[t, j] = p.sum(), p.abs().sum()
+    terms = 2 * (8 * -(-K // 2048) + 5 + 8)
+    assert torch.all((dw.cpu().double() - want).abs() <= terms * 2.0 ** -24 * mag)
+
+
+def test_sort_of_almost_2_to_the_31_slots():
+    rows, top_k, E = (1 << 25) - 1, 64, 64
+    n = rows * top_k
+    ids = torch.arange(64, dtype=torch.int32, device="cuda").repeat(rows)  # slot s goes to expert s % 64
+    off = torch.empty(E + 2, dtype=torch.int32, device="cuda")
+    row, slot = torch.empty(n, dtype=torch.int32, device="cuda"), torch.empty(n, dtype=torch.int32, device="cuda")
+    ws = torch.empty(bsfp8.bsmx_moe_sort_workspace(rows, top_k, E), dtype=torch.uint8, device="cuda")
+    bsfp8.bsmx_moe_sort(ids, off, row, ws, rows, top_k, E, slot_of_row=slot)
+    assert off.tolist() == [e * rows for e in range(E + 1)] + [n]
+    e = torch.arange(64, device="cuda")
+    for t0 in range(0, rows, 1 << 22):
+        t = torch.arange(t0, min(t0 + (1 << 22), rows), device="cuda")
+        assert torch.equal(row.view(rows, 64)[t0: t0 + len(t)].long(), e * rows + t[:, None])
+        assert torch.equal(slot.view(64, rows)[:, t0: t0 + len(t)].long(), t * 64 + e[:, None])
+
+
 # ---------------------------------------------------------------------- with the products
 def _bf16_bound(want, terms):
     """2 bf16 ulp and 1e-6 of the sum of magnitudes: the grouped GEMM's own bound."""
