@@ -193,6 +193,7 @@ def dist_env():
 def dist_init(world: int, backend: str):
     if world <= 1:
         return None
+    os.environ["BSFP8_TMA_MULTICAST"] = "0"  # this rank may see one GPU, the job has more
     import torch.distributed as dist
     os.environ.setdefault("MASTER_ADDR", "127.0.0.1")
     dist.init_process_group(backend=backend)

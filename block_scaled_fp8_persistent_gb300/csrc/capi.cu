@@ -149,6 +149,22 @@ double blockwise_makespan(int64_t M_total, int N, int E, int tile_rows, int unit
   return std::ceil(tiles / (double)(units > 0 ? units : 1));
 }
 
+// The 224-row pair fills its peer's shared memory by TMA multicast.  That stays with programs on
+// one GPU: where the process has several, or BSFP8_TMA_MULTICAST=0 says that it is one of a job on
+// several, the 192-row pair, whose CTAs load their own operands, takes its place.
+bool multicast_switched_off() {
+  const char* v = std::getenv("BSFP8_TMA_MULTICAST");
+  return v && !std::strcmp(v, "0");
+}
+
+bool multicast_allowed() {
+  static const bool one = [] {
+    int count = 0;
+    return cudaGetDeviceCount(&count) == cudaSuccess && count == 1;
+  }();
+  return one && !multicast_switched_off();
+}
+
 // Tile configuration for a launch.  Candidates, all with the role warps on a TMEM
 // sub-partition of their own (a sub-partition that runs producer or MMA issue next to
 // epilogue warps slows those warps down about twofold, so the 128-row single-CTA layouts
@@ -159,12 +175,12 @@ double blockwise_makespan(int64_t M_total, int N, int E, int tile_rows, int unit
 // smaller (the estimates count whole waves, so an error of one tile can flip them).  The
 // environment variable BSFP8_BLOCKWISE_TILE (cta1_96 | pair_192 | pair_224 | cta1_256 |
 // pair_256 | pair_160 | pair_128 | cta1_128 | cta1_96x192 | pair_192x192 | cta1_128x192)
-// selects a configuration.
+// selects a configuration (pair_224 where multicast is allowed, see above).
 constexpr double kPair192Time = 0.95;  // 192 x 256 pair tile time / 96 x 256 one-CTA tile time
 constexpr double kPair224Time = 0.97;  // 224 x 256 pair tile time / 96 x 256 one-CTA tile time
 constexpr double kSwitchMargin = 0.92;
 
-BlockwiseTile choose_blockwise_tile(int64_t M_total, int N, int E, int num_sms) {
+BlockwiseTile choose_blockwise_tile(int64_t M_total, int N, int E, int num_sms, bool multicast) {
   if (const char* v = std::getenv("BSFP8_BLOCKWISE_TILE")) {
     if (!std::strcmp(v, "cta1_256")) return TILE_CTA1_256;
     if (!std::strcmp(v, "pair_256")) return TILE_PAIR_256;
@@ -176,14 +192,14 @@ BlockwiseTile choose_blockwise_tile(int64_t M_total, int N, int E, int num_sms) 
     if (!std::strcmp(v, "cta1_96x192")) return TILE_CTA1_96x192;
     if (!std::strcmp(v, "pair_192x192")) return TILE_PAIR_192x192;
     if (!std::strcmp(v, "cta1_128x192")) return TILE_CTA1_128x192;
-    if (!std::strcmp(v, "pair_224")) return TILE_PAIR_224;
+    if (!std::strcmp(v, "pair_224")) return multicast ? TILE_PAIR_224 : TILE_PAIR_192;
   }
   const double single = blockwise_makespan(M_total, N, E, 96, num_sms);
   const double pair192 = blockwise_makespan(M_total, N, E, 192, num_sms / 2) * kPair192Time;
   const double pair224 = blockwise_makespan(M_total, N, E, 224, num_sms / 2) * kPair224Time;
-  const double best_pair = std::min(pair192, pair224);
+  const double best_pair = multicast ? std::min(pair192, pair224) : pair192;
   if (best_pair >= kSwitchMargin * single) return TILE_CTA1_96;
-  return pair224 <= pair192 ? TILE_PAIR_224 : TILE_PAIR_192;
+  return multicast && pair224 <= pair192 ? TILE_PAIR_224 : TILE_PAIR_192;
 }
 
 // MXFP8 kernel choice from the average token rows per expert (the per-expert counts live on
@@ -274,20 +290,21 @@ bsfp8_status blockwise_gemm(const void* A, const void* B, const float* a_scales,
                ? BSFP8_OK
                : BSFP8_ERR_CUDA;
   };
+  const bool multicast = multicast_allowed();
   if (const char* v = std::getenv("BSFP8_BLOCKWISE_TILE")) {
     if (!std::strcmp(v, "split")) {
-      // groups of at least split_rows rows on 224-row CTA-pair tiles, then the others on
+      // groups of at least split_rows rows on the largest CTA-pair tiles, then the others on
       // 96-row tiles (two launches on `stream`, each over its own groups)
       const char* r = std::getenv("BSFP8_BLOCKWISE_SPLIT_ROWS");
       const int64_t split_rows = r ? std::atoll(r) : 448;
       GemmArgs heavy = args, light = args;
       heavy.min_group_rows = split_rows;
       light.max_group_rows = split_rows;
-      const bsfp8_status s1 = run(TILE_PAIR_224, heavy);
+      const bsfp8_status s1 = run(multicast ? TILE_PAIR_224 : TILE_PAIR_192, heavy);
       return s1 != BSFP8_OK ? s1 : run(TILE_CTA1_96, light);
     }
   }
-  return run(choose_blockwise_tile(M_total, N, G, dev->num_sms), args);
+  return run(choose_blockwise_tile(M_total, N, G, dev->num_sms, multicast), args);
 }
 
 // packed_b: b_scales are in the 512-byte block layout of bsmxfp8_pack_b_scales (both kernels:
@@ -527,7 +544,8 @@ extern "C" bsfp8_status bsfp8_blockwise_plan(int64_t M_total, int N, int num_exp
   if (!out) return BSFP8_ERR_NULL;
   if (M_total < 0 || N < 128 || N % 128 != 0 || num_experts < 1 || num_sms < 2)
     return BSFP8_ERR_SHAPE;
-  const BlockwiseTile tile = choose_blockwise_tile(M_total, N, num_experts, num_sms);
+  const BlockwiseTile tile = choose_blockwise_tile(M_total, N, num_experts, num_sms,
+                                                   !multicast_switched_off());
   const int ctas = (tile == TILE_PAIR_256 || tile == TILE_PAIR_160 || tile == TILE_PAIR_128 ||
                     tile == TILE_PAIR_192 || tile == TILE_PAIR_192x192 ||
                     tile == TILE_PAIR_224) ? 2 : 1;

@@ -417,7 +417,10 @@ bsfp8_status bsmxfp8_tmem_plan(int block_k, int epilogue_n, int vec, int overlap
  * pair_192, pair_224, cta1_256, pair_256, ...), or "split": groups with at least
  * BSFP8_BLOCKWISE_SPLIT_ROWS rows (default 448) on 224 x 256 pair tiles, then the others on
  * 96 x 256 tiles, as two kernels on the GEMM's stream; this function then reports the default
- * plan.  BSFP8_ERR_NULL / BSFP8_ERR_SHAPE on bad input.
+ * plan.  The 224 x 256 pair, whose loads include TMA multicast, is used by programs on one GPU
+ * alone: a process that sees several GPUs, or has BSFP8_TMA_MULTICAST=0 set (for the ranks of a
+ * job on several that see one each), gets the 192 x 256 pair in its place.  (This function looks
+ * at the variable only: it touches no GPU.)  BSFP8_ERR_NULL / BSFP8_ERR_SHAPE on bad input.
  */
 bsfp8_status bsfp8_blockwise_plan(int64_t M_total, int N, int num_experts, int num_sms,
                                   int32_t* out);

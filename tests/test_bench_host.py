@@ -34,6 +34,19 @@ def _rank(rank, world, port, q):
     dist.destroy_process_group()
 
 
+def test_ranks_of_several_gpus_use_no_multicast(monkeypatch):
+    import torch.distributed as dist
+    sys.path.insert(0, ROOT)
+    import bench
+    monkeypatch.setenv("BSFP8_TMA_MULTICAST", "1")
+    monkeypatch.setenv("MASTER_ADDR", "127.0.0.1")
+    monkeypatch.setattr(dist, "init_process_group", lambda backend: None)
+    bench.dist_init(1, "gloo")
+    assert os.environ["BSFP8_TMA_MULTICAST"] == "1"
+    bench.dist_init(2, "gloo")
+    assert os.environ["BSFP8_TMA_MULTICAST"] == "0"
+
+
 def test_replica_aggregation_two_gloo_ranks():
     ctx = mp.get_context("spawn")
     q = ctx.Queue()

@@ -65,6 +65,17 @@ def test_environment_override(monkeypatch, name, rows, cols, ctas):
     assert plan(4096, 4096, 8) == {"tile_rows": rows, "tile_cols": cols, "ctas_per_tile": ctas}
 
 
+@pytest.mark.parametrize("M,N,E", [(8192, 8192, 1), (30000, 7168, 1), (4096, 4096, 8), (16384, 2048, 64), (8192, 2048, 2)])
+def test_jobs_on_several_gpus_use_no_multicast(monkeypatch, M, N, E):
+    # the 224-row pair, the only form with multicast loads, is neither a candidate nor selectable
+    monkeypatch.setenv("BSFP8_TMA_MULTICAST", "0")
+    single, p192 = _model(M, N, E, 96, SMS), _model(M, N, E, 192, SMS // 2) * 0.95
+    want = {"tile_rows": 96, "ctas_per_tile": 1} if p192 >= 0.92 * single else {"tile_rows": 192, "ctas_per_tile": 2}
+    assert plan(M, N, E) == {**want, "tile_cols": 256}
+    monkeypatch.setenv("BSFP8_BLOCKWISE_TILE", "pair_224")
+    assert plan(M, N, E) == {"tile_rows": 192, "tile_cols": 256, "ctas_per_tile": 2}
+
+
 @pytest.mark.parametrize("args", [(-1, 256, 1), (10, 100, 1), (10, 256, 0)])
 def test_bad_input(args):
     with pytest.raises(bsfp8.BsFp8Error):

@@ -110,3 +110,13 @@ def test_m_total_zero_is_noop():
     off = torch.zeros(3, dtype=torch.int32, device="cuda")
     bsfp8.bsfp8_grouped_gemm(None, B, None, sb, off, None, 0, 128, 128, 2)
     assert bsfp8.bsfp8_get_device_error() == 0
+
+
+@pytest.mark.parametrize("form", [None, "pair_224", "split"])
+def test_without_multicast(monkeypatch, form):
+    # what a job on several GPUs runs: 192-row pairs in the 224-row pairs' place
+    monkeypatch.setenv("BSFP8_TMA_MULTICAST", "0")
+    if form:
+        monkeypatch.setenv("BSFP8_BLOCKWISE_TILE", form)
+    _check_full(gen.blockwise_problem([500, 3, 0, 447, 448, 130, 900], 256, 384, seed=61))
+    _check_full(gen.blockwise_problem([2500], 2048, 384, seed=62))
