@@ -347,7 +347,8 @@ def bsmx_moe_combine_backward(d_out, C, row_of_slot, weights, dC, d_weights, row
                               in_rows: int, top_k: int, N: int, stream=None) -> None:
     """Gradient of bsmx_moe_combine: dC[row_of_slot[t, j]] = weights[t, j] * d_out[t] and
     d_weights[t, j] = <d_out[t], C[row_of_slot[t, j]]>, for row maps that name no row twice (as
-    bsmx_moe_sort's).  See include/bsfp8.h.  Raises BsFp8Error."""
+    bsmx_moe_sort's).  Rows of dC that no slot names are left as they are: clear dC first where
+    slots are dropped and their gradient is read.  See include/bsfp8.h.  Raises BsFp8Error."""
     st = (_binding or load_binding()).moe_combine_backward(
         d_out, C, row_of_slot, weights, dC, d_weights, rows, in_rows, top_k, N, stream)
     if st:

@@ -46,7 +46,7 @@ __device__ __forceinline__ void load16(const void* x, int64_t at, float (&v)[16]
 // Rows of the element-wise operators: a thread takes one 16-element piece of a row.
 // ---------------------------------------------------------------------------------------
 constexpr int kPieceThreads = 256;
-constexpr int kPieceBlocks = 6;  // per SM: at most 42 registers
+constexpr int kPieceBlocks = 6;  // per SM: at most 40 registers
 
 // Blocks that follow a row map.  With many rows a block takes a whole row (up to 8192 elements),
 // so that each copy is written in one go: 8192 rows of 7168 to 8 places in mxfp8, with their
@@ -166,7 +166,7 @@ __device__ __forceinline__ void store16_fp32(float* p, const float (&v)[16]) {
 // allow it: with 16-byte stores each line is written in parts (16381 rows of 8192, fp32
 // residual, blockwise: 234 -> 209 us, 7.1 TB/s).  bf16 residuals fit 32 registers, 2048
 // threads per SM (16384 rows of 7168 with y, mxfp8: 152 us, 7.0 TB/s, against 161 with 1536);
-// fp32 ones take 42 (209 against 214).
+// fp32 ones take 40 (209 against 214).
 template <int FMT, bool Q, int RT, int ITEMS, bool WIDE, int LANES, int THREADS, int BLOCKS>
 __global__ void __launch_bounds__(THREADS, BLOCKS) rmsnorm_kernel(NormArgs a, bool early) {
   const int64_t t = LANES ? (int64_t)blockIdx.x * (blockDim.x / (LANES ? LANES : 1)) +
@@ -260,8 +260,9 @@ __device__ __forceinline__ float exp2_approx(float x) {
 // g / (1 + exp(-g)) * u for two elements.  The exponent's product with log2(e) is rounded, which
 // puts |g| 2^-24 of relative error on the exponential: it matters least where |g| is large,
 // beside 1 (g > 0) or in a result far below the block's largest (g < 0).  Of 100 million
-// quantised elements 187 differ from the 64-bit result's, with expf 189, in plain fp32 227;
-// expf takes 101 us where this takes 92 (65536 x 2048).
+// quantised elements of one sample 187 differ from the 64-bit result's, with expf 189, in plain
+// fp32 227 (a few hundred that lie next to a tie: other samples turn it round); expf takes 101 us
+// where this takes 92 (65536 x 2048).
 __device__ __forceinline__ void swiglu2(float& g0, float& g1, float u0, float u1) {
   constexpr float kNegLog2E = -1.4426950408889634f;
   float t0, t1;

@@ -21,10 +21,10 @@ namespace {
 // order could show: equal keys keep their order.  Bound by launches and round trips to L2, not
 // by bytes (12 per slot).  64 / 256 experts: one block up to kSortSingle slots (128 slots 1.9 us,
 // 512 slots 2.4; 1024 would take 3.3 / 3.7); a cluster of eight, whose blocks read each other's
-// counts from shared memory, up to kSortCluster (1024 slots 2.8 / 3.1 us, 4096 slots 3.5 / 3.8,
+// counts from shared memory, up to kSortCluster (1024 slots 2.8 / 3.2 us, 4096 slots 3.6 / 3.9,
 // 16384 slots 5.4 / 6.2; 65536 would take 11.1 / 12.4); above that many blocks and two launches,
-// the second started before the first ends (8192 would take 5.5 / 7.0, 65536 slots 5.9 / 7.7,
-// 524288 slots 9.1 / 11.4; back to back in a graph).
+// the second started before the first ends (8192 would take 5.7 / 7.1, 16384 slots 5.9 / 7.3;
+// 65536 slots 5.9 / 7.7, 524288 slots 9.1 / 11.5; back to back in a graph).
 // ---------------------------------------------------------------------------------------
 constexpr int kSortThreads = 1024;
 constexpr int kSortMaxChunks = 128;
@@ -277,7 +277,8 @@ __global__ void __launch_bounds__(kSortThreads) sort_cluster_kernel(SortArgs a, 
 //
 // Bound by HBM: every named row of C is read once.  A thread takes 8 columns of a token (16-byte
 // accesses, a warp's are 512 bytes of a row) and has the rows of up to 8 slots in flight, as
-// many as top_k needs; the registers are held to what leaves 1000 to 2000 threads per SM.
+// many as top_k needs; the registers are held to what leaves 1024 to 2048 threads per SM (the
+// gradient's 8 rows 80 registers and 768 threads).
 //   sum, 8 rows     blocks of 64 threads, 64 registers: 8192 tokens of 7168 columns 140 us,
 //                   6.9 TB/s (70 registers 146, 128 threads 145, 256 threads with 70 172)
 //   4 / 2 rows      128 threads: 8192 tokens of 4096 columns 61.4 / 41.5 us (64 threads 61.9 /

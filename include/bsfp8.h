@@ -296,7 +296,9 @@ bsfp8_status bsmx_grouped_gemm(int a_format, int b_format, const void* A, const 
  * of zeros has scale 1; a block that holds a NaN or an infinity has a NaN scale (UE8M0 0xFF,
  * e4m3 0x7F, fp32 NaN), so that what is computed of it is NaN.  q is 16-byte aligned, BLOCKWISE
  * scales 4-byte (the GEMM wants that of all scales); K and N are multiples of 128, at most 2^24;
- * inputs are 16-byte aligned.  Outputs overlap inputs only where that is said.  BSFP8_ERR_FORMAT for a format or type that is not listed.
+ * inputs are 16-byte aligned.  Outputs overlap inputs only where that is said.  BSFP8_ERR_FORMAT
+ * for a format or type that is not listed.  NVFP4 has no second scale for the whole tensor: blocks
+ * whose largest magnitude is below 6 * 2^-9 share the smallest scale and lose codes.
  */
 
 /*
@@ -378,7 +380,8 @@ bsfp8_status bsmx_moe_combine(const void* C, const int32_t* row_of_slot, const f
  * Its gradient, d_out bf16 [rows, N] being that of out (and of the residual):
  *   dC[row_of_slot[t, j]] = bf16( weights[t, j] * d_out[t] )
  *   d_weights[t, j]       = sum_n d_out[t, n] * C[row_of_slot[t, j], n]      fp32
- * d_weights is 0 for dropped slots; rows of dC that no slot names are left as they are.  No row
+ * d_weights is 0 for dropped slots; rows of dC that no slot names are left as they are (a caller
+ * with dropped slots who wants their zero gradient clears dC first).  No row
  * is to be named twice, as in the maps of bsmx_moe_sort: each slot stores its row of dC whole, so
  * of two slots with the same row one would be lost, and which one is not defined (the forward sum
  * takes such maps).  dC may not overlap C or d_out.  With distinct rows the result is the same
