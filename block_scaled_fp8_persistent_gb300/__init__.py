@@ -16,6 +16,11 @@ device, layout, type and size of every tensor, then the C entry point):
     bsfp8.bsmx_rmsnorm_quant(...), bsfp8.bsmx_moe_sort(...), bsfp8.bsmx_quantize(...),
     bsfp8.bsmx_swiglu_quant(...), bsfp8.bsmx_moe_combine(...), bsfp8.bsmx_moe_combine_backward(...)
 
+as do the experts' products in 16 bits and the backward pass of the experts:
+
+    bsfp8.bs16_grouped_gemm(...), bsfp8.bs16_grouped_wgrad(...), bsfp8.bsfp8_grouped_wgrad(...),
+    bsfp8.bsfp8_quantize_columns(...), bsfp8.bsmx_swiglu_backward(...)
+
 Tensors are torch CUDA tensors (or raw device addresses as ints) in the layouts of
 include/bsfp8.h; ``stream`` is a torch.cuda.Stream, a raw cudaStream_t int, or None for
 torch's current stream.
@@ -51,8 +56,9 @@ EXPORTED = ("bsfp8_grouped_gemm", "bsmxfp8_grouped_gemm", "bsfp8_grouped_gemm_id
             "bsmxfp8_tmem_plan", "bsfp8_blockwise_plan", "bsmxfp8_plan", "bsmx_plan",
             "bsmx_grouped_gemm", "bsmx_quantize", "bsmx_rmsnorm_quant", "bsmx_swiglu_quant",
             "bsmx_moe_sort_workspace", "bsmx_moe_sort", "bsmx_moe_combine",
-            "bsmx_moe_combine_backward", "bsfp8_get_device_error", "bsfp8_check_wait_timeout",
-            "bsfp8_status_string")
+            "bsmx_moe_combine_backward", "bs16_grouped_gemm", "bs16_grouped_wgrad",
+            "bsfp8_grouped_wgrad", "bsfp8_quantize_columns", "bsmx_swiglu_backward",
+            "bsfp8_get_device_error", "bsfp8_check_wait_timeout", "bsfp8_status_string")
 
 
 class BsFp8Error(RuntimeError):
@@ -112,6 +118,16 @@ def load_library() -> ctypes.CDLL:
         lib.bsmx_moe_combine.restype = i32
         lib.bsmx_moe_combine_backward.argtypes = [p, p, p, p, p, p, i64, i64, i32, i32, p]
         lib.bsmx_moe_combine_backward.restype = i32
+        lib.bs16_grouped_gemm.argtypes = [i32, i32, p, p, p, p, p, i64, i32, i32, i32, i32, p]
+        lib.bs16_grouped_gemm.restype = i32
+        lib.bs16_grouped_wgrad.argtypes = [i32, i32, p, p, p, p, p, i64, i32, i32, i32, p]
+        lib.bs16_grouped_wgrad.restype = i32
+        lib.bsfp8_grouped_wgrad.argtypes = [i32, p, p, p, p, p, p, p, i64, i32, i32, i32, p]
+        lib.bsfp8_grouped_wgrad.restype = i32
+        lib.bsfp8_quantize_columns.argtypes = [i32, p, p, i32, p, p, p, i64, i64, i32, i32, p]
+        lib.bsfp8_quantize_columns.restype = i32
+        lib.bsmx_swiglu_backward.argtypes = [i32, i32, p, p, p, p, p, p, i64, i32, p]
+        lib.bsmx_swiglu_backward.restype = i32
         lib.bsfp8_get_device_error.argtypes = [p, ctypes.POINTER(ctypes.c_int)]
         lib.bsfp8_get_device_error.restype = i32
         lib.bsfp8_check_wait_timeout.argtypes = [ctypes.c_int64, p]
@@ -247,6 +263,8 @@ def bsmxfp8_grouped_gemm_prepacked(A, B, a_scales, b_scales_packed, expert_offse
 # ---------------------------------------------------------------------------------------
 _OPERATORS = ("bsmx_quantize", "bsmx_rmsnorm_quant", "bsmx_swiglu_quant", "bsmx_moe_sort",
               "bsmx_moe_combine", "bsmx_moe_combine_backward")
+_EXPERT_OPERATORS = ("bs16_grouped_gemm", "bs16_grouped_wgrad", "bsfp8_grouped_wgrad",
+                     "bsfp8_quantize_columns", "bsmx_swiglu_backward")
 _binding = None
 
 
@@ -270,8 +288,9 @@ def load_binding():
         module = importlib.util.module_from_spec(spec)
         loader.exec_module(module)
         lib = load_library()
-        module.bind(*(ctypes.cast(getattr(lib, name), ctypes.c_void_p).value
-                      for name in _OPERATORS))
+        address = lambda name: ctypes.cast(getattr(lib, name), ctypes.c_void_p).value  # noqa: E731
+        module.bind(*map(address, _OPERATORS))
+        module.bind_experts(*map(address, _EXPERT_OPERATORS))
         _binding = module
     return _binding
 
@@ -353,6 +372,79 @@ def bsmx_moe_combine_backward(d_out, C, row_of_slot, weights, dC, d_weights, row
         d_out, C, row_of_slot, weights, dC, d_weights, rows, in_rows, top_k, N, stream)
     if st:
         raise BsFp8Error(st, "bsmx_moe_combine_backward")
+
+
+# ---------------------------------------------------------------------------------------
+# the experts in 16 bits, and their backward pass
+# ---------------------------------------------------------------------------------------
+def _type(name: str | None) -> int:
+    return -1 if name is None else TYPES[name]
+
+
+def bs16_grouped_gemm(A, B, group_offsets, C, M_total: int, N: int, K: int, num_groups: int,
+                      num_experts: int, expert_ids=None, transposed: bool = False,
+                      type: str | None = None, stream=None) -> None:
+    """C[m] = A[m] B[e]^T for the rows m of group g, e = expert_ids[g] (None: g), in bf16 or fp16:
+    A [M_total, K], B [num_experts, N, K], or [num_experts, K, N] where transposed (then
+    C[m] = A[m] B[e], the gradient of a product's rows), C [M_total, N].  Rows behind the last
+    group are left as they are.  See include/bsfp8.h.  Raises BsFp8Error."""
+    st = (_binding or load_binding()).grouped_gemm_16(
+        _type(type), 1 if transposed else 0, A, B, group_offsets, expert_ids, C, M_total, N, K,
+        num_groups, num_experts, stream)
+    if st:
+        raise BsFp8Error(st, "bs16_grouped_gemm")
+
+
+def bs16_grouped_wgrad(dC, A, group_offsets, dB, M_total: int, N: int, K: int, num_experts: int,
+                       add=None, type: str | None = None, out_type: str | None = None,
+                       stream=None) -> None:
+    """dB[e] = add[e] + dC[rows of e]^T A[rows of e] of bf16 or fp16 dC [M_total, N] and A
+    [M_total, K]; dB and add [num_experts, N, K] of their type or fp32 (add may be dB itself).
+    See include/bsfp8.h.  Raises BsFp8Error."""
+    st = (_binding or load_binding()).grouped_wgrad_16(
+        _type(type), _type(out_type), dC, A, group_offsets, add, dB, M_total, N, K, num_experts,
+        stream)
+    if st:
+        raise BsFp8Error(st, "bs16_grouped_wgrad")
+
+
+def bsfp8_grouped_wgrad(dC, A, dc_scales, a_scales, group_offsets, dB, M_total: int, N: int,
+                        K: int, num_experts: int, add=None, out_type: str | None = None,
+                        stream=None) -> None:
+    """The same of e4m3 operands quantised along the rows (bsfp8_quantize_columns) with their
+    scales [M_total / 128 + num_experts, N] and [.., K]; dB and add of bf16, fp16 or fp32.  See
+    include/bsfp8.h.  Raises BsFp8Error."""
+    st = (_binding or load_binding()).grouped_wgrad_8(
+        _type(out_type), dC, A, dc_scales, a_scales, group_offsets, add, dB, M_total, N, K,
+        num_experts, stream)
+    if st:
+        raise BsFp8Error(st, "bsfp8_grouped_wgrad")
+
+
+def bsfp8_quantize_columns(x, group_offsets, q, scales, M_total: int, K: int, num_groups: int,
+                           slot_of_row=None, top_k: int = 1, x_rows: int | None = None,
+                           x_type: str | None = None, stream=None) -> None:
+    """Quantise x (bf16, fp16 or fp32) along the rows into e4m3 q [M_total, K] and fp32 scales
+    [M_total / 128 + num_groups, K]: in each group, blocks of 128 rows of a column share a scale.
+    With slot_of_row, row r of q is row slot_of_row[r] // top_k of x [x_rows, K] (None:
+    M_total // top_k rows).  See include/bsfp8.h.  Raises BsFp8Error."""
+    st = (_binding or load_binding()).quantize_columns(
+        _type(x_type), x, slot_of_row, top_k, group_offsets, q, scales, M_total,
+        M_total // max(top_k, 1) if x_rows is None else x_rows, K, num_groups, stream)
+    if st:
+        raise BsFp8Error(st, "bsfp8_quantize_columns")
+
+
+def bsmx_swiglu_backward(h, d_act, rows: int, N: int, d_h=None, act=None, q=None, scales=None,
+                         format: str = "blockwise", type: str | None = None,
+                         stream=None) -> None:
+    """Gradient of act = silu(h[:, :N]) * h[:, N:] in bf16 or fp16: writes the gradient of h to
+    d_h, quantised in `format` to (q, scales), and act itself, each where it is given (act alone:
+    d_act None).  See include/bsfp8.h.  Raises BsFp8Error."""
+    st = (_binding or load_binding()).swiglu_backward(
+        _type(type), QUANT_FORMATS[format], h, d_act, d_h, act, q, scales, rows, N, stream)
+    if st:
+        raise BsFp8Error(st, "bsmx_swiglu_backward")
 
 
 def bsmxfp8_tmem_plan(block_k: int, epilogue_n: int, vec: int, overlap: bool) -> dict:

@@ -32,7 +32,9 @@ LIB = os.path.join(LIBDIR, "libbsfp8.so")
 DEBUG_LIB = os.path.join(LIBDIR, "libbsfp8_debug.so")
 
 SOURCES = ["capi.cu", "bsfp8_grouped.cu", "bsmxfp8_grouped.cu", "bsmxfp8_pair.cu",
-           "capi_moe.cu", "moe_quant.cu", "moe_route.cu"]
+           "capi_moe.cu", "moe_quant.cu", "moe_route.cu",
+           "capi_experts.cu", "grouped16.cu", "wgrad.cu", "quant_columns.cu",
+           "swiglu_grad.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "-I" + CSRC, "-I" + INCLUDE]
 

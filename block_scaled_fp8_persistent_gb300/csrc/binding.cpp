@@ -20,13 +20,22 @@ decltype(&bsmx_swiglu_quant) f_swiglu_quant = nullptr;
 decltype(&bsmx_moe_sort) f_moe_sort = nullptr;
 decltype(&bsmx_moe_combine) f_moe_combine = nullptr;
 decltype(&bsmx_moe_combine_backward) f_moe_combine_backward = nullptr;
+decltype(&bs16_grouped_gemm) f_grouped_gemm_16 = nullptr;
+decltype(&bs16_grouped_wgrad) f_grouped_wgrad_16 = nullptr;
+decltype(&bsfp8_grouped_wgrad) f_grouped_wgrad_8 = nullptr;
+decltype(&bsfp8_quantize_columns) f_quantize_columns = nullptr;
+decltype(&bsmx_swiglu_backward) f_swiglu_backward = nullptr;
 
 // A set of scalar types, as bits.
 constexpr uint64_t of(at::ScalarType t) {
   return static_cast<unsigned>(t) < 64 ? uint64_t{1} << static_cast<unsigned>(t) : 0;
 }
 constexpr uint64_t kBf16 = of(at::kBFloat16), kFp32 = of(at::kFloat), kInt32 = of(at::kInt);
-constexpr uint64_t kAnyInput = kBf16 | kFp32 | of(at::kHalf);
+constexpr uint64_t kFp16 = of(at::kHalf), kHalves = kBf16 | kFp16;
+constexpr uint64_t kAnyInput = kHalves | kFp32;
+constexpr uint64_t type_bits(int type) {
+  return type == BSMX_BF16 ? kBf16 : type == BSMX_FP16 ? kFp16 : kFp32;
+}
 
 // Reads the arguments of one call in order; the first failure sets a Python error, after which
 // everything returns zeros.
@@ -323,6 +332,127 @@ PyObject* moe_combine_backward(PyObject*, PyObject* const* args, Py_ssize_t n) {
   });
 }
 
+// grouped_gemm_16(type, transposed, A, B, offsets, ids, C, M_total, N, K, groups, experts, stream)
+PyObject* grouped_gemm_16(PyObject*, PyObject* const* args, Py_ssize_t n) {
+  Args a(args, n, 13);
+  int type = a.int32();
+  const int transposed = a.int32();
+  Buffer A = a.buffer("A"), B = a.buffer("B"), offsets = a.buffer("group_offsets"),
+         ids = a.buffer("expert_ids"), C = a.buffer("C");
+  const int64_t M = a.integer();
+  const int N = a.int32(), K = a.int32(), groups = a.int32(), experts = a.int32();
+  a.stream();
+  type = a.type_of(A.tensor ? A : B, A.tensor ? "A" : "B", type, kHalves);
+  a.check(A, "A", M * K, type_bits(type));
+  a.check(B, "B", (int64_t)experts * N * K, type_bits(type));
+  a.check(offsets, "group_offsets", (int64_t)groups + 1, kInt32);
+  a.check(ids, "expert_ids", groups, kInt32);
+  a.check(C, "C", M * N, type_bits(type));
+  return status(a, [&](cudaStream_t stream) {
+    return f_grouped_gemm_16(type, transposed, A.address, B.address,
+                             static_cast<const int32_t*>(offsets.address),
+                             static_cast<const int32_t*>(ids.address), C.address, M, N, K, groups,
+                             experts, stream);
+  });
+}
+
+// grouped_wgrad_16(type, out_type, dC, A, offsets, add, dB, M_total, N, K, experts, stream)
+PyObject* grouped_wgrad_16(PyObject*, PyObject* const* args, Py_ssize_t n) {
+  Args a(args, n, 12);
+  int type = a.int32(), out = a.int32();
+  Buffer dC = a.buffer("dC"), A = a.buffer("A"), offsets = a.buffer("group_offsets"),
+         add = a.buffer("add"), dB = a.buffer("dB");
+  const int64_t M = a.integer();
+  const int N = a.int32(), K = a.int32(), experts = a.int32();
+  a.stream();
+  type = a.type_of(dC.tensor ? dC : A, dC.tensor ? "dC" : "A", type, kHalves);
+  out = a.type_of(dB, "dB", out, kAnyInput);
+  a.check(dC, "dC", M * N, type_bits(type));
+  a.check(A, "A", M * K, type_bits(type));
+  a.check(offsets, "group_offsets", (int64_t)experts + 1, kInt32);
+  a.check(add, "add", (int64_t)experts * N * K, type_bits(out));
+  a.check(dB, "dB", (int64_t)experts * N * K, type_bits(out));
+  return status(a, [&](cudaStream_t stream) {
+    return f_grouped_wgrad_16(type, out, dC.address, A.address,
+                              static_cast<const int32_t*>(offsets.address), add.address,
+                              dB.address, M, N, K, experts, stream);
+  });
+}
+
+// grouped_wgrad_8(out_type, dC, A, dc_scales, a_scales, offsets, add, dB, M_total, N, K, experts,
+//                 stream)
+PyObject* grouped_wgrad_8(PyObject*, PyObject* const* args, Py_ssize_t n) {
+  Args a(args, n, 13);
+  int out = a.int32();
+  Buffer dC = a.buffer("dC"), A = a.buffer("A"), sc = a.buffer("dc_scales"),
+         sa = a.buffer("a_scales"), offsets = a.buffer("group_offsets"), add = a.buffer("add"),
+         dB = a.buffer("dB");
+  const int64_t M = a.integer();
+  const int N = a.int32(), K = a.int32(), experts = a.int32();
+  a.stream();
+  out = a.type_of(dB, "dB", out, kAnyInput);
+  const int64_t blocks = M / 128 + experts;
+  a.check(dC, "dC", M * N, 0, 1);
+  a.check(A, "A", M * K, 0, 1);
+  a.check(sc, "dc_scales", blocks * N, kFp32);
+  a.check(sa, "a_scales", blocks * K, kFp32);
+  a.check(offsets, "group_offsets", (int64_t)experts + 1, kInt32);
+  a.check(add, "add", (int64_t)experts * N * K, type_bits(out));
+  a.check(dB, "dB", (int64_t)experts * N * K, type_bits(out));
+  return status(a, [&](cudaStream_t stream) {
+    return f_grouped_wgrad_8(out, dC.address, A.address, static_cast<const float*>(sc.address),
+                             static_cast<const float*>(sa.address),
+                             static_cast<const int32_t*>(offsets.address), add.address,
+                             dB.address, M, N, K, experts, stream);
+  });
+}
+
+// quantize_columns(x_type, x, slot_of_row, top_k, offsets, q, scales, M_total, x_rows, K, groups,
+//                  stream)
+PyObject* quantize_columns(PyObject*, PyObject* const* args, Py_ssize_t n) {
+  Args a(args, n, 12);
+  int type = a.int32();
+  Buffer x = a.buffer("x"), map = a.buffer("slot_of_row");
+  const int top_k = a.int32();
+  Buffer offsets = a.buffer("group_offsets"), q = a.buffer("q"), scales = a.buffer("scales");
+  const int64_t M = a.integer(), x_rows = a.integer();
+  const int K = a.int32(), groups = a.int32();
+  a.stream();
+  type = a.type_of(x, "x", type, kAnyInput);
+  a.check(x, "x", x_rows * K, type_bits(type));
+  a.check(map, "slot_of_row", M, kInt32);
+  a.check(offsets, "group_offsets", (int64_t)groups + 1, kInt32);
+  a.check(q, "q", M * K, 0, 1);
+  a.check(scales, "scales", (M / 128 + groups) * K, kFp32);
+  return status(a, [&](cudaStream_t stream) {
+    return f_quantize_columns(type, x.address, static_cast<const int32_t*>(map.address), top_k,
+                              static_cast<const int32_t*>(offsets.address), q.address,
+                              static_cast<float*>(scales.address), M, x_rows, K, groups, stream);
+  });
+}
+
+// swiglu_backward(type, format, h, d_act, d_h, act, q, scales, rows, N, stream)
+PyObject* swiglu_backward(PyObject*, PyObject* const* args, Py_ssize_t n) {
+  Args a(args, n, 11);
+  int type = a.int32();
+  const int format = a.int32();
+  Buffer h = a.buffer("h"), d_act = a.buffer("d_act"), d_h = a.buffer("d_h"),
+         act = a.buffer("act"), q = a.buffer("q"), scales = a.buffer("scales");
+  const int64_t rows = a.integer();
+  const int N = a.int32();
+  a.stream();
+  type = a.type_of(h, "h", type, kHalves);
+  a.check(h, "h", rows * 2 * N, type_bits(type));
+  a.check(d_act, "d_act", rows * N, type_bits(type));
+  a.check(d_h, "d_h", rows * 2 * N, type_bits(type));
+  a.check(act, "act", rows * N, type_bits(type));
+  if (q.tensor || q.address) check_operand(a, format, q, scales, rows, 2 * (int64_t)N);
+  return status(a, [&](cudaStream_t stream) {
+    return f_swiglu_backward(type, format, h.address, d_act.address, d_h.address, act.address,
+                             q.address, scales.address, rows, N, stream);
+  });
+}
+
 // current_stream(): the raw stream torch launches on
 PyObject* current_stream(PyObject*, PyObject*) {
   return PyLong_FromVoidPtr(c10::cuda::getCurrentCUDAStream().stream());
@@ -340,6 +470,20 @@ PyObject* bind(PyObject*, PyObject* const* args, Py_ssize_t n) {
   f_moe_sort = reinterpret_cast<decltype(f_moe_sort)>(p[3]);
   f_moe_combine = reinterpret_cast<decltype(f_moe_combine)>(p[4]);
   f_moe_combine_backward = reinterpret_cast<decltype(f_moe_combine_backward)>(p[5]);
+  Py_RETURN_NONE;
+}
+
+// bind_experts(addresses): those of the experts' products in 16 bits and of their backward pass
+PyObject* bind_experts(PyObject*, PyObject* const* args, Py_ssize_t n) {
+  Args a(args, n, 5);
+  void* p[5];
+  for (void*& q : p) q = reinterpret_cast<void*>(a.integer());
+  if (!a.ok()) return nullptr;
+  f_grouped_gemm_16 = reinterpret_cast<decltype(f_grouped_gemm_16)>(p[0]);
+  f_grouped_wgrad_16 = reinterpret_cast<decltype(f_grouped_wgrad_16)>(p[1]);
+  f_grouped_wgrad_8 = reinterpret_cast<decltype(f_grouped_wgrad_8)>(p[2]);
+  f_quantize_columns = reinterpret_cast<decltype(f_quantize_columns)>(p[3]);
+  f_swiglu_backward = reinterpret_cast<decltype(f_swiglu_backward)>(p[4]);
   Py_RETURN_NONE;
 }
 
@@ -375,7 +519,13 @@ PyMethodDef methods[] = {fast<quantize>("quantize"),
                          fast<moe_sort>("moe_sort"),
                          fast<moe_combine>("moe_combine"),
                          fast<moe_combine_backward>("moe_combine_backward"),
+                         fast<grouped_gemm_16>("grouped_gemm_16"),
+                         fast<grouped_wgrad_16>("grouped_wgrad_16"),
+                         fast<grouped_wgrad_8>("grouped_wgrad_8"),
+                         fast<quantize_columns>("quantize_columns"),
+                         fast<swiglu_backward>("swiglu_backward"),
                          fast<bind>("bind"),
+                         fast<bind_experts>("bind_experts"),
                          {"current_stream", guarded_stream, METH_NOARGS, nullptr},
                          {nullptr, nullptr, 0, nullptr}};
 

@@ -8,6 +8,7 @@
 
 #include "bsfp8.h"
 #include "common.cuh"
+#include "expert_ops.cuh"
 #include "moe_ops.cuh"
 #include "ptx.cuh"
 
@@ -66,6 +67,13 @@ std::mutex g_dev_mu;
 bsfp8_status device_info(DeviceInfo** out) {
   int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMaxDevices) return BSFP8_ERR_CUDA;
+  // A thread that has made no other CUDA call has a device but no context yet, and tensor maps
+  // are encoded by the driver, which wants one.
+  static thread_local int bound = -1;
+  if (bound != dev) {
+    if (cudaSetDevice(dev) != cudaSuccess) return BSFP8_ERR_CUDA;
+    bound = dev;
+  }
   std::lock_guard<std::mutex> lock(g_dev_mu);
   DeviceInfo& d = g_dev[dev];
   if (!d.ready) {
@@ -260,6 +268,33 @@ int bsfp8::device_error_word(int** err) {
   const bsfp8_status st = device_info(&dev);
   if (st == BSFP8_OK) *err = dev->err_word;
   return st;
+}
+
+int bsfp8::device_error_word_and_sms(int** err, int* num_sms) {
+  DeviceInfo* dev = nullptr;
+  const bsfp8_status st = device_info(&dev);
+  if (st == BSFP8_OK) {
+    *err = dev->err_word;
+    *num_sms = dev->num_sms;
+  }
+  return st;
+}
+
+bool bsfp8::encode_swizzled(CUtensorMap* map, bool bytes, const void* base, int rank,
+                            const uint64_t* dims, uint32_t box_rows) {
+  EncodeTiledFn fn = encode_fn();
+  if (!fn || rank < 2 || rank > 3) return false;
+  const cuuint64_t size = bytes ? 1 : 2;
+  cuuint64_t d[3], strides[2];
+  for (int i = 0; i < rank; ++i) {
+    d[i] = dims[i];
+    if (i > 0) strides[i - 1] = (i > 1 ? strides[i - 2] : size) * dims[i - 1];
+  }
+  const cuuint32_t box[3] = {(cuuint32_t)(128 / size), box_rows, 1}, one[3] = {1, 1, 1};
+  return fn(map, bytes ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_UINT16,
+            (cuuint32_t)rank, const_cast<void*>(base), d, strides, box, one,
+            CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+            CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
 using namespace bsfp8;

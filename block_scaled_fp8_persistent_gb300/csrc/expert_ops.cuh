@@ -1,0 +1,113 @@
+// Launchers of the experts' products in 16 bits and of the backward pass of the experts
+// (grouped16.cu, wgrad.cu, quant_columns.cu) for the C-ABI layer (capi_experts.cu), and what
+// their kernels share.  Each launcher returns the launch error; sizes and alignment are checked
+// by the caller.
+#pragma once
+#include <cuda.h>
+#include <cuda_runtime.h>
+#include <cstdint>
+
+#include "common.cuh"
+#include "ptx.cuh"
+
+namespace bsfp8 {
+
+// The current device's error word and number of SMs (a bsfp8_status); capi.cu.
+int device_error_word_and_sms(int** err, int* num_sms);
+
+// Tensor map of a row-major array of `rank` dimensions, innermost first, whose box is 128 bytes
+// wide and swizzled over them; what lies outside reads as zero.  bytes: elements of one byte,
+// else of two.  False if the driver refuses it.  capi.cu.
+bool encode_swizzled(CUtensorMap* map, bool bytes, const void* base, int rank,
+                     const uint64_t* dims, uint32_t box_rows);
+
+// C[m, n] = sum_k A[m, k] B[e, n, k], or B[e, k, n] (transposed), in bf16 or fp16; the members
+// up to `err` are those that the tile scheduler and the offsets' check read.
+struct Product16Args {
+  const int32_t* offsets;     // [E + 1]
+  const int32_t* expert_ids;  // [E], or nullptr: group e multiplies expert e
+  int64_t M_total;
+  int N, K;
+  int E;            // groups
+  int num_experts;  // experts in B
+  int64_t min_group_rows, max_group_rows;
+  int* err;
+  const void* A;
+  const void* B;
+  void* C;
+  bool bf16;
+  bool transposed;
+};
+cudaError_t launch_product16(const Product16Args& a, int num_sms, cudaStream_t stream);
+
+// dB[e, n, k] = add[e, n, k] + sum over the rows m of group e of dC[m, n] A[m, k]; e4m3 operands
+// (fp8) have a scale for each block of 128 rows of a column.
+enum GradType : int { GRAD_BF16 = 0, GRAD_FP16 = 1, GRAD_FP32 = 2 };
+struct WgradArgs {
+  const int32_t* offsets;  // [E + 1]
+  int64_t M_total;
+  int N, K;
+  int E;
+  int* err;
+  const void* dC;          // [M_total, N]
+  const void* A;           // [M_total, K]
+  const float* dc_scales;  // fp8: [M_total / 128 + E, N]
+  const float* a_scales;   // fp8: [M_total / 128 + E, K]
+  const void* add;         // [E, N, K] of out_type, or nullptr
+  void* dB;                // [E, N, K] of out_type
+  int out_type;            // GradType
+  bool fp8;
+  bool bf16;               // of 16-bit operands
+};
+cudaError_t launch_wgrad(const WgradArgs& a, int num_sms, cudaStream_t stream);
+
+// q = e4m3(x / scale) in blocks of 128 rows of a column, counted from each group's first row.
+struct ColumnsArgs {
+  const void* x;
+  const int32_t* slot_of_row;  // [M_total], or nullptr: row r of q from row r of x
+  const int32_t* offsets;      // [E + 1]
+  uint8_t* q;                  // [M_total, K]
+  float* scales;               // [M_total / 128 + E, K]
+  int64_t M_total, x_rows;
+  int top_k, K, E;
+  int* err;
+};
+cudaError_t launch_quantize_columns(int x_type, const ColumnsArgs& a, cudaStream_t stream);
+
+// ---------------------------------------------------------------------------------------
+// device side
+// ---------------------------------------------------------------------------------------
+
+// Groups of rows may end before M_total: offsets[0] == 0 <= offsets[1] <= .. <= offsets[E] <=
+// M_total.  One full warp checks them (and the expert ids, where there are any) and counts the
+// tiles of BM rows; every lane gets the status (0 or a device error code) and the count.
+template <int BM>
+__device__ __forceinline__ int check_groups(const int32_t* off, const int32_t* ids, int E,
+                                            int num_experts, int64_t M_total,
+                                            int64_t& row_tiles) {
+  const uint32_t lane = lane_id();
+  int good = 1, good_ids = 1;
+  long long tiles = 0;
+  for (int e = (int)lane; e < E; e += 32) {
+    const int a = off[e], b = off[e + 1];
+    if (a < 0 || b < a || b > M_total) good = 0;
+    else tiles += (b - a + BM - 1) / BM;
+    if (ids) {
+      const int x = ids[e];
+      if (x < 0 || x >= num_experts) good_ids = 0;
+    }
+  }
+  if (lane == 0 && off[0] != 0) good = 0;
+  for (int s = 16; s > 0; s >>= 1) tiles += __shfl_xor_sync(0xffffffffu, tiles, s);
+  row_tiles = tiles;
+  return !__all_sync(0xffffffffu, good)       ? DEV_BAD_OFFSETS
+         : !__all_sync(0xffffffffu, good_ids) ? DEV_BAD_EXPERT_IDS
+                                              : 0;
+}
+
+__device__ __forceinline__ void give_up(int* err, volatile int* abort) {
+  atomicCAS(err, 0, (int)DEV_TIMEOUT);
+  *abort = 1;
+}
+
+}  // namespace bsfp8

@@ -105,6 +105,19 @@ struct SwigluArgs {
 };
 cudaError_t launch_swiglu_quant(int format, const SwigluArgs& a, cudaStream_t stream);
 
+struct SwigluBackwardArgs {
+  const void* h;      // [rows, 2N], gate then up
+  const void* d_act;  // [rows, N], or nullptr: act only
+  void* d_h;          // [rows, 2N], or nullptr
+  void* act;          // [rows, N], or nullptr
+  uint8_t* q;         // of d_h, or nullptr
+  void* scales;
+  int64_t rows;
+  int N;
+};
+cudaError_t launch_swiglu_backward(int format, int type, const SwigluBackwardArgs& a,
+                                   cudaStream_t stream);
+
 struct SortArgs {
   const int32_t* ids;    // [slots]
   int32_t* offsets;      // [experts + 2]

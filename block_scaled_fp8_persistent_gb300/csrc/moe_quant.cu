@@ -7,41 +7,13 @@
 // threads per SM.  Measured against that on the same shapes: a loop over several rows per block
 // with the next row's loads in flight 104 to 127 us where this takes 94 (SwiGLU, 65536 x 2048),
 // tiles of 8 rows x 128 columns per warp 122.
-#include <cuda_fp16.h>
-
 #include "moe_ops.cuh"
+#include "pieces.cuh"
 #include "ptx.cuh"
 #include "quant.cuh"
 
 namespace bsfp8 {
 namespace {
-// 16 elements as they are stored, and as fp32.
-template <int XT>
-constexpr int kWords = XT == E_FP32 ? 16 : 8;
-
-template <int XT>
-__device__ __forceinline__ void to_float(const uint32_t (&w)[kWords<XT>], float (&v)[16]) {
-#pragma unroll
-  for (int i = 0; i < kWords<XT>; ++i) {
-    if constexpr (XT == E_FP32) {
-      v[i] = __uint_as_float(w[i]);
-    } else if constexpr (XT == E_BF16) {
-      unpack_bf16x2(w[i], v[2 * i], v[2 * i + 1]);
-    } else {
-      const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&w[i]));
-      v[2 * i] = f.x;
-      v[2 * i + 1] = f.y;
-    }
-  }
-}
-
-template <int XT, bool WIDE = false>
-__device__ __forceinline__ void load16(const void* x, int64_t at, float (&v)[16]) {
-  uint32_t w[kWords<XT>];
-  load_words<kWords<XT>, WIDE>(static_cast<const char*>(x) + at * (XT == E_FP32 ? 4 : 2), w);
-  to_float<XT>(w, v);
-}
-
 // ---------------------------------------------------------------------------------------
 // Rows of the element-wise operators: a thread takes one 16-element piece of a row.
 // ---------------------------------------------------------------------------------------
@@ -244,19 +216,6 @@ __global__ void __launch_bounds__(THREADS, BLOCKS) rmsnorm_kernel(NormArgs a, bo
 // ---------------------------------------------------------------------------------------
 // SwiGLU: g / (1 + exp(-g)) * u
 // ---------------------------------------------------------------------------------------
-// 1 / x for x >= 1, within an ulp; 0 where it would be subnormal.
-__device__ __forceinline__ float rcp_approx(float x) {
-  float r;
-  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
-  return r;
-}
-
-__device__ __forceinline__ float exp2_approx(float x) {
-  float r;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
-  return r;
-}
-
 // g / (1 + exp(-g)) * u for two elements.  The exponent's product with log2(e) is rounded, which
 // puts |g| 2^-24 of relative error on the exponential: it matters least where |g| is large,
 // beside 1 (g > 0) or in a result far below the block's largest (g < 0).  Of 100 million

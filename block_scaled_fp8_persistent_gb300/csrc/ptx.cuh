@@ -56,6 +56,13 @@ __device__ __forceinline__ void mbar_arrive_cluster(uint32_t cluster_bar) {
   asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(cluster_bar) : "memory");
 }
 
+// The same publishing this thread's writes to its CTA's shared memory, for a thread of the
+// barrier's CTA that waits with mbar_wait_cluster.
+__device__ __forceinline__ void mbar_arrive_release_cluster(uint32_t cluster_bar) {
+  asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(cluster_bar)
+               : "memory");
+}
+
 __device__ __forceinline__ void mbar_arrive_expect_tx(uint32_t bar, uint32_t bytes) {
   asm volatile("mbarrier.arrive.expect_tx.release.cta.shared::cta.b64 _, [%0], %1;" ::"r"(bar),
                "r"(bytes)
@@ -242,6 +249,28 @@ __device__ __forceinline__ void tma_load_2d_pair_hint(uint32_t dst, const void* 
       : "memory");
 }
 
+// 3D forms of tma_load_2d_hint and tma_load_2d_pair_hint (what lies past a coordinate's end,
+// the end of one matrix of a stack among others, reads as zero).
+__device__ __forceinline__ void tma_load_3d_hint(uint32_t dst, const void* tmap, int32_t x,
+                                                 int32_t y, int32_t z, uint32_t bar,
+                                                 uint64_t policy) {
+  asm volatile(
+      "cp.async.bulk.tensor.3d.shared::cluster.global.mbarrier::complete_tx::bytes.L2::cache_hint"
+      " [%0], [%1, {%2, %3, %4}], [%5], %6;" ::"r"(dst),
+      "l"(reinterpret_cast<uint64_t>(tmap)), "r"(x), "r"(y), "r"(z), "r"(bar), "l"(policy)
+      : "memory");
+}
+
+__device__ __forceinline__ void tma_load_3d_pair_hint(uint32_t dst, const void* tmap, int32_t x,
+                                                      int32_t y, int32_t z, uint32_t bar,
+                                                      uint64_t policy) {
+  asm volatile(
+      "cp.async.bulk.tensor.3d.cta_group::2.shared::cluster.global.mbarrier::complete_tx::bytes"
+      ".L2::cache_hint [%0], [%1, {%2, %3, %4}], [%5], %6;" ::"r"(dst),
+      "l"(reinterpret_cast<uint64_t>(tmap)), "r"(x), "r"(y), "r"(z), "r"(bar), "l"(policy)
+      : "memory");
+}
+
 // CTA-pair load into the shared memory of the CTAs in `mask` (at this CTA's offset dst), with
 // the completion of each copy counted on the pair leader's barrier at offset `bar`
 // (.cta_group::2).  Used to fill a peer CTA that runs no producer of its own.
@@ -345,16 +374,23 @@ __device__ __forceinline__ void umma_f8f6f4(uint32_t d_tmem, uint64_t a_desc, ui
         : "memory");
 }
 
-// D[tmem] (+)= A[smem desc] * B[smem desc]^T, fp16 x fp16 -> fp32 (kind::f16, K = 16).
+// D[tmem] (+)= A[smem desc] * B[smem desc]^T, both operands fp16 or both bf16 -> fp32
+// (kind::f16, K = 16).
 template <int CG>
 __device__ __forceinline__ void umma_f16(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc,
                                          uint32_t idesc, uint32_t accumulate) {
-  static_assert(CG == 1, "one CTA");
-  asm volatile(
-      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
-      "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
-      "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate)
-      : "memory");
+  if constexpr (CG == 1)
+    asm volatile(
+        "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
+        "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate)
+        : "memory");
+  else
+    asm volatile(
+        "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
+        "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate)
+        : "memory");
 }
 
 // Block-scaled MMA: e4m3 x e4m3 with UE8M0 scales (one per 32 K) read from TMEM.
@@ -544,6 +580,14 @@ __device__ __forceinline__ uint64_t kmajor_sw64_desc(uint32_t saddr) {
   return make_smem_desc(saddr, 16, 512, LAYOUT_SW64);
 }
 
+// MN-major operand tile loaded as boxes of 128 bytes of the row or column index x K rows,
+// 128-byte swizzled by TMA: within a box 8 K rows are an atom of 1024 bytes (the stride); the
+// next 128 bytes of the row or column index are the next box, box_bytes away (the leading
+// offset).  Advancing K moves the start address by whole 128-byte rows.
+__device__ __forceinline__ uint64_t mnmajor_sw128_desc(uint32_t saddr, uint32_t box_bytes) {
+  return make_smem_desc(saddr, box_bytes, 1024, LAYOUT_SW128);
+}
+
 // Instruction descriptor for kind::f8f6f4, e4m3 x e4m3 -> fp32, both operands K-major:
 //   bits 4-5 D format (1 = f32), 7-9 A format (0 = e4m3), 10-12 B format (0 = e4m3),
 //   15/16 A/B major (0 = K), 17-22 N >> 3, 24-28 M >> 4.
@@ -556,6 +600,11 @@ __host__ __device__ constexpr uint32_t idesc_f8f6f4_e4m3(uint32_t M, uint32_t N)
 __host__ __device__ constexpr uint32_t idesc_f16_f32(uint32_t M, uint32_t N) {
   return (1u << 4) | ((N >> 3) << 17) | ((M >> 4) << 24);
 }
+
+// Bits that make either of the two descriptors above one of bf16 operands (kind::f16, format 1),
+// and of operands that are MN-major.
+constexpr uint32_t IDESC_BF16 = (1u << 7) | (1u << 10);
+constexpr uint32_t IDESC_A_MN = 1u << 15, IDESC_B_MN = 1u << 16;
 
 // Instruction descriptor for kind::mxf8f6f4 (block scaled), e4m3 operands, UE8M0 scales:
 //   bits 4-5 B scale-factor id, 7-9 A format, 10-12 B format, 17-22 N >> 3,
@@ -626,6 +675,12 @@ __device__ __forceinline__ void prefetch_l1(const void* p) {
 __device__ __forceinline__ uint32_t pack_bf16x2(float lo, float hi) {
   uint32_t r;
   asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+  return r;
+}
+
+__device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
+  uint32_t r;
+  asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
   return r;
 }
 

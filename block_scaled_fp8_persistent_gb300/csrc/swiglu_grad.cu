@@ -1,0 +1,105 @@
+// SwiGLU's gradient: with s = 1 / (1 + exp(-g)) and act = g s u,
+//
+//   d_u = d g s,   d_g = d u s (1 + g (1 - s))
+//
+// written in 16 bits and / or quantised as the A of the products that follow, and act itself.  Bound
+// by HBM: a thread reads 16 elements of each of g, u and d once and writes what is made of them.
+#include "moe_ops.cuh"
+#include "pieces.cuh"
+#include "ptx.cuh"
+#include "quant.cuh"
+
+namespace bsfp8 {
+namespace {
+
+constexpr int kPieceThreads = 256;
+
+// What is quantised is not rounded before.  The exponential is that of the forward operator
+// (its product with log2(e) is rounded: |g| 2^-24 relative); 1 - s costs |g| 2^-25 beside 1 in d_g.
+__device__ __forceinline__ float sigmoid(float g) {
+  return rcp_approx(1.0f + exp2_approx(g * -1.4426950408889634f));
+}
+
+template <int XT>
+__device__ __forceinline__ void store16(void* p, int64_t at, const float (&v)[16]) {
+  uint32_t w[8];
+#pragma unroll
+  for (int e = 0; e < 8; ++e)
+    w[e] = XT == E_BF16 ? pack_bf16x2(v[2 * e], v[2 * e + 1]) : pack_f16x2(v[2 * e], v[2 * e + 1]);
+  uint16_t* q = static_cast<uint16_t*>(p) + at;
+  st_global_v4(q, w[0], w[1], w[2], w[3]);
+  st_global_v4(q + 8, w[4], w[5], w[6], w[7]);
+}
+
+template <int FMT, int XT, bool Q>
+__global__ void __launch_bounds__(kPieceThreads, 3) swiglu_backward_kernel(SwigluBackwardArgs a,
+                                                                           bool early) {
+  begin_early(early);
+  const int items = a.N / 16;
+  const int64_t p = (int64_t)blockIdx.x * kPieceThreads + threadIdx.x;
+  const int64_t t = p / items;
+  const int i = (int)(p - t * items);
+  const bool live = t < a.rows;
+  float g[16] = {}, u[16] = {};
+  if (live) {
+    const int64_t at = t * 2 * a.N + (int64_t)i * 16;
+    float d[16] = {}, act[16];
+    load16<XT>(a.h, at, g);
+    load16<XT>(a.h, at + a.N, u);
+    if (a.d_act) load16<XT>(a.d_act, t * a.N + (int64_t)i * 16, d);
+#pragma unroll
+    for (int e = 0; e < 16; ++e) {
+      const float s = sigmoid(g[e]), silu = g[e] * s, ds = d[e] * s;
+      act[e] = silu * u[e];
+      const float d_g = ds * u[e] * fmaf(g[e], 1.0f - s, 1.0f);
+      u[e] = d[e] * silu;
+      g[e] = d_g;
+    }
+    if (a.act) store16<XT>(a.act, t * a.N + (int64_t)i * 16, act);
+    if (a.d_h) {
+      store16<XT>(a.d_h, at, g);
+      store16<XT>(a.d_h, at + a.N, u);
+    }
+  }
+  if constexpr (Q) {
+    const Quantised<FMT> og = quantise16<FMT>(g), ou = quantise16<FMT>(u);
+    if (live) {
+      store_codes<FMT>(og, a.q, t, i, 2 * a.N);
+      store_scale<FMT>(og, a.scales, t, a.rows, i, 2 * a.N);
+      store_codes<FMT>(ou, a.q, t, i + items, 2 * a.N);
+      store_scale<FMT>(ou, a.scales, t, a.rows, i + items, 2 * a.N);
+    }
+  }
+}
+
+template <int FMT, int XT, bool Q>
+cudaError_t swiglu_backward_as(const SwigluBackwardArgs& a, cudaStream_t stream) {
+  const int64_t pieces = a.rows * (a.N / 16);
+  const dim3 grid((unsigned)((pieces + kPieceThreads - 1) / kPieceThreads));
+  const int each = 16 * (6 + (a.d_h ? 4 : 0) + (a.act ? 2 : 0) + (Q ? 2 : 0));
+  const bool early = starts_early(grid, (int64_t)kPieceThreads * each);
+  return launch(swiglu_backward_kernel<FMT, XT, Q>, grid, kPieceThreads, 0, early, stream, 1, a, early);
+}
+
+template <int FMT>
+cudaError_t swiglu_backward_format(int type, const SwigluBackwardArgs& a, cudaStream_t stream) {
+  return type == E_BF16 ? swiglu_backward_as<FMT, E_BF16, true>(a, stream)
+                        : swiglu_backward_as<FMT, E_FP16, true>(a, stream);
+}
+
+}  // namespace
+
+cudaError_t launch_swiglu_backward(int format, int type, const SwigluBackwardArgs& a,
+                                   cudaStream_t stream) {
+  if (!a.q)
+    return type == E_BF16 ? swiglu_backward_as<Q_MXFP8, E_BF16, false>(a, stream)
+                          : swiglu_backward_as<Q_MXFP8, E_FP16, false>(a, stream);
+  switch (format) {
+    case Q_MXFP8: return swiglu_backward_format<Q_MXFP8>(type, a, stream);
+    case Q_MXFP4: return swiglu_backward_format<Q_MXFP4>(type, a, stream);
+    case Q_NVFP4: return swiglu_backward_format<Q_NVFP4>(type, a, stream);
+    default: return swiglu_backward_format<Q_BLOCKWISE>(type, a, stream);
+  }
+}
+
+}  // namespace bsfp8

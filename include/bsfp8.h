@@ -393,6 +393,107 @@ bsfp8_status bsmx_moe_combine_backward(const void* d_out, const void* C,
                                        int N, cudaStream_t stream);
 
 /*
+ * The experts in 16 bits, and their backward pass.  A product's rows, gradients and weights are
+ *
+ *   C  = A B^T          bs16_grouped_gemm                    (or a block-scaled grouped GEMM)
+ *   dA = dC B           bs16_grouped_gemm, transposed        (8 bits: bsfp8_grouped_gemm of dC
+ *                       quantised along its rows and of the weights' transpose)
+ *   dB = dC^T A         bs16_grouped_wgrad, bsfp8_grouped_wgrad
+ *
+ * per expert, and between two products stands bsmx_swiglu_backward.  The conventions above hold,
+ * but for the offsets:
+ *
+ *   group_offsets  int32 [num_groups + 1]: group_offsets[0] = 0, non-decreasing,
+ *                  group_offsets[num_groups] <= M_total.  Rows behind the last group are neither
+ *                  read nor written.  The first num_experts + 1 offsets of bsmx_moe_sort do, with
+ *                  M_total = rows * top_k, whether slots were dropped or not.  Offsets that are
+ *                  not so are recorded as BSFP8_ERR_DEVICE_OFFSETS.
+ *
+ * Groups may be empty; num_groups and num_experts are at most 2^20; M_total, N and K as below.
+ * Sums are held in fp32.  The same inputs give the same bits every time: each sum has one order.
+ */
+
+/*
+ * Products grouped by expert in 16 bits:
+ *   C[m, n] = sum_k A[m, k] * B[e, n, k]      transposed == 0: B [num_experts, N, K]
+ *   C[m, n] = sum_k A[m, k] * B[e, k, n]      else:            B [num_experts, K, N]
+ * with e = expert_ids[g] for the rows of group g, or g where expert_ids is NULL (then num_groups
+ * <= num_experts).  A [M_total, K], B and C [M_total, N] are all of `type`, BSMX_BF16 or
+ * BSMX_FP16 (BSFP8_ERR_FORMAT else); C is rounded once (fp16 results past 65504 are infinite).
+ * N and K are multiples of 8, at most 2^24, N * K < 2^38; A, B and C 16-byte aligned (C 32-byte
+ * aligned and N % 16 == 0: wider stores).  An expert id outside [0, num_experts) is recorded as
+ * BSFP8_ERR_DEVICE_EXPERT_IDS, with nothing written.  M_total == 0 is a no-op.
+ */
+bsfp8_status bs16_grouped_gemm(int type, int transposed, const void* A, const void* B,
+                               const int32_t* group_offsets, const int32_t* expert_ids, void* C,
+                               int64_t M_total, int N, int K, int num_groups, int num_experts,
+                               cudaStream_t stream);
+
+/*
+ * Weight gradient of that product:
+ *   dB[e, n, k] = add[e, n, k] + sum over the rows m of group e of dC[m, n] * A[m, k]
+ * dC [M_total, N] and A [M_total, K] of `type` (BSMX_BF16 or BSMX_FP16); dB and add [num_experts,
+ * N, K] of out_type, which is `type` or BSMX_FP32.  add may be NULL (zeros), or dB itself, which
+ * adds to it.  All of dB is written: an expert without rows gets add, or zeros, M_total == 0
+ * included.  N and K are multiples of 8, at most 2^24; all 16-byte aligned.  Rows of other groups
+ * and behind the last one do not reach the sum, whatever they hold.
+ */
+bsfp8_status bs16_grouped_wgrad(int type, int out_type, const void* dC, const void* A,
+                                const int32_t* group_offsets, const void* add, void* dB,
+                                int64_t M_total, int N, int K, int num_experts,
+                                cudaStream_t stream);
+
+/*
+ * The same of e4m3 operands that are quantised along the rows (bsfp8_quantize_columns):
+ *   dB[e, n, k] = add[e, n, k]
+ *                 + sum_t dc_scales[s + t, n] * a_scales[s + t, k]
+ *                         * sum over the rows m of block t of group e of dC[m, n] * A[m, k]
+ * Block t of group e holds its rows 128 t .. 128 t + 127 (the last block fewer), and
+ * s = group_offsets[e] / 128 + e (integer division): scales of M_total / 128 + num_experts rows
+ * hold every block of any partition.  dc_scales fp32 [M_total / 128 + num_experts, N], a_scales
+ * the same of K.  dB and add are of out_type (a bsmx_type).  N and K are multiples of 128;
+ * a_scales 16-byte aligned, dc_scales 4-byte.  The rest is as for bs16_grouped_wgrad.
+ */
+bsfp8_status bsfp8_grouped_wgrad(int out_type, const void* dC, const void* A,
+                                 const float* dc_scales, const float* a_scales,
+                                 const int32_t* group_offsets, const void* add, void* dB,
+                                 int64_t M_total, int N, int K, int num_experts,
+                                 cudaStream_t stream);
+
+/*
+ * Quantises along the rows: block t of group e and column k have one scale,
+ *   scales[group_offsets[e] / 128 + e + t, k] = a / 448,   a the block's largest magnitude,
+ * at least 2^-126, 1 for a block of zeros, NaN for one that holds a NaN or an infinity; q is
+ * value / scale (the product with its fp32 reciprocal) rounded to the nearest e4m3 code, ties to
+ * even.  q e4m3 [M_total, K], scales fp32 [M_total / 128 + num_groups, K].
+ *   slot_of_row NULL  row r of q is row r of x; top_k == 1, x_rows == M_total
+ *   slot_of_row       int32 [M_total] (bsmx_moe_sort): row r of q is row slot_of_row[r] / top_k of
+ *                     x [x_rows, K]; zeros where it is negative.  A row >= x_rows counts as zeros
+ *                     and is recorded as BSFP8_ERR_DEVICE_ROWS.
+ * x is of x_type (a bsmx_type).  Rows of q behind the last group and rows of scales that no block
+ * has are left as they are.  K is a multiple of 128, at most 2^22; 1 <= top_k <= 64; x, q and
+ * scales 16-byte aligned.
+ */
+bsfp8_status bsfp8_quantize_columns(int x_type, const void* x, const int32_t* slot_of_row,
+                                    int top_k, const int32_t* group_offsets, void* q,
+                                    float* scales, int64_t M_total, int64_t x_rows, int K,
+                                    int num_groups, cudaStream_t stream);
+
+/*
+ * SwiGLU's gradient.  Of h = [gate | up] [rows, 2N] and d_act [rows, N], with g = gate, u = up,
+ * s = 1 / (1 + exp(-g)):
+ *   act = g s u      d_h = [d_act u s (1 + g (1 - s)) | d_act g s]
+ * in fp32.  Outputs, each optional but not all NULL: d_h [rows, 2N] and act [rows, N] of `type`,
+ * and d_h (unrounded) quantised along its rows in `format` into q and scales, an operand of rows x
+ * 2N.  h and d_act are of `type`, BSMX_BF16 or BSMX_FP16.  act alone needs no d_act: it is the
+ * activation in 16 bits.  d_h may be h's own buffer and act d_act's.  N is a multiple of 128, at
+ * most 2^23, rows * N at most 2^42; all 16-byte aligned (scales as for bsmx_quantize).
+ */
+bsfp8_status bsmx_swiglu_backward(int type, int format, const void* h, const void* d_act,
+                                  void* d_h, void* act, void* q, void* scales, int64_t rows,
+                                  int N, cudaStream_t stream);
+
+/*
  * TMEM storage plan of double-buffered block-scaled accumulators (host only, no GPU use).
  * For a 256-column tile with 512 TMEM columns, block_k elements of K per MMA stage,
  * epilogue subtiles of epilogue_n columns and one scale per vec (16 or 32) elements of K,
