@@ -32,7 +32,7 @@ bsfp8_status wgrad(const WgradArgs& a, int step, cudaStream_t stream) {
     return BSFP8_ERR_NULL;
   if (!rows_ok(a.M_total) || !matrix_ok(a.N, a.K, step) || !groups_ok(a.E)) return BSFP8_ERR_SHAPE;
   if (!aligned(a.dC, 16) || !aligned(a.A, 16) || !aligned(a.dB, 16) || !aligned(a.add, 16) ||
-      !aligned(a.dc_scales, 4) || !aligned(a.a_scales, 16) || !aligned(a.offsets, 4))
+      !aligned(a.dc_scales, 16) || !aligned(a.a_scales, 16) || !aligned(a.offsets, 4))
     return BSFP8_ERR_ALIGN;
   WgradArgs go = a;
   int sms = 0;

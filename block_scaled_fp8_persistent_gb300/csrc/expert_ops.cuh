@@ -21,6 +21,10 @@ int device_error_word_and_sms(int** err, int* num_sms);
 bool encode_swizzled(CUtensorMap* map, bool bytes, const void* base, int rank,
                      const uint64_t* dims, uint32_t box_rows);
 
+// Tensor map of an fp32 array [rows, cols] whose box is one row of box_cols, not swizzled.
+bool encode_rows_f32(CUtensorMap* map, const void* base, uint64_t cols, uint64_t rows,
+                     uint32_t box_cols);
+
 // C[m, n] = sum_k A[m, k] B[e, n, k], or B[e, k, n] (transposed), in bf16 or fp16; the members
 // up to `err` are those that the tile scheduler and the offsets' check read.
 struct Product16Args {

@@ -207,13 +207,13 @@ product16_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant_
       bool ok = true;
       for (int64_t t = tile0; ok && t < total_tiles; t += tile_stride) {
         if (!sched.locate(args, t, tc)) break;
-        if (!mbar_wait(tempty_bar(acc), acc_phase ^ 1, abort)) {
+        if (!mbar_wait_sleep(tempty_bar(acc), acc_phase ^ 1, abort)) {
           give_up(args.err, abort);
           break;
         }
         const uint32_t d = tmem_base + acc * C::BN;
         for (int kb = 0; kb < KB; ++kb) {
-          if (!mbar_wait(full_bar(stage), phase, abort)) {
+          if (!mbar_wait_sleep(full_bar(stage), phase, abort)) {
             give_up(args.err, abort);
             ok = false;
             break;

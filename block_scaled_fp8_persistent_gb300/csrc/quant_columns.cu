@@ -5,13 +5,17 @@
 //   block holds a NaN or an infinity),  q = e4m3(x / scale)
 //
 // the blockwise rule of quant.cuh turned by 90 degrees.  Rows may be gathered: row r of q comes
-// from the token whose slot lies in row r.  Bound by HBM: each element is read once, kept in
-// registers while its block's largest magnitude is found, and written once.
+// from the token whose slot lies in row r.  Each element is read once, kept in registers while its
+// block's largest magnitude is found, and written once: 65536 rows of 7168 take 216 us, 6.6 TB/s,
+// what HBM gives.  Gathered from 8192 tokens the same rows come out of L2, and at 172 us the
+// instructions bound it (with the loads left out 147).
 //
-// A block of threads takes 128 rows x 128 columns: thread (i, c) the 8 columns 8 c.. of the rows
-// i, i + 16, .., so that 16 threads read 256 bytes of a row (16-bit) and write 128.  Which rows
-// those are the offsets say: block b of the scales belongs to the last group e with
-// offsets[e] / 128 + e <= b, which the threads count together.
+// A block of threads takes the 128 rows of a scale block and walks over tiles of 128 columns, the
+// next two under way (cp.async; a thread reads back what it copied itself): thread (i, c) the 8
+// columns 8 c.. of the rows i, i + 16, .., so that 16 threads read 256 bytes of a row (16-bit) and
+// write 128.  Which rows those are the offsets say: block b of the scales belongs to the last
+// group e with offsets[e] / 128 + e <= b, which the threads count together, once for all tiles.
+#include <atomic>
 #include <cuda_fp16.h>
 
 #include "expert_ops.cuh"
@@ -23,50 +27,106 @@ namespace {
 
 constexpr int kBlockRows = 128, kTileCols = 128;
 constexpr int kThreads = 256;
-constexpr int kColumnThreads = kTileCols / 8;            // threads side by side
-constexpr int kRowThreads = kThreads / kColumnThreads;   // 16
-constexpr int kRowsEach = kBlockRows / kRowThreads;      // 8
+constexpr int kColumnThreads = kTileCols / 8;           // threads side by side
+constexpr int kRowThreads = kThreads / kColumnThreads;  // 16
+constexpr int kRowsEach = kBlockRows / kRowThreads;     // 8
+
+// Tiles in flight and blocks per SM.  Gathered rows come out of L2, and more threads are worth more
+// than more tiles: 65536 rows of 7168 by 8 of 8192 172 us, with 3 and 2 195; rows that lie side by
+// side come from HBM and want the depth (320 rows of 2048 3.5 us against 4.0).
+template <bool GATHER>
+constexpr int kStages = GATHER ? 2 : 3;
+template <int XT, bool GATHER>
+constexpr int kResident = XT == E_FP32 ? 1 : GATHER ? 3 : 2;
 
 template <int XT>
-struct Eight {  // elements of a row, as they are stored
-  uint32_t w[XT == E_FP32 ? 8 : 4];
+constexpr int kEightBytes = XT == E_FP32 ? 32 : 16;  // of 8 elements as they are stored
+
+template <int XT>
+constexpr int kStageBytes = kBlockRows * kColumnThreads * kEightBytes<XT>;
+
+// Eight elements as they are stored.
+template <int XT>
+struct Eight {
+  uint32_t w[kEightBytes<XT> / 4];
 };
 
 template <int XT>
-__device__ __forceinline__ void unpack(const Eight<XT>& r, float (&v)[8]) {
-  if constexpr (XT == E_FP32) {
+__device__ __forceinline__ Eight<XT> read8(const uint8_t* p) {
+  Eight<XT> x;
 #pragma unroll
-    for (int j = 0; j < 8; ++j) v[j] = __uint_as_float(r.w[j]);
-  } else {
+  for (int i = 0; i < kEightBytes<XT> / 16; ++i) {
+    const uint4 w = reinterpret_cast<const uint4*>(p)[i];
+    x.w[4 * i] = w.x;
+    x.w[4 * i + 1] = w.y;
+    x.w[4 * i + 2] = w.z;
+    x.w[4 * i + 3] = w.w;
+  }
+  return x;
+}
+
+// Largest magnitudes of eight columns so far.  16-bit values are compared as they lie: without
+// their signs they are ordered as integers, infinities and NaNs last, two to an instruction.
+template <int XT>
+__device__ __forceinline__ void take_max(Eight<XT>& top, const Eight<XT>& a, const Eight<XT>& b) {
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      if constexpr (XT == E_BF16) {
-        unpack_bf16x2(r.w[j], v[2 * j], v[2 * j + 1]);
-      } else {
-        const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&r.w[j]));
-        v[2 * j] = f.x;
-        v[2 * j + 1] = f.y;
-      }
-    }
+  for (int i = 0; i < kEightBytes<XT> / 4; ++i) {
+    if constexpr (XT == E_FP32)
+      top.w[i] = max(max(top.w[i], a.w[i] & 0x7fffffffu), b.w[i] & 0x7fffffffu);
+    else
+      top.w[i] = __vimax3_u16x2(top.w[i], a.w[i] & 0x7fff7fffu, b.w[i] & 0x7fff7fffu);
   }
 }
 
+template <int XT>
+__device__ __forceinline__ uint32_t max_words(uint32_t a, uint32_t b) {
+  return XT == E_FP32 ? max(a, b) : __vmaxu2(a, b);
+}
+
+// The two columns of a word (fp32: one, in v.x).
+template <int XT>
+__device__ __forceinline__ float2 word_values(uint32_t w) {
+  if constexpr (XT == E_FP32) {
+    return make_float2(__uint_as_float(w), 0.0f);
+  } else if constexpr (XT == E_BF16) {
+    return make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xffff0000u));
+  } else {
+    return __half22float2(*reinterpret_cast<const __half2*>(&w));
+  }
+}
+
+// Elements 2 j and 2 j + 1.
+template <int XT>
+__device__ __forceinline__ float2 pair(const Eight<XT>& x, int j) {
+  if constexpr (XT == E_FP32)
+    return make_float2(__uint_as_float(x.w[2 * j]), __uint_as_float(x.w[2 * j + 1]));
+  else
+    return word_values<XT>(x.w[j]);
+}
+
 template <int XT, bool GATHER>
-__global__ void __launch_bounds__(kThreads, XT == E_FP32 ? 2 : 4) columns_kernel(ColumnsArgs a) {
-  __shared__ float part[kThreads / 32][kTileCols];
-  const int b = blockIdx.x;
+__global__ void __launch_bounds__(kThreads, kResident<XT, GATHER>)
+    columns_kernel(ColumnsArgs a, int blocks, int each, bool early) {
+  extern __shared__ __align__(16) uint8_t stages[];
+  constexpr int STAGES = kStages<GATHER>;
+  constexpr int kWords = kEightBytes<XT> / 4;          // of a thread's eight columns
+  constexpr int kTileWords = kWords * kColumnThreads;  // of a tile's row
+  __shared__ __align__(16) uint32_t part[2][kThreads / 32][kTileWords];
+  __shared__ __align__(16) float inverse[2][kTileCols];
+  __shared__ int counts[kThreads / 32];
+  const int stripe = blockIdx.x / blocks, b = blockIdx.x - stripe * blocks;
+  begin_early(early);
   // the groups whose first block is b or before it; a group's first block grows with the group
   int before = 0;
   for (int e = threadIdx.x; e < a.E; e += kThreads) before += a.offsets[e] / kBlockRows + e <= b;
 #pragma unroll
   for (int d = 16; d > 0; d /= 2) before += __shfl_xor_sync(0xffffffffu, before, d);
-  __shared__ int counts[kThreads / 32];
   if (threadIdx.x % 32 == 0) counts[threadIdx.x / 32] = before;
   __syncthreads();
   int e = -1;
 #pragma unroll
   for (int i = 0; i < kThreads / 32; ++i) e += counts[i];
-  if (blockIdx.x == 0 && blockIdx.y == 0 && threadIdx.x < 32) {
+  if (blockIdx.x == 0 && threadIdx.x < 32) {
     int64_t unused;
     const int status = check_groups<1>(a.offsets, nullptr, a.E, a.E, a.M_total, unused);
     if (status && threadIdx.x == 0) atomicCAS(a.err, 0, status);
@@ -79,101 +139,149 @@ __global__ void __launch_bounds__(kThreads, XT == E_FP32 ? 2 : 4) columns_kernel
   const int rows = r1 - first < kBlockRows ? (int)(r1 - first) : kBlockRows;
 
   const int c = threadIdx.x % kColumnThreads, i0 = threadIdx.x / kColumnThreads;
-  const int col = blockIdx.y * kTileCols + 8 * c;
   constexpr int kBytes = XT == E_FP32 ? 4 : 2;
-  int64_t from[kRowsEach];
+  const int tile0 = stripe * each;
+  const int tiles = min(each, a.K / kTileCols - tile0);
+  // the rows' elements of the tile that is fetched next; rows that hold nothing are filled with
+  // zeros and read nothing (16 bytes or none)
+  const char* from[kRowsEach];
+  uint32_t bytes[kRowsEach];
 #pragma unroll
   for (int j = 0; j < kRowsEach; ++j) {
     const int i = i0 + j * kRowThreads;
-    from[j] = -1;
+    int64_t row = -1;
     if (i < rows) {
+      row = first + i;
       if constexpr (GATHER) {
-        const int slot = a.slot_of_row[first + i];
-        from[j] = slot < 0 ? -1 : slot / a.top_k;
-      } else {
-        from[j] = first + i;
+        const int slot = a.slot_of_row[row];
+        row = slot < 0 ? -1 : slot / a.top_k;
+        if (row >= a.x_rows) {
+          atomicCAS(a.err, 0, DEV_BAD_ROWS);
+          row = -1;
+        }
       }
     }
+    bytes[j] = row < 0 ? 0 : 16;
+    from[j] = static_cast<const char*>(a.x) + ((row < 0 ? 0 : row) * a.K + tile0 * kTileCols + 8 * c) * kBytes;
   }
-  Eight<XT> x[kRowsEach];
+  uint8_t* const mine = stages + threadIdx.x * kEightBytes<XT>;  // + stage, + row j
+  const uint32_t mine_u32 = smem_u32(mine);
+  auto fetch = [&](bool any, int stage) {
+    if (any) {
+      const uint32_t dst = mine_u32 + stage * kStageBytes<XT>;
 #pragma unroll
-  for (int j = 0; j < kRowsEach; ++j) {
-    if constexpr (GATHER) {
-      if (from[j] >= a.x_rows) {
-        atomicCAS(a.err, 0, DEV_BAD_ROWS);
-        from[j] = -1;
+      for (int j = 0; j < kRowsEach; ++j) {
+#pragma unroll
+        for (int h = 0; h < kEightBytes<XT>; h += 16)
+          cp_async_16(dst + j * kThreads * kEightBytes<XT> + h, from[j] + h, bytes[j]);
+        from[j] += kTileCols * kBytes;
       }
     }
+    cp_async_commit();
+  };
 #pragma unroll
-    for (uint32_t& w : x[j].w) w = 0;
-    if (from[j] >= 0)
-      load_words<sizeof(Eight<XT>) / 4>(
-          static_cast<const char*>(a.x) + (from[j] * a.K + col) * kBytes, x[j].w);
-  }
-  float top[8] = {};
+  for (int s = 0; s < STAGES - 1; ++s) fetch(s < tiles, s);
+  const uint64_t pol = l2_policy_evict_first();  // x is what is read again, by other slots
+  uint8_t* q = a.q + (first + i0) * a.K + tile0 * kTileCols + 8 * c;
+  float* scale_at = a.scales + (int64_t)b * a.K + tile0 * kTileCols;
+  const int64_t q_rows = (int64_t)kRowThreads * a.K;
+  const bool full = rows == kBlockRows;
+  int stage = 0, side = 0;
+  for (int tile = 0; tile < tiles; ++tile, side ^= 1, q += kTileCols, scale_at += kTileCols) {
+    fetch(tile + STAGES - 1 < tiles, stage == 0 ? STAGES - 1 : stage - 1);
+    cp_async_wait_group<STAGES - 1>();
+    Eight<XT> x[kRowsEach], top = {};
 #pragma unroll
-  for (int j = 0; j < kRowsEach; j += 2) {
-    float v[8], u[8];
-    unpack<XT>(x[j], v);
-    unpack<XT>(x[j + 1], u);
+    for (int j = 0; j < kRowsEach; ++j)
+      x[j] = read8<XT>(mine + stage * kStageBytes<XT> + j * kThreads * kEightBytes<XT>);
+    if (++stage == STAGES) stage = 0;
 #pragma unroll
-    for (int k = 0; k < 8; ++k) top[k] = max3_nan(top[k], fabsf(v[k]), fabsf(u[k]));
-  }
+    for (int j = 0; j < kRowsEach; j += 2) take_max<XT>(top, x[j], x[j + 1]);
 #pragma unroll
-  for (int k = 0; k < 8; ++k) top[k] = max_nan(top[k], __shfl_xor_sync(0xffffffffu, top[k], 16));
-  if (threadIdx.x % 32 < kColumnThreads) {
-    float4* p = reinterpret_cast<float4*>(&part[threadIdx.x / 32][8 * c]);
-    p[0] = make_float4(top[0], top[1], top[2], top[3]);
-    p[1] = make_float4(top[4], top[5], top[6], top[7]);
-  }
-  __syncthreads();
-  if (threadIdx.x < kTileCols) {  // one column each: its scale, and the scale's reciprocal
-    float m = part[0][threadIdx.x];
+    for (int i = 0; i < kWords; ++i)
+      top.w[i] = max_words<XT>(top.w[i], __shfl_xor_sync(0xffffffffu, top.w[i], 16));
+    if (threadIdx.x % 32 < kColumnThreads) {
+      uint4* p = reinterpret_cast<uint4*>(&part[side][threadIdx.x / 32][kWords * c]);
 #pragma unroll
-    for (int w = 1; w < kThreads / 32; ++w) m = max_nan(m, part[w][threadIdx.x]);
-    const bool finite = m < __int_as_float(0x7f800000);
-    const float scale = m == 0.0f ? 1.0f : fmaxf(__fdiv_rn(m, 448.0f), 0x1p-126f);
-    a.scales[(int64_t)b * a.K + blockIdx.y * kTileCols + threadIdx.x] =
-        finite ? scale : __int_as_float(0x7fffffff);
-    part[0][threadIdx.x] = finite ? __frcp_rn(scale) : 0.0f;
-  }
-  __syncthreads();
-  float inv[8];
-  {
-    const float4* p = reinterpret_cast<const float4*>(&part[0][8 * c]);
-    const float4 lo = p[0], hi = p[1];
-    inv[0] = lo.x; inv[1] = lo.y; inv[2] = lo.z; inv[3] = lo.w;
-    inv[4] = hi.x; inv[5] = hi.y; inv[6] = hi.z; inv[7] = hi.w;
-  }
+      for (int i = 0; i < kWords / 4; ++i)
+        p[i] = make_uint4(top.w[4 * i], top.w[4 * i + 1], top.w[4 * i + 2], top.w[4 * i + 3]);
+    }
+    __syncthreads();
+    if (threadIdx.x < kTileWords) {  // a word's columns each: their scales and those's reciprocals
+      uint32_t m = part[side][0][threadIdx.x];
 #pragma unroll
-  for (int j = 0; j < kRowsEach; ++j) {
-    const int i = i0 + j * kRowThreads;
-    if (i >= rows) break;
-    float v[8];
-    unpack<XT>(x[j], v);
+      for (int w = 1; w < kThreads / 32; ++w) m = max_words<XT>(m, part[side][w][threadIdx.x]);
+      const float2 amax = word_values<XT>(m);
+      constexpr int kCols = XT == E_FP32 ? 1 : 2;
 #pragma unroll
-    for (int k = 0; k < 8; ++k) v[k] *= inv[k];
-    const uint32_t lo = cvt_e4m3x2(v[0], v[1]) | (cvt_e4m3x2(v[2], v[3]) << 16);
-    const uint32_t hi = cvt_e4m3x2(v[4], v[5]) | (cvt_e4m3x2(v[6], v[7]) << 16);
-    *reinterpret_cast<uint2*>(a.q + (first + i) * a.K + col) = make_uint2(lo, hi);
+      for (int i = 0; i < kCols; ++i) {
+        const float a_i = i ? amax.y : amax.x;
+        const int col = threadIdx.x * kCols + i;
+        const bool finite = a_i < __int_as_float(0x7f800000);
+        const float scale = a_i == 0.0f ? 1.0f : fmaxf(__fdiv_rn(a_i, 448.0f), 0x1p-126f);
+        scale_at[col] = finite ? scale : __int_as_float(0x7fffffff);
+        inverse[side][col] = finite ? __frcp_rn(scale) : 0.0f;
+      }
+    }
+    __syncthreads();
+    const float4 lo = *reinterpret_cast<const float4*>(&inverse[side][8 * c]);
+    const float4 hi = *reinterpret_cast<const float4*>(&inverse[side][8 * c + 4]);
+    const float2 inv[4] = {{lo.x, lo.y}, {lo.z, lo.w}, {hi.x, hi.y}, {hi.z, hi.w}};
+    auto store = [&](int j, uint8_t* to) {
+      uint32_t code[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        float2 v = pair<XT>(x[j], i);
+        mul2(v.x, v.y, inv[i].x, inv[i].y, v.x, v.y);
+        code[i] = cvt_e4m3x2(v.x, v.y);
+      }
+      st_global_v2_hint(to, code[0] | (code[1] << 16), code[2] | (code[3] << 16), pol);
+    };
+    uint8_t* to = q;
+    if (full) {
+#pragma unroll
+      for (int j = 0; j < kRowsEach; ++j, to += q_rows) store(j, to);
+    } else {
+#pragma unroll
+      for (int j = 0; j < kRowsEach; ++j, to += q_rows)
+        if (i0 + j * kRowThreads < rows) store(j, to);
+    }
   }
 }
 
-template <int XT>
+template <int XT, bool GATHER>
 cudaError_t columns_as(const ColumnsArgs& a, cudaStream_t stream) {
-  const dim3 grid((unsigned)(a.M_total / kBlockRows + a.E), (unsigned)(a.K / kTileCols));
-  if (a.slot_of_row) columns_kernel<XT, true><<<grid, kThreads, 0, stream>>>(a);
-  else columns_kernel<XT, false><<<grid, kThreads, 0, stream>>>(a);
-  return cudaGetLastError();
+  // A stripe of columns for all row blocks, then the next: what is gathered several times stays in
+  // L2 that long.  A block's way to its rows (offsets, slots, rows) is three round trips to L2, so
+  // stripes are no narrower than it takes to keep the SMs busy to the end.
+  constexpr int64_t kBlocks = 2500;
+  constexpr int kSmem = kStages<GATHER> * kStageBytes<XT>;
+  static std::atomic<bool> attr_set[64];  // per device; several host threads may launch
+  int dev = 0;
+  cudaGetDevice(&dev);
+  if (dev >= 64 || !attr_set[dev].load(std::memory_order_acquire)) {
+    const cudaError_t e = cudaFuncSetAttribute(columns_kernel<XT, GATHER>,
+                                               cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
+    if (e != cudaSuccess) return e;
+    if (dev < 64) attr_set[dev].store(true, std::memory_order_release);
+  }
+  const int64_t blocks = a.M_total / kBlockRows + a.E;
+  const int tiles = a.K / kTileCols;
+  const int64_t want = (kBlocks + blocks - 1) / blocks;
+  const int each = (int)((tiles + want - 1) / want);
+  const dim3 grid((unsigned)(blocks * ((tiles + each - 1) / each)));
+  const bool early = starts_early(grid, (int64_t)kBlockRows * kTileCols * 3 * each);
+  return launch(columns_kernel<XT, GATHER>, grid, kThreads, kSmem, early, stream, 1, a, (int)blocks, each, early);
 }
 
 }  // namespace
 
 cudaError_t launch_quantize_columns(int x_type, const ColumnsArgs& a, cudaStream_t stream) {
+  const bool gather = a.slot_of_row != nullptr;
   switch (x_type) {
-    case E_BF16: return columns_as<E_BF16>(a, stream);
-    case E_FP16: return columns_as<E_FP16>(a, stream);
-    default: return columns_as<E_FP32>(a, stream);
+    case E_BF16: return gather ? columns_as<E_BF16, true>(a, stream) : columns_as<E_BF16, false>(a, stream);
+    case E_FP16: return gather ? columns_as<E_FP16, true>(a, stream) : columns_as<E_FP16, false>(a, stream);
+    default: return gather ? columns_as<E_FP32, true>(a, stream) : columns_as<E_FP32, false>(a, stream);
   }
 }
 

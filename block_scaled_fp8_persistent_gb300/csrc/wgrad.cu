@@ -14,9 +14,24 @@
 // stage to the MMA thread; MMA steps that hold no row of the group are not issued.
 //
 // Sums: a chunk of rows accumulates in TMEM (fp8: the 128 rows of a scale block; 16-bit operands:
-// CHUNK rows), and the epilogue warps add the chunks into fp32 registers, scaled by sc[n] * sa[k].
-// The tensor core's own additions do not round to nearest; chunks keep them few (see CHUNK).
-// Two chunks are in TMEM at a time, so that the MMAs of the next run meanwhile.
+// 512 rows), and the epilogue warps add the chunks into fp32 registers, scaled by sc[n] * sa[k].
+// The tensor core's additions do not round to nearest, and their errors add up: of 65536 rows in
+// one chunk the sum is off by 7.6e-5 of its norm, in chunks of 2048 by 2.1e-6, of 512 by 5e-7, as
+// a plain fp32 sum; chunks of 512 cost 3 % of the time of one.  Two chunks are in TMEM at a time,
+// so that the MMAs of the next run meanwhile.
+//
+// What bounds it: 16-bit, the tensor core (65536 rows, 2048 x 4608: 795 us, 1555 TFLOP/s with 144
+// tiles for 76 pairs) or, with few rows per expert, the gradients' bytes (16384 rows over 64
+// experts of 2048 x 7168 to fp32: 617 us, 6.6 TB/s).  8 bits, the epilogue: 2 operations for each
+// element of a 128-row block on the FMA pipe beside 512 clocks of MMA (the same rows: 579 us, 2136
+// TFLOP/s; without the scales' products 500, without any sums 440).  What made it so: the scales
+// land with the operands, counted on their barrier (read from global memory two blocks ahead, the
+// epilogue waited for them: 826 us); a warp reads TMEM as 16 x 256-bit pieces, of which a thread
+// gets 4 rows x 32 columns, 36 scales, and not a row of 128 columns, 129 (shared memory is what the
+// MMA is fed from: 740 -> 646); the pieces are double-buffered, with registers to hold them (589);
+// the roles that wait beside the epilogue sleep in their barriers (16-bit: 880 -> 785).  Four
+// stages: with six the loads of operands run so far ahead that they stand in the way of the
+// gradients' stores (745 -> 617 us).
 //
 // Roles (12 warps): warp 0 TMA producer; warp 1 TMEM owner and, in CTA 0 of a pair, the MMA thread;
 // warp 2 fixer; warps 4-11 epilogue (TMEM lanes 32 * (w % 4)..: columns n of dC; half of the tile's
@@ -33,6 +48,7 @@ constexpr int EPI_WARP0 = 4;
 constexpr int BN = 256;  // columns k of a tile
 constexpr uint32_t TMEM_COLS = 512;
 
+// CHUNK: stages of 64 rows that accumulate in TMEM, of 16-bit operands
 template <bool FP8_, int CG_, int STAGES_, int CHUNK_>
 struct Cfg {
   static constexpr bool FP8 = FP8_;
@@ -47,13 +63,20 @@ struct Cfg {
   static constexpr int M_BOXES = 128 / BOX_COLS;         // of dC per CTA
   static constexpr int N_BOXES = BN / CG / BOX_COLS;     // of A per CTA
   static constexpr uint32_t STAGE = (M_BOXES + N_BOXES) * BOX;
+  static constexpr uint32_t STAGE_TX = STAGE + (FP8 ? (BN + 128) * 4 : 0);  // and its scales
   static constexpr uint32_t STEP_BYTES = STEP * 128;
+  // registers of the role warps and of the epilogue warps, of the 168 each is launched with
+  static constexpr int ROLE_REGS = 40;
+  static constexpr int SUM_REGS = 232;
+  static_assert(4 * ROLE_REGS + 8 * SUM_REGS <= 12 * 168, "the launch's registers");
   static constexpr uint32_t IDESC =
       (FP8 ? idesc_f8f6f4_e4m3(BM, BN) : idesc_f16_f32(BM, BN)) | IDESC_A_MN | IDESC_B_MN;
-  // scales of a chunk's 128 columns k, per epilogue warp: fetched two chunks ahead
-  static constexpr int SA_SLOTS = 4;
-  static constexpr uint32_t SMEM_SA = STAGES * STAGE;
-  static constexpr uint32_t SMEM_CTL = SMEM_SA + (FP8 ? 8 * SA_SLOTS * 128 * 4 : 0);
+  // fp8: slots of a stage's scales, [256 columns k | 128 columns n] (see the producer)
+  static constexpr int SLOTS = 8;
+  static constexpr uint32_t SLOT = (BN + 128) * 4;
+  static constexpr uint32_t SMEM_SF = STAGES * STAGE;
+  static constexpr uint32_t SMEM_CTL = SMEM_SF + (FP8 ? SLOTS * SLOT : 0);
+  static_assert(!FP8 || SLOTS >= STAGES + 2, "a slot is read to the end before it is filled again");
 };
 
 template <class C>
@@ -77,30 +100,33 @@ constexpr uint32_t smem_bytes() {
 
 // Tiles are numbered expert by expert, inside one in bands of 8 column tiles of dC, whose columns
 // of dC and A stay in L2 while the band's tiles are in flight.  An expert without rows has tiles
-// too: its gradient is written.
-struct Tile {
-  int e, n0, k0;
-  int64_t r0;
-  int rows;
+// too: its gradient is written.  A role walks the tiles `stride` apart; the walk is a few integers
+// (the roles' warps have few registers).
+struct Shape {
+  uint32_t experts, nt, kt;  // tiles per side of an expert's matrix
 };
 
-template <class C>
-__device__ __forceinline__ Tile tile_at(const WgradArgs& a, int64_t t) {
-  constexpr int BAND = 8;
-  const int nt = (a.N + C::BM - 1) / C::BM, kt = (a.K + BN - 1) / BN;
-  const int64_t per = (int64_t)nt * kt;
-  Tile x;
-  x.e = (int)(t / per);
-  const int64_t local = t - x.e * per;
-  const int band = (int)(local / ((int64_t)BAND * kt));
-  const int in_band = (int)(local - (int64_t)band * BAND * kt);
-  const int high = nt - band * BAND < BAND ? nt - band * BAND : BAND;
-  x.n0 = (band * BAND + in_band % high) * C::BM;
-  x.k0 = in_band / high * BN;
-  x.r0 = a.offsets[x.e];
-  x.rows = (int)(a.offsets[x.e + 1] - x.r0);
-  return x;
-}
+struct Walk {
+  uint32_t e = 0, local;
+  __device__ explicit Walk(uint32_t first) : local(first) {}
+  __device__ bool inside(const Shape& s) {  // and to the tile's expert
+    const uint32_t per = s.nt * s.kt;
+    while (local >= per && e < s.experts) {
+      local -= per;
+      ++e;
+    }
+    return e < s.experts;
+  }
+  __device__ int rows(const WgradArgs& a) const { return a.offsets[e + 1] - a.offsets[e]; }
+  template <int BM>
+  __device__ void corner(const Shape& s, int& n0, int& k0) const {
+    constexpr uint32_t BAND = 8;
+    const uint32_t band = local / (BAND * s.kt), in_band = local - band * BAND * s.kt;
+    const uint32_t high = s.nt - band * BAND < BAND ? s.nt - band * BAND : BAND;
+    n0 = (int)((band * BAND + in_band % high) * BM);
+    k0 = (int)(in_band / high * BN);
+  }
+};
 
 __device__ __forceinline__ float2 mul_f32x2(float2 a, float2 b) {
   float2 r;
@@ -112,27 +138,56 @@ __device__ __forceinline__ float2 mul_f32x2(float2 a, float2 b) {
   return r;
 }
 
-// Eight columns of a row of dB, `left` of which are the matrix's (8 or more: all).
+// v[j] of lane 4 r + q becomes v[q] of lane 4 r + j.
+__device__ __forceinline__ void quad_transpose(float2 (&v)[4], uint32_t lane) {
+#pragma unroll
+  for (int d = 1; d <= 2; d *= 2) {
+    const bool up = (lane & d) != 0;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      if (j & d) continue;
+      // the lower lane gives its v[j + d] for the upper one's v[j]
+      float2 out = up ? v[j] : v[j + d];
+      out.x = __shfl_xor_sync(0xffffffffu, out.x, d);
+      out.y = __shfl_xor_sync(0xffffffffu, out.y, d);
+      if (up) v[j] = out;
+      else v[j + d] = out;
+    }
+  }
+}
+
+// Eight columns of a row of a 16-bit add; not the read-only path, as add may be dB.
 template <int OUT>
-__device__ __forceinline__ void store8(const WgradArgs& a, int64_t at, const float2* v,
-                                       bool wide, uint64_t pol) {
-  float f[8];
+__device__ __forceinline__ void load8(const void* add, int64_t at, float2 (&v)[4]) {
+  uint32_t w[4];
+  asm volatile("ld.global.v4.b32 {%0, %1, %2, %3}, [%4];"
+               : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3])
+               : "l"(static_cast<const uint16_t*>(add) + at));
 #pragma unroll
   for (int j = 0; j < 4; ++j) {
-    f[2 * j] = v[j].x;
-    f[2 * j + 1] = v[j].y;
-  }
-  if constexpr (OUT == GRAD_FP32) {
-    if (a.add) {
-      const float4* s = reinterpret_cast<const float4*>(static_cast<const float*>(a.add) + at);
-      const float4 x = s[0], y = s[1];
-      f[0] += x.x; f[1] += x.y; f[2] += x.z; f[3] += x.w;
-      f[4] += y.x; f[5] += y.y; f[6] += y.z; f[7] += y.w;
+    if constexpr (OUT == GRAD_BF16) {
+      v[j] = make_float2(__uint_as_float(w[j] << 16), __uint_as_float(w[j] & 0xffff0000u));
+    } else {
+      asm("{\n\t.reg .f16 l, h;\n\tmov.b32 {l, h}, %2;\n\t"
+          "cvt.f32.f16 %0, l;\n\tcvt.f32.f16 %1, h;\n\t}"
+          : "=f"(v[j].x), "=f"(v[j].y)
+          : "r"(w[j]));
     }
+  }
+}
+
+// Eight columns of a row of dB.
+template <int OUT>
+__device__ __forceinline__ void store8(void* dB, int64_t at, const float2 (&v)[4], bool wide,
+                                       uint64_t pol) {
+  if constexpr (OUT == GRAD_FP32) {
     uint32_t w[8];
 #pragma unroll
-    for (int j = 0; j < 8; ++j) w[j] = __float_as_uint(f[j]);
-    float* d = static_cast<float*>(a.dB) + at;
+    for (int j = 0; j < 4; ++j) {
+      w[2 * j] = __float_as_uint(v[j].x);
+      w[2 * j + 1] = __float_as_uint(v[j].y);
+    }
+    float* d = static_cast<float*>(dB) + at;
     if (wide) {
       st_global_v8_hint(d, w, pol);
     } else {
@@ -140,38 +195,19 @@ __device__ __forceinline__ void store8(const WgradArgs& a, int64_t at, const flo
       st_global_v4_hint(d + 4, w[4], w[5], w[6], w[7], pol);
     }
   } else {
-    if (a.add) {
-      const uint4 s = *reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(a.add) + at);
-      const uint32_t w[4] = {s.x, s.y, s.z, s.w};
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        if constexpr (OUT == GRAD_BF16) {
-          f[2 * j] += __uint_as_float(w[j] << 16);
-          f[2 * j + 1] += __uint_as_float(w[j] & 0xffff0000u);
-        } else {
-          float lo, hi;
-          asm("{\n\t.reg .f16 l, h;\n\tmov.b32 {l, h}, %2;\n\t"
-              "cvt.f32.f16 %0, l;\n\tcvt.f32.f16 %1, h;\n\t}"
-              : "=f"(lo), "=f"(hi)
-              : "r"(w[j]));
-          f[2 * j] += lo;
-          f[2 * j + 1] += hi;
-        }
-      }
-    }
     uint32_t w[4];
 #pragma unroll
     for (int j = 0; j < 4; ++j)
-      w[j] = OUT == GRAD_BF16 ? pack_bf16x2(f[2 * j], f[2 * j + 1])
-                              : pack_f16x2(f[2 * j], f[2 * j + 1]);
-    st_global_v4_hint(static_cast<uint16_t*>(a.dB) + at, w[0], w[1], w[2], w[3], pol);
+      w[j] = OUT == GRAD_BF16 ? pack_bf16x2(v[j].x, v[j].y) : pack_f16x2(v[j].x, v[j].y);
+    st_global_v4_hint(static_cast<uint16_t*>(dB) + at, w[0], w[1], w[2], w[3], pol);
   }
 }
 
 template <class C, int OUT>
 __global__ void __launch_bounds__(THREADS, 1)
 wgrad_kernel(const __grid_constant__ CUtensorMap tmC, const __grid_constant__ CUtensorMap tmA,
-             const WgradArgs args, const int64_t total_tiles) {
+             const __grid_constant__ CUtensorMap tmSC, const __grid_constant__ CUtensorMap tmSA,
+             const WgradArgs args, const Shape shape) {
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                              ~static_cast<uintptr_t>(1023));
@@ -180,8 +216,8 @@ wgrad_kernel(const __grid_constant__ CUtensorMap tmC, const __grid_constant__ CU
   const uint32_t warp = threadIdx.x >> 5;
   const uint32_t lane = threadIdx.x & 31;
   const uint32_t rank = C::CG == 2 ? cluster_ctarank() : 0;
-  const int64_t tile0 = blockIdx.x / C::CG;
-  const int64_t tile_stride = gridDim.x / C::CG;
+  const uint32_t tile0 = blockIdx.x / C::CG;  // the grid has no more pairs than there are tiles
+  const uint32_t tile_stride = gridDim.x / C::CG;
 
   if (warp == 0) {
     int64_t unused;
@@ -193,7 +229,7 @@ wgrad_kernel(const __grid_constant__ CUtensorMap tmC, const __grid_constant__ CU
     }
   }
   __syncthreads();
-  if (!ctl->valid || tile0 >= total_tiles) return;  // both CTAs of a pair agree
+  if (!ctl->valid) return;
 
   const uint32_t base = smem_u32(smem);
   auto full_bar = [&](int s) { return smem_u32(&ctl->full[s]); };
@@ -229,41 +265,61 @@ wgrad_kernel(const __grid_constant__ CUtensorMap tmC, const __grid_constant__ CU
   const uint32_t tmem_base = ctl->tmem_base;
 
   if (warp < EPI_WARP0) {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(C::ROLE_REGS));
     if (warp == 0 && lane == 0) {
       // ------------------------------- TMA producer -------------------------------
+      // fp8: a stage's scales go into a ring of their own, which no barrier frees: the MMAs that
+      // this stage waits for (STAGES blocks ago) began when every epilogue warp had read the
+      // partial sums, and before them the scales, of two blocks earlier.
       const uint64_t pol = l2_policy_evict_normal();
-      uint32_t stage = 0, phase = 0;
+      uint32_t stage = 0, phase = 0, slot = 0;
       int64_t issued = 0;
       bool ok = true;
-      for (int64_t t = tile0; ok && t < total_tiles; t += tile_stride) {
-        const Tile x = tile_at<C>(args, t);
-        const int col_m = x.n0 + 128 * rank, col_n = x.k0 + (BN / C::CG) * rank;
-        for (int r = 0; r < x.rows; r += C::ROWS) {
+      for (Walk t(tile0); ok && t.inside(shape); t.local += tile_stride) {
+        const int rows = t.rows(args), r0 = args.offsets[t.e];
+        int n0, k0;
+        t.corner<C::BM>(shape, n0, k0);
+        const int col_m = n0 + 128 * rank, col_n = k0 + (BN / C::CG) * rank;
+        for (int r = 0; r < rows; r += C::ROWS) {
           if (!mbar_wait_sleep(empty_bar(stage), phase ^ 1, abort)) {
             give_up(args.err, abort);
             ok = false;
             break;
           }
           const uint32_t m = base + stage * C::STAGE, n = m + C::M_BOXES * C::BOX;
-          const int32_t row = (int32_t)(x.r0 + r);
-          if (C::CG == 1 || r + C::ROWS > x.rows) {
+          const int32_t row = r0 + r;
+          const int32_t at = r0 / 128 + (int)t.e + r / 128;  // fp8: its scales' row
+          const uint32_t dst = base + C::SMEM_SF + slot * C::SLOT;
+          if (C::CG == 1 || r + C::ROWS > rows) {
             // counted in this CTA: the fixer comes first where the group ends inside
-            const uint32_t bar = r + C::ROWS > x.rows ? tail_bar(stage) : full_bar(stage);
-            mbar_arrive_expect_tx(bar, C::STAGE);
+            const uint32_t bar = r + C::ROWS > rows ? tail_bar(stage) : full_bar(stage);
+            mbar_arrive_expect_tx(bar, C::STAGE_TX);
+#pragma unroll
             for (int i = 0; i < C::M_BOXES; ++i)
               tma_load_2d_hint(m + i * C::BOX, &tmC, col_m + i * C::BOX_COLS, row, bar, pol);
+#pragma unroll
             for (int i = 0; i < C::N_BOXES; ++i)
               tma_load_2d_hint(n + i * C::BOX, &tmA, col_n + i * C::BOX_COLS, row, bar, pol);
+            if constexpr (C::FP8) {
+              tma_load_2d_hint(dst, &tmSA, k0, at, bar, pol);
+              tma_load_2d_hint(dst + BN * 4, &tmSC, col_m, at, bar, pol);
+            }
           } else {
             // both CTAs' bytes are counted on the leader's barrier
             const uint32_t bar = mapa_shared(full_bar(stage), 0);
-            if (rank == 0) mbar_arrive_expect_tx(full_bar(stage), 2 * C::STAGE);
+            if (rank == 0) mbar_arrive_expect_tx(full_bar(stage), 2 * C::STAGE_TX);
+#pragma unroll
             for (int i = 0; i < C::M_BOXES; ++i)
               tma_load_2d_pair_hint(m + i * C::BOX, &tmC, col_m + i * C::BOX_COLS, row, bar, pol);
+#pragma unroll
             for (int i = 0; i < C::N_BOXES; ++i)
               tma_load_2d_pair_hint(n + i * C::BOX, &tmA, col_n + i * C::BOX_COLS, row, bar, pol);
+            if constexpr (C::FP8) {
+              tma_load_2d_pair_hint(dst, &tmSA, k0, at, bar, pol);
+              tma_load_2d_pair_hint(dst + BN * 4, &tmSC, col_m, at, bar, pol);
+            }
           }
+          if (++slot == C::SLOTS) slot = 0;
           ++issued;
           if (++stage == C::STAGES) { stage = 0; phase ^= 1; }
         }
@@ -283,12 +339,16 @@ wgrad_kernel(const __grid_constant__ CUtensorMap tmC, const __grid_constant__ CU
       const uint64_t ndesc0 = mnmajor_sw128_desc(base + C::M_BOXES * C::BOX, C::BOX);
       uint32_t stage = 0, phase = 0, acc = 0, acc_phase = 0;
       bool ok = true;
-      for (int64_t t = tile0; ok && t < total_tiles; t += tile_stride) {
-        const Tile x = tile_at<C>(args, t);
+      for (Walk t(tile0); ok && t.inside(shape); t.local += tile_stride) {
+        const int rows = t.rows(args);
         int in_chunk = 0;
-        for (int r = 0; r < x.rows; r += C::ROWS) {
-          if (!mbar_wait(full_bar(stage), phase, abort) ||
-              (in_chunk == 0 && !mbar_wait(tempty_bar(acc), acc_phase ^ 1, abort))) {
+        for (int r = 0; r < rows; r += C::ROWS) {
+          if (!mbar_wait_sleep(full_bar(stage), phase, abort)) {
+            give_up(args.err, abort);
+            ok = false;
+            break;
+          }
+          if (in_chunk == 0 && !mbar_wait_sleep(tempty_bar(acc), acc_phase ^ 1, abort)) {
             give_up(args.err, abort);
             ok = false;
             break;
@@ -297,7 +357,7 @@ wgrad_kernel(const __grid_constant__ CUtensorMap tmC, const __grid_constant__ CU
           const uint32_t d = tmem_base + acc * BN;
           const uint64_t mdesc = mdesc0 + ((stage * C::STAGE) >> 4);
           const uint64_t ndesc = ndesc0 + ((stage * C::STAGE) >> 4);
-          const int steps = x.rows - r >= C::ROWS ? 4 : (x.rows - r + C::STEP - 1) / C::STEP;
+          const int steps = rows - r >= C::ROWS ? 4 : (rows - r + C::STEP - 1) / C::STEP;
 #pragma unroll
           for (int k = 0; k < 4; ++k) {
             if (k < steps) {
@@ -311,7 +371,7 @@ wgrad_kernel(const __grid_constant__ CUtensorMap tmC, const __grid_constant__ CU
           if constexpr (C::CG == 1) umma_commit(empty_bar(stage));
           else umma_commit_pair(empty_bar(stage), 0x3);
           if (++stage == C::STAGES) { stage = 0; phase ^= 1; }
-          if (++in_chunk == C::CHUNK || r + C::ROWS >= x.rows) {
+          if (++in_chunk == C::CHUNK || r + C::ROWS >= rows) {
             if constexpr (C::CG == 1) umma_commit(tfull_bar(acc));
             else umma_commit_pair(tfull_bar(acc), 0x3);
             in_chunk = 0;
@@ -329,10 +389,10 @@ wgrad_kernel(const __grid_constant__ CUtensorMap tmC, const __grid_constant__ CU
       // the end of the MMA step that holds it (whole 128-byte lines, whatever the swizzle).
       uint32_t stage = 0;
       uint32_t seen = 0;  // parity of every stage's tail barrier, a bit each
-      for (int64_t t = tile0; t < total_tiles; t += tile_stride) {
-        const Tile x = tile_at<C>(args, t);
-        const int stages = (x.rows + C::ROWS - 1) / C::ROWS;
-        const int left = x.rows % C::ROWS;
+      for (Walk t(tile0); t.inside(shape); t.local += tile_stride) {
+        const int rows = t.rows(args);
+        const int stages = (rows + C::ROWS - 1) / C::ROWS;
+        const int left = rows % C::ROWS;
         const uint32_t last = (stage + stages + C::STAGES - 1) % C::STAGES;
         stage = (stage + stages) % C::STAGES;
         if (left == 0) continue;
@@ -365,114 +425,152 @@ wgrad_kernel(const __grid_constant__ CUtensorMap tmC, const __grid_constant__ CU
     __syncwarp();
   } else {
     // --------------------------------- epilogue ---------------------------------
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 224;");
-    const uint32_t w = warp - EPI_WARP0;
-    const uint32_t quarter = warp & 3, half = w >> 2;
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(C::SUM_REGS));
+    const uint32_t quarter = warp & 3, half = (warp - EPI_WARP0) >> 2;
     const uint64_t pol = l2_policy_evict_first();
     const bool wide = (reinterpret_cast<uintptr_t>(args.dB) & 31) == 0 && args.K % 8 == 0;
     const uint32_t taddr0 = tmem_base + ((quarter * 32) << 16) + half * 128;
     uint32_t acc = 0, acc_phase = 0;
     bool ok = true;
 
-    // fp8: this warp's column scales go through SA_SLOTS slots of shared memory, a chunk each,
-    // and this lane's row scale through registers; both are fetched two chunks ahead, those of a
-    // tile's first two before the tile before it is stored.
-    float* sa_slots = reinterpret_cast<float*>(smem + C::SMEM_SA) + w * C::SA_SLOTS * 128;
-    uint32_t slot = 0;  // of the chunk that is added next
-    float sc_0 = 0.0f, sc_1 = 0.0f;
-    auto chunks_of = [&](const Tile& x) {
-      return (x.rows + C::ROWS * C::CHUNK - 1) / (C::ROWS * C::CHUNK);
+    uint32_t slot = 0;
+    // 16-bit chunks are long: the warps sleep, so as not to poll beside the MMA thread
+    auto wait = [&](uint32_t bar, uint32_t parity) {
+      return C::FP8 ? mbar_wait(bar, parity, abort) : mbar_wait_sleep(bar, parity, abort);
     };
-    auto fetch = [&](const Tile& x, int chunk, uint32_t to) {
-      float sc = 0.0f;
-      if (chunk < chunks_of(x)) {
-        const int64_t s = x.r0 / 128 + x.e + chunk;
-        const int n = x.n0 + 128 * (int)rank + (int)quarter * 32 + (int)lane;
-        const int k = x.k0 + (int)half * 128 + 4 * (int)lane;
-        const bool in = x.k0 + (int)half * 128 < args.K;  // K is a multiple of 128
-        cp_async_16(smem_u32(sa_slots + (to % C::SA_SLOTS) * 128 + 4 * lane),
-                    args.a_scales + s * args.K + (in ? k : 0), in ? 16 : 0);
-        if (n < args.N) sc = args.dc_scales[s * args.N + n];
-      }
-      cp_async_commit();
-      return sc;
-    };
-
-    Tile x = {};
-    if (tile0 < total_tiles) {
-      x = tile_at<C>(args, tile0);
-      if constexpr (C::FP8) {
-        sc_0 = fetch(x, 0, slot);
-        sc_1 = fetch(x, 1, slot + 1);
-      }
-    }
-    for (int64_t t = tile0; ok && t < total_tiles; t += tile_stride) {
-      float2 sum[64];
+    const uint32_t tempty_0 = C::CG == 2 ? mapa_shared(tempty_bar(0), 0) : tempty_bar(0);
+    const uint32_t tempty_1 = C::CG == 2 ? mapa_shared(tempty_bar(1), 0) : tempty_bar(1);
+    for (Walk t(tile0); t.inside(shape); t.local += tile_stride) {
+      const int rows = t.rows(args);
+      int n0, k0;
+      t.corner<C::BM>(shape, n0, k0);
+      // Rows n of lanes lane / 4 + 8 i, columns 8 g + 2 (lane % 4) and the next.  The sums begin
+      // with add, whose loads need no registers of their own here: fp32 pairs go where they
+      // belong, of 16-bit values each lane reads 8 columns of a row, and four lanes exchange
+      // theirs (as they do before dB is stored).
+      n0 += 128 * (int)rank + (int)quarter * 32 + (int)lane / 4;
+      k0 += (int)half * 128;
+      const int k8 = k0 + 8 * (int)(lane % 4);
+      float2 sum[4][4][4];
 #pragma unroll
-      for (int j = 0; j < 64; ++j) sum[j] = make_float2(0.0f, 0.0f);
-      const int chunks = chunks_of(x);
-      for (int c = 0; c < chunks; ++c) {
-        float sc = 1.0f;
-        if constexpr (C::FP8) {
-          sc = sc_0;
-          sc_0 = sc_1;
-          sc_1 = fetch(x, c + 2, slot + 2);
-          cp_async_wait_group<2>();
-          __syncwarp();
+      for (int i = 0; i < 4; ++i)
+#pragma unroll
+        for (int g = 0; g < 4; ++g)
+#pragma unroll
+          for (int j = 0; j < 4; ++j) sum[i][g][j] = make_float2(0.0f, 0.0f);
+      if (args.add) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const int64_t row = ((int64_t)t.e * args.N + n0 + 8 * i) * args.K;
+#pragma unroll
+          for (int g = 0; g < 4; ++g) {
+            if constexpr (OUT == GRAD_FP32) {
+              const float* p = static_cast<const float*>(args.add) + row + k0 + 32 * g + 2 * (lane % 4);
+#pragma unroll
+              for (int j = 0; j < 4; ++j)
+                if (n0 + 8 * i < args.N && k0 + 32 * g + 8 * j < args.K)
+                  asm volatile("ld.global.v2.f32 {%0, %1}, [%2];"
+                               : "=f"(sum[i][g][j].x), "=f"(sum[i][g][j].y)
+                               : "l"(p + 8 * j));
+            } else {
+              if (n0 + 8 * i < args.N && k8 + 32 * g < args.K)
+                load8<OUT>(args.add, row + k8 + 32 * g, sum[i][g]);
+            }
+          }
         }
-        if (!__all_sync(0xffffffffu, mbar_wait(tfull_bar(acc), acc_phase, abort))) {
-          if (lane == 0) give_up(args.err, abort);
-          ok = false;
-          break;
+        if constexpr (OUT != GRAD_FP32) {
+          // The exchange waits for the values: the next tile's go into L2 meanwhile, a line at a
+          // time (64 experts of 2048 x 7168, 256 rows each, bf16 added: 1319 -> 1058 us; fp32
+          // pairs are waited for by the first sums only, and lose by it, 1309 -> 1500).
+          Walk next = t;
+          next.local += tile_stride;
+          if (next.inside(shape)) {
+            int n, k;
+            next.corner<C::BM>(shape, n, k);
+            n += 128 * (int)rank + (int)quarter * 32 + (int)lane;
+            k += (int)half * 128;
+            const uint16_t* p = static_cast<const uint16_t*>(args.add) +
+                                ((int64_t)next.e * args.N + n) * args.K + k;
+#pragma unroll
+            for (int c = 0; c < 128; c += 64)
+              if (n < args.N && k + c < args.K) prefetch_l2(p + c);
+          }
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+#pragma unroll
+            for (int g = 0; g < 4; ++g) quad_transpose(sum[i][g], lane);
         }
+      }
+      // A chunk's 32 rows x 128 columns come in pieces of 32 columns, one in flight while the one
+      // before is added: the first of the next chunk too, so that the loads' latency is hidden but
+      // at a tile's start.  One wait is for all: the MMAs began when the stage's scales had landed.
+      // A lane that gives up goes through the motions to the tile's end, where all of them look.
+      uint32_t p[2][2][16];
+      auto load = [&](int q) {  // columns 32 q..
+        tmem_ld_16x256b_x4(taddr0 + acc * BN + 32 * q, p[q % 2][0]);
+        tmem_ld_16x256b_x4(taddr0 + (16 << 16) + acc * BN + 32 * q, p[q % 2][1]);
+      };
+      auto start = [&]() {
+        ok &= wait(tfull_bar(acc), acc_phase);
+        __syncwarp();
         tc_fence_after();
-        const float2 sc2 = make_float2(sc, sc);
-        const float4* sa = reinterpret_cast<const float4*>(sa_slots + (slot % C::SA_SLOTS) * 128);
+        load(0);
+      };
+      if (rows > 0) start();
+      for (int r = 0; r < rows; r += C::ROWS * C::CHUNK) {
+        float sc[4];
+        float2 sa[4];
+        const float* scales = reinterpret_cast<const float*>(smem + C::SMEM_SF + slot * C::SLOT);
+        const float2* sa_at = reinterpret_cast<const float2*>(scales + half * 128) + lane % 4;
+        if constexpr (C::FP8) {
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          uint32_t p[64];
-          tmem_ld_32x32b_x64(taddr0 + acc * BN + 64 * h, p);
+          for (int i = 0; i < 4; ++i) sc[i] = scales[BN + quarter * 32 + lane / 4 + 8 * i];
+        }
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          if constexpr (C::FP8) {
+#pragma unroll
+            for (int g = 0; g < 4; ++g) sa[g] = sa_at[16 * q + 4 * g];
+          }
           tmem_ld_wait();
-          if (h == 1) {  // TMEM is read: the MMA thread may have it
+          if (q < 3) {
+            load(q + 1);
+          } else {  // TMEM is read: the MMA thread may have it
             tc_fence_before();
             __syncwarp();
-            if (lane == 0)
-              mbar_arrive_cluster_or_local<C::CG>(C::CG == 2 ? mapa_shared(tempty_bar(acc), 0)
-                                                             : tempty_bar(acc));
+            if (lane == 0) mbar_arrive_cluster_or_local<C::CG>(acc ? tempty_1 : tempty_0);
+            if (++acc == 2) { acc = 0; acc_phase ^= 1; }
+            if (r + C::ROWS * C::CHUNK < rows) start();
           }
 #pragma unroll
-          for (int j = 0; j < 32; j += 2) {
-            float2 a = make_float2(__uint_as_float(p[2 * j]), __uint_as_float(p[2 * j + 1]));
-            float2 b = make_float2(__uint_as_float(p[2 * j + 2]), __uint_as_float(p[2 * j + 3]));
-            if constexpr (C::FP8) {
-              const float4 s = sa[16 * h + j / 2];
-              a = mul_f32x2(a, make_float2(s.x, s.y));
-              b = mul_f32x2(b, make_float2(s.z, s.w));
+          for (int i = 0; i < 4; ++i) {
+#pragma unroll
+            for (int g = 0; g < 4; ++g) {
+              const uint32_t* w = &p[q % 2][i / 2][4 * g + 2 * (i % 2)];
+              const float2 v = make_float2(__uint_as_float(w[0]), __uint_as_float(w[1]));
+              float2& to = sum[i][q][g];
+              if constexpr (C::FP8)
+                to = __ffma2_rn(make_float2(sc[i], sc[i]), mul_f32x2(v, sa[g]), to);
+              else
+                to = __ffma2_rn(make_float2(1.0f, 1.0f), v, to);
             }
-            sum[32 * h + j] = __ffma2_rn(sc2, a, sum[32 * h + j]);
-            sum[32 * h + j + 1] = __ffma2_rn(sc2, b, sum[32 * h + j + 1]);
           }
         }
-        ++slot;
-        if (++acc == 2) { acc = 0; acc_phase ^= 1; }
+        if (++slot == C::SLOTS) slot = 0;
       }
-      if (!ok) break;
-      const Tile now = x;
-      if (t + tile_stride < total_tiles) {
-        x = tile_at<C>(args, t + tile_stride);
-        if constexpr (C::FP8) {
-          // a tile of fewer than two chunks left later slots fetched for nothing: start behind
-          sc_0 = fetch(x, 0, slot);
-          sc_1 = fetch(x, 1, slot + 1);
-        }
+      if (!__all_sync(0xffffffffu, ok)) {
+        if (lane == 0) give_up(args.err, abort);
+        break;
       }
-      const int n = now.n0 + 128 * (int)rank + (int)quarter * 32 + (int)lane;
-      const int k0 = now.k0 + (int)half * 128;
-      if (n < args.N) {
-        const int64_t at = ((int64_t)now.e * args.N + n) * args.K + k0;
 #pragma unroll
-        for (int j = 0; j < 16; ++j)
-          if (k0 + 8 * j < args.K) store8<OUT>(args, at + 8 * j, sum + 4 * j, wide, pol);
+      for (int i = 0; i < 4; ++i) {
+        const int64_t at = ((int64_t)t.e * args.N + n0 + 8 * i) * args.K + k8;
+#pragma unroll
+        for (int g = 0; g < 4; ++g) {
+          quad_transpose(sum[i][g], lane);
+          if (n0 + 8 * i < args.N && k8 + 32 * g < args.K)
+            store8<OUT>(args.dB, at + 32 * g, sum[i][g], wide, pol);
+        }
       }
     }
   }
@@ -497,6 +595,14 @@ cudaError_t launch(const WgradArgs& args, int num_sms, cudaStream_t stream) {
   if (!encode_swizzled(&tmC, C::FP8, args.M_total > 0 ? args.dC : args.dB, 2, c_dims, C::ROWS) ||
       !encode_swizzled(&tmA, C::FP8, args.M_total > 0 ? args.A : args.dB, 2, a_dims, C::ROWS))
     return cudaErrorInvalidValue;
+  CUtensorMap tmSC = {}, tmSA = {};
+  if constexpr (C::FP8) {
+    const uint64_t blocks = args.M_total / 128 + args.E;
+    const bool any = args.M_total > 0;
+    if (!encode_rows_f32(&tmSC, any ? args.dc_scales : args.dB, args.N, any ? blocks : 1, 128) ||
+        !encode_rows_f32(&tmSA, any ? args.a_scales : args.dB, args.K, any ? blocks : 1, BN))
+      return cudaErrorInvalidValue;
+  }
   static std::atomic<bool> attr_set[64];  // per device; several host threads may launch
   int dev = 0;
   cudaGetDevice(&dev);
@@ -507,7 +613,9 @@ cudaError_t launch(const WgradArgs& args, int num_sms, cudaStream_t stream) {
     if (e != cudaSuccess) return e;
     if (dev < 64) attr_set[dev].store(true, std::memory_order_release);
   }
-  const int64_t tiles = (int64_t)args.E * ((args.N + C::BM - 1) / C::BM) * ((args.K + BN - 1) / BN);
+  const Shape shape = {(uint32_t)args.E, (uint32_t)((args.N + C::BM - 1) / C::BM),
+                       (uint32_t)((args.K + BN - 1) / BN)};
+  const int64_t tiles = (int64_t)shape.experts * shape.nt * shape.kt;
   const int64_t units = num_sms / C::CG;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)((tiles < units ? tiles : units) * C::CG));
@@ -520,7 +628,7 @@ cudaError_t launch(const WgradArgs& args, int num_sms, cudaStream_t stream) {
   attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, wgrad_kernel<C, OUT>, tmC, tmA, args, tiles);
+  return cudaLaunchKernelEx(&cfg, wgrad_kernel<C, OUT>, tmC, tmA, tmSC, tmSA, args, shape);
 }
 
 template <class C>
@@ -535,8 +643,8 @@ cudaError_t by_type(const WgradArgs& a, int num_sms, cudaStream_t stream) {
 }  // namespace wg
 
 cudaError_t launch_wgrad(const WgradArgs& a, int num_sms, cudaStream_t stream) {
-  return a.fp8 ? wg::by_type<wg::Cfg<true, 2, 6, 1>>(a, num_sms, stream)
-               : wg::by_type<wg::Cfg<false, 2, 6, 8>>(a, num_sms, stream);
+  return a.fp8 ? wg::by_type<wg::Cfg<true, 2, 4, 1>>(a, num_sms, stream)
+               : wg::by_type<wg::Cfg<false, 2, 4, 8>>(a, num_sms, stream);
 }
 
 }  // namespace bsfp8

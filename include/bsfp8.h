@@ -451,8 +451,8 @@ bsfp8_status bs16_grouped_wgrad(int type, int out_type, const void* dC, const vo
  * Block t of group e holds its rows 128 t .. 128 t + 127 (the last block fewer), and
  * s = group_offsets[e] / 128 + e (integer division): scales of M_total / 128 + num_experts rows
  * hold every block of any partition.  dc_scales fp32 [M_total / 128 + num_experts, N], a_scales
- * the same of K.  dB and add are of out_type (a bsmx_type).  N and K are multiples of 128;
- * a_scales 16-byte aligned, dc_scales 4-byte.  The rest is as for bs16_grouped_wgrad.
+ * the same of K, both 16-byte aligned.  dB and add are of out_type (a bsmx_type).  N and K are
+ * multiples of 128.  The rest is as for bs16_grouped_wgrad.
  */
 bsfp8_status bsfp8_grouped_wgrad(int out_type, const void* dC, const void* A,
                                  const float* dc_scales, const float* a_scales,
