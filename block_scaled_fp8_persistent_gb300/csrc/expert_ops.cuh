@@ -5,9 +5,11 @@
 #pragma once
 #include <cuda.h>
 #include <cuda_runtime.h>
+#include <atomic>
 #include <cstdint>
 
 #include "common.cuh"
+#include "moe_ops.cuh"
 #include "ptx.cuh"
 
 namespace bsfp8 {
@@ -78,6 +80,43 @@ struct ColumnsArgs {
 };
 cudaError_t launch_quantize_columns(int x_type, const ColumnsArgs& a, cudaStream_t stream);
 
+// Launches a persistent kernel in clusters of `cluster` blocks, one block to an SM.  It starts while
+// the one before it on the stream is still running (moe_ops.cuh): barriers, tensor memory and
+// tensor maps are ready by the time its inputs are.  It lets the next one do so once it has its
+// tensor memory, so that no kernel that waits for it can hold what it needs.
+template <typename... Params, typename... Args>
+cudaError_t launch_persistent(void (*kernel)(Params...), int64_t units, int cluster, int threads,
+                              size_t smem, cudaStream_t stream, const Args&... args) {
+  cudaLaunchAttribute attrs[2] = {};
+  attrs[0].id = cudaLaunchAttributeClusterDimension;
+  attrs[0].val.clusterDim.x = cluster;
+  attrs[0].val.clusterDim.y = attrs[0].val.clusterDim.z = 1;
+  attrs[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attrs[1].val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)(units * cluster));
+  cfg.blockDim = dim3(threads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = stream;
+  cfg.attrs = attrs;
+  cfg.numAttrs = 2;
+  return cudaLaunchKernelEx(&cfg, kernel, args...);
+}
+
+// A kernel's limit of dynamic shared memory, set once per device (several host threads may call).
+template <auto kernel>
+cudaError_t allow_smem(size_t bytes) {
+  static std::atomic<bool> set[64];
+  int dev = 0;
+  const cudaError_t got = cudaGetDevice(&dev);
+  if (got != cudaSuccess) return got;
+  if (dev < 64 && set[dev].load(std::memory_order_acquire)) return cudaSuccess;
+  const cudaError_t e =
+      cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
+  if (e == cudaSuccess && dev < 64) set[dev].store(true, std::memory_order_release);
+  return e;
+}
+
 // ---------------------------------------------------------------------------------------
 // device side
 // ---------------------------------------------------------------------------------------
@@ -94,14 +133,13 @@ __device__ __forceinline__ int check_groups(const int32_t* off, const int32_t* i
   long long tiles = 0;
   for (int e = (int)lane; e < E; e += 32) {
     const int a = off[e], b = off[e + 1];
-    if (a < 0 || b < a || b > M_total) good = 0;
+    if (a < 0 || b < a || b > M_total || (e == 0 && a != 0)) good = 0;
     else tiles += (b - a + BM - 1) / BM;
     if (ids) {
       const int x = ids[e];
       if (x < 0 || x >= num_experts) good_ids = 0;
     }
   }
-  if (lane == 0 && off[0] != 0) good = 0;
   for (int s = 16; s > 0; s >>= 1) tiles += __shfl_xor_sync(0xffffffffu, tiles, s);
   row_tiles = tiles;
   return !__all_sync(0xffffffffu, good)       ? DEV_BAD_OFFSETS

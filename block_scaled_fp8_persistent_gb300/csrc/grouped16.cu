@@ -9,16 +9,17 @@
 // reads zeros and not the next expert; rows of A past a group's end belong to its neighbour, give
 // rows of the tile that are not stored, and touch no others.
 //
-// Roles (6 warps): warp 0 TMA producer; warp 1 TMEM owner and, in CTA 0, the MMA thread (per 64 K
-// four MMAs of K = 16 and one commit); warps 2-5 epilogue, TMEM lanes 32 * (w % 4)..: rows of
-// C, which are stored as 32-byte sectors while the next tile accumulates in the other half of
-// TMEM.
-//
-// Tiles: a CTA pair takes 256 rows x 256 columns (each CTA 128 rows and half of B); one CTA 128 x
-// 256 or 32 x 128.  With few rows per expert the weights' bytes bound the product, and what counts
-// is how many of them are in flight: tiles of 32 rows keep 8 stages of 16 KB of weights per SM, and
-// the MMA computes 128 rows of which the last 96 (whatever follows in shared memory) are not read.
-#include <atomic>
+// Two kernels, for what bounds them:
+//   few rows per expert: the weights' bytes.  One CTA takes 32 rows x 128 columns, and what counts is
+//   how many bytes are in flight: 9 stages of 16 KB of weights per SM.  The MMA (M = 128 rows of A)
+//   computes 96 rows that nobody reads.  2091 rows over 128 experts of 4096 x 2048: 323 us, 6.7 TB/s,
+//   99 % of the measured copy.  Where the tiles are fewer than the SMs, clusters of CTAs share a
+//   tile's K and add up their parts through distributed shared memory.
+//   more rows: the tensor core, and the way from L2 to it.  A CTA pair takes 256 columns x up to 512
+//   rows; the rows are the MMA's N, which goes by 16, so that a group's last rows cost what they are.
+//   8192^3: 560 us, 1960 TFLOP/s (a library product 557).
+// In both: a TMA producer, an MMA thread (per 64 K four MMAs of K = 16 and one commit) and epilogue
+// warps that store one tile while the next accumulates in the other half of TMEM.
 #include "expert_ops.cuh"
 #include "ptx.cuh"
 #include "sched.cuh"
@@ -27,7 +28,6 @@ namespace bsfp8 {
 namespace g16 {
 
 constexpr int BK = 64;  // elements: 128 bytes
-constexpr int THREADS = 192;
 
 // The tiles that CTA (or pair) `unit` of `units` takes: one of every `units`, in each round the next
 // place.  Row tiles of a group follow one another in the numbering, the last often a small one; at
@@ -46,83 +46,66 @@ struct Turns {
   }
 };
 
-template <int CG_, int BN_, int ROWS_, bool BT_, int STAGES_>
-struct Cfg {
-  static constexpr int CG = CG_;          // CTAs per tile
-  static constexpr int BN = BN_;          // tile columns
-  static constexpr int ROWS = ROWS_;      // rows of A per CTA
-  static constexpr int BM = CG * ROWS;    // tile rows
-  static constexpr bool BT = BT_;         // B [E, K, N]
-  static constexpr int STAGES = STAGES_;
-  static constexpr int EPI_WARPS = ROWS / 32;  // that hold rows
-  static constexpr int B_ROWS = BN / CG;       // columns of C whose weights a CTA loads
-  static constexpr uint32_t A_STAGE = ROWS * BK * 2;
-  static constexpr uint32_t B_STAGE = B_ROWS * BK * 2;
-  static constexpr uint32_t B_BOX = BT ? 64 * BK * 2 : B_STAGE;
-  static constexpr uint32_t STAGE_TX = (A_STAGE + B_STAGE) * CG;
-  static constexpr uint32_t SMEM_A = 0;
-  static constexpr uint32_t SMEM_B = SMEM_A + STAGES * A_STAGE;
-  static constexpr uint32_t SMEM_CTL = SMEM_B + STAGES * B_STAGE;
-  static constexpr uint32_t TMEM_COLS = 2 * BN;
-  static constexpr uint32_t IDESC = idesc_f16_f32(128 * CG, BN) | (BT ? IDESC_B_MN : 0u);
-  // what the MMA of the last stage reads past A ends inside B
-  static_assert(ROWS == 128 || (128 - ROWS) * BK * 2 <= (int)(STAGES * B_STAGE), "A's overhang");
-  // row tiles that share a column of B within a wave (as in the 8-bit kernels)
-  static constexpr int TILE_BAND = CG == 2 ? 16 : 1;
+// ---------------------------------------------------------------------------------------
+// Few rows: 32 rows x 128 columns per CTA, or per cluster of SPLIT CTAs that share its K
+// ---------------------------------------------------------------------------------------
+template <bool BT_, int SPLIT_>
+struct Few {
+  static constexpr bool BT = BT_;        // B [E, K, N]
+  static constexpr int SPLIT = SPLIT_;
 };
+constexpr int FEW_THREADS = 192;  // warp 0 producer, 1 MMA thread, 4 epilogue (TMEM lanes 0..31)
+constexpr int FEW_ROWS = 32, FEW_COLS = 128, FEW_STAGES = 9;
+constexpr uint32_t FEW_A = FEW_ROWS * BK * 2, FEW_B = FEW_COLS * BK * 2;
+constexpr uint32_t FEW_SMEM_B = FEW_STAGES * FEW_A;
+constexpr uint32_t FEW_CTL = FEW_SMEM_B + FEW_STAGES * FEW_B;
+// what the MMA reads past the 32 rows of the last stage is B's
+static_assert((128 - FEW_ROWS) * BK * 2 <= FEW_STAGES * FEW_B, "A's overhang");
+// a split tile's part of the sums, in the ring (which is done with by then): padded rows
+constexpr int PART_STRIDE = FEW_COLS + 4;
+static_assert(FEW_ROWS * PART_STRIDE * 4 <= FEW_CTL, "part");
 
-template <class C>
-struct Ctl {
-  uint64_t full[C::STAGES];
-  uint64_t empty[C::STAGES];
+struct FewCtl {
+  uint64_t full[FEW_STAGES];
+  uint64_t empty[FEW_STAGES];
   uint64_t tfull[2];
   uint64_t tempty[2];
   uint64_t mma_done;
   uint32_t tmem_base;
   int abort;
-  int valid;
-  int pad;
   long long total_tiles;
+  TileCoord tile;  // that a cluster shares
 };
+constexpr uint32_t kFewSmem = FEW_CTL + sizeof(FewCtl) + 1024;  // + alignment slack
 
-template <class C>
-constexpr uint32_t smem_bytes() {
-  return C::SMEM_CTL + sizeof(Ctl<C>) + 1024;  // + alignment slack
+__device__ __forceinline__ float4 load_cluster_f4(uint32_t addr) {
+  float4 v;
+  asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
+               : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
+               : "r"(addr)
+               : "memory");
+  return v;
 }
 
-template <class C>
-__global__ void __launch_bounds__(THREADS, 1)
-product16_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
-                 const Product16Args args) {
+template <class F>
+__global__ void __launch_bounds__(FEW_THREADS, 1)
+product16_few_kernel(const __grid_constant__ CUtensorMap tmA,
+                     const __grid_constant__ CUtensorMap tmB, const Product16Args args) {
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                              ~static_cast<uintptr_t>(1023));
-  Ctl<C>* ctl = reinterpret_cast<Ctl<C>*>(smem + C::SMEM_CTL);
+  FewCtl* ctl = reinterpret_cast<FewCtl*>(smem + FEW_CTL);
   volatile int* abort = &ctl->abort;
   const uint32_t warp = threadIdx.x >> 5;
   const uint32_t lane = threadIdx.x & 31;
+  const uint32_t part = F::SPLIT > 1 ? cluster_ctarank() : 0;
   const int KB = (args.K + BK - 1) / BK;
-  const uint32_t rank = C::CG == 2 ? cluster_ctarank() : 0;
-  const int64_t tile0 = blockIdx.x / C::CG;
-  const int64_t tile_stride = gridDim.x / C::CG;
+  const int kb0 = (int)((int64_t)KB * part / F::SPLIT);
+  const int kb1 = (int)((int64_t)KB * (part + 1) / F::SPLIT);
+  const int64_t tile0 = blockIdx.x / F::SPLIT;
+  const int64_t tile_stride = gridDim.x / F::SPLIT;
 
-  if (warp == 0) {
-    int64_t row_tiles;
-    const int status = check_groups<C::BM>(args.offsets, args.expert_ids, args.E,
-                                           args.num_experts, args.M_total, row_tiles);
-    if (lane == 0) {
-      ctl->valid = status == 0;
-      ctl->total_tiles = row_tiles * ((args.N + C::BN - 1) / C::BN);
-      ctl->abort = 0;
-      if (status && blockIdx.x == 0) atomicCAS(args.err, 0, status);
-    }
-  }
-  __syncthreads();
-  const int64_t total_tiles = ctl->total_tiles;
-  if (!ctl->valid || tile0 >= total_tiles) return;  // both CTAs of a pair agree
-
-  const uint32_t sA = smem_u32(smem + C::SMEM_A);
-  const uint32_t sB = smem_u32(smem + C::SMEM_B);
+  const uint32_t sA = smem_u32(smem), sB = smem_u32(smem + FEW_SMEM_B);
   auto full_bar = [&](int s) { return smem_u32(&ctl->full[s]); };
   auto empty_bar = [&](int s) { return smem_u32(&ctl->empty[s]); };
   auto tfull_bar = [&](int s) { return smem_u32(&ctl->tfull[s]); };
@@ -130,177 +113,171 @@ product16_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant_
   if (warp == 0 && lane == 0) {
     tma_prefetch_desc(&tmA);
     tma_prefetch_desc(&tmB);
-    for (int s = 0; s < C::STAGES; ++s) {
-      mbar_init(full_bar(s), 1);   // the leader's producer (+ both CTAs' bytes)
+    for (int s = 0; s < FEW_STAGES; ++s) {
+      mbar_init(full_bar(s), 1);   // the producer (+ bytes)
       mbar_init(empty_bar(s), 1);  // one commit
     }
     for (int s = 0; s < 2; ++s) {
-      mbar_init(tfull_bar(s), 1);                       // one commit
-      mbar_init(tempty_bar(s), C::EPI_WARPS * C::CG);   // every epilogue warp of the pair
+      mbar_init(tfull_bar(s), 1);   // one commit
+      mbar_init(tempty_bar(s), 1);  // the epilogue warp
     }
     mbar_init(smem_u32(&ctl->mma_done), 1);
+    ctl->abort = 0;
+    ctl->tile = TileCoord{};
     fence_mbarrier_init();
   }
   if (warp == 1) {
-    tmem_alloc<C::CG>(smem_u32(&ctl->tmem_base), C::TMEM_COLS);
-    tmem_relinquish<C::CG>();
+    tmem_alloc<1>(smem_u32(&ctl->tmem_base), 2 * FEW_COLS);
+    tmem_relinquish<1>();
+    launch_dependents();
+  }
+  wait_for_previous();
+  if (warp == 2) {
+    int64_t row_tiles;
+    const int status = check_groups<FEW_ROWS>(args.offsets, args.expert_ids, args.E,
+                                              args.num_experts, args.M_total, row_tiles);
+    if (lane == 0) {
+      ctl->total_tiles = status ? 0 : row_tiles * ((args.N + FEW_COLS - 1) / FEW_COLS);
+      if (status && blockIdx.x == 0) atomicCAS(args.err, 0, status);
+    }
   }
   tc_fence_before();
   __syncthreads();
-  if constexpr (C::CG == 2) cluster_sync();  // the peer's barriers before any use
   tc_fence_after();
   const uint32_t tmem_base = ctl->tmem_base;
+  const int64_t total_tiles = ctl->total_tiles;
 
-  GroupedScheduler<C::BM, C::BN, C::TILE_BAND> sched;
+  GroupedScheduler<FEW_ROWS, FEW_COLS, 1, false> sched;
   TileCoord tc;
   if (warp == 0) {
     if (lane == 0) {
       // ------------------------------- TMA producer -------------------------------
-      // Pairs walk in bands whose rows of A stay in L2 while B goes by; decode-sized tiles read
-      // every weight once.
-      const uint64_t pol_a = l2_policy_evict_last();
-      const uint64_t pol_b = C::ROWS == 32 ? l2_policy_evict_first() : l2_policy_evict_normal();
+      const uint64_t pol_a = l2_policy_evict_last(), pol_b = l2_policy_evict_first();
       uint32_t stage = 0, phase = 0;
       int64_t issued = 0;
       bool ok = true;
       for (Turns t(tile0, tile_stride); ok && t.at < total_tiles; t.next()) {
         if (!sched.locate(args, t.at, tc)) break;
-        const int32_t a_row = (int32_t)(tc.m0 + C::ROWS * rank);
-        const int32_t col = tc.n0 + C::B_ROWS * rank;
-        for (int kb = 0; kb < KB; ++kb) {
+        for (int kb = kb0; kb < kb1; ++kb) {
           if (!mbar_wait_sleep(empty_bar(stage), phase ^ 1, abort)) {
             give_up(args.err, abort);
             ok = false;
             break;
           }
-          const uint32_t a = sA + stage * C::A_STAGE, b = sB + stage * C::B_STAGE;
-          if constexpr (C::CG == 1) {
-            mbar_arrive_expect_tx(full_bar(stage), C::STAGE_TX);
-            tma_load_2d_hint(a, &tmA, kb * BK, a_row, full_bar(stage), pol_a);
-            if constexpr (C::BT) {
-              for (int i = 0; i < C::B_ROWS / 64; ++i)
-                tma_load_3d_hint(b + i * C::B_BOX, &tmB, col + 64 * i, kb * BK, tc.be,
-                                 full_bar(stage), pol_b);
-            } else {
-              tma_load_3d_hint(b, &tmB, kb * BK, col, tc.be, full_bar(stage), pol_b);
-            }
+          const uint32_t a = sA + stage * FEW_A, b = sB + stage * FEW_B, bar = full_bar(stage);
+          mbar_arrive_expect_tx(bar, FEW_A + FEW_B);
+          if constexpr (F::BT) {
+            tma_load_3d_hint(b, &tmB, tc.n0, kb * BK, tc.be, bar, pol_b);
+            tma_load_3d_hint(b + FEW_B / 2, &tmB, tc.n0 + 64, kb * BK, tc.be, bar, pol_b);
           } else {
-            // both CTAs' bytes are counted on the leader's barrier
-            const uint32_t bar = mapa_shared(full_bar(stage), 0);
-            if (rank == 0) mbar_arrive_expect_tx(full_bar(stage), C::STAGE_TX);
-            tma_load_2d_pair_hint(a, &tmA, kb * BK, a_row, bar, pol_a);
-            if constexpr (C::BT) {
-              for (int i = 0; i < C::B_ROWS / 64; ++i)
-                tma_load_3d_pair_hint(b + i * C::B_BOX, &tmB, col + 64 * i, kb * BK, tc.be, bar,
-                                      pol_b);
-            } else {
-              tma_load_3d_pair_hint(b, &tmB, kb * BK, col, tc.be, bar, pol_b);
-            }
+            tma_load_3d_hint(b, &tmB, kb * BK, tc.n0, tc.be, bar, pol_b);
           }
+          tma_load_2d_hint(a, &tmA, kb * BK, (int32_t)tc.m0, bar, pol_a);
           ++issued;
-          if (++stage == C::STAGES) { stage = 0; phase ^= 1; }
+          if (++stage == FEW_STAGES) { stage = 0; phase ^= 1; }
         }
       }
-      // This CTA's last loads land, and the MMAs that read them end, before it can exit (after
-      // an abort the first wait runs out, which is time enough for the loads).
-      const int64_t pending = issued < C::STAGES ? issued : C::STAGES;
+      // the last loads land, and the MMAs that read them end, before the CTA can exit (after an
+      // abort the first wait runs out, which is time enough for the loads)
+      const int64_t pending = issued < FEW_STAGES ? issued : FEW_STAGES;
       for (int64_t i = 0; i < pending; ++i) {
-        stage = (stage + C::STAGES - 1) % C::STAGES;
-        if (stage == C::STAGES - 1) phase ^= 1;
+        stage = (stage + FEW_STAGES - 1) % FEW_STAGES;
+        if (stage == FEW_STAGES - 1) phase ^= 1;
         if (!mbar_wait_timed(empty_bar(stage), phase)) break;
       }
     }
     __syncwarp();
   } else if (warp == 1) {
-    if (lane == 0 && rank == 0) {
+    if (lane == 0) {
       // -------------------------------- MMA thread --------------------------------
-      const uint32_t idesc = C::IDESC | (args.bf16 ? IDESC_BF16 : 0u);
+      const uint32_t idesc = idesc_f16_f32(128, FEW_COLS) | (F::BT ? IDESC_B_MN : 0u) |
+                             (args.bf16 ? IDESC_BF16 : 0u);
       const uint64_t adesc0 = kmajor_sw128_desc(sA);
-      const uint64_t bdesc0 = C::BT ? mnmajor_sw128_desc(sB, C::B_BOX) : kmajor_sw128_desc(sB);
+      const uint64_t bdesc0 = F::BT ? mnmajor_sw128_desc(sB, FEW_B / 2) : kmajor_sw128_desc(sB);
       // 16 K: 32 bytes along a K-major row, 16 rows of 128 bytes of an MN-major box
-      constexpr uint64_t kStepA = 32 >> 4, kStepB = (C::BT ? 2048 : 32) >> 4;
+      constexpr uint64_t kStepA = 32 >> 4, kStepB = (F::BT ? 2048 : 32) >> 4;
       uint32_t stage = 0, phase = 0, acc = 0, acc_phase = 0;
       bool ok = true;
       for (Turns t(tile0, tile_stride); ok && t.at < total_tiles; t.next()) {
         if (!sched.locate(args, t.at, tc)) break;
-        if (!mbar_wait_sleep(tempty_bar(acc), acc_phase ^ 1, abort)) {
+        ok = mbar_wait_sleep(tempty_bar(acc), acc_phase ^ 1, abort);
+        const uint32_t d = tmem_base + acc * FEW_COLS;
+        for (int kb = kb0; ok && kb < kb1; ++kb) {
+          ok = mbar_wait_sleep(full_bar(stage), phase, abort);
+          if (!ok) break;
+          tc_fence_after();
+          const uint64_t adesc = adesc0 + ((stage * FEW_A) >> 4);
+          const uint64_t bdesc = bdesc0 + ((stage * FEW_B) >> 4);
+#pragma unroll
+          for (int k = 0; k < BK / 16; ++k)
+            umma_f16<1>(d, adesc + k * kStepA, bdesc + k * kStepB, idesc, kb > kb0 || k > 0);
+          umma_commit(empty_bar(stage));
+          if (++stage == FEW_STAGES) { stage = 0; phase ^= 1; }
+        }
+        if (!ok) {
           give_up(args.err, abort);
           break;
         }
-        const uint32_t d = tmem_base + acc * C::BN;
-        for (int kb = 0; kb < KB; ++kb) {
-          if (!mbar_wait_sleep(full_bar(stage), phase, abort)) {
-            give_up(args.err, abort);
-            ok = false;
-            break;
-          }
-          tc_fence_after();
-          const uint64_t adesc = adesc0 + ((stage * C::A_STAGE) >> 4);
-          const uint64_t bdesc = bdesc0 + ((stage * C::B_STAGE) >> 4);
-#pragma unroll
-          for (int k = 0; k < BK / 16; ++k)
-            umma_f16<C::CG>(d, adesc + k * kStepA, bdesc + k * kStepB, idesc, (kb | k) > 0);
-          if constexpr (C::CG == 1) umma_commit(empty_bar(stage));
-          else umma_commit_pair(empty_bar(stage), 0x3);
-          if (++stage == C::STAGES) { stage = 0; phase ^= 1; }
-        }
-        if (!ok) break;
-        if constexpr (C::CG == 1) umma_commit(tfull_bar(acc));
-        else umma_commit_pair(tfull_bar(acc), 0x3);
+        umma_commit(tfull_bar(acc));
         if (++acc == 2) { acc = 0; acc_phase ^= 1; }
       }
       // every MMA has finished before TMEM is released
-      if constexpr (C::CG == 1) umma_commit(smem_u32(&ctl->mma_done));
-      else umma_commit_pair(smem_u32(&ctl->mma_done), 0x1);
+      umma_commit(smem_u32(&ctl->mma_done));
       if (!mbar_wait_timed(smem_u32(&ctl->mma_done), 0)) give_up(args.err, abort);
     }
     __syncwarp();
-  } else if ((warp & 3) < C::EPI_WARPS) {
+  } else if (warp == 4) {
     // --------------------------------- epilogue ---------------------------------
-    const uint32_t quarter = warp & 3;
     uint16_t* Cmat = static_cast<uint16_t*>(args.C);
     const bool wide = (reinterpret_cast<uintptr_t>(args.C) & 31) == 0 && args.N % 16 == 0;
     const uint64_t pol_c = l2_policy_evict_first();
     uint32_t acc = 0, acc_phase = 0;
     for (Turns t(tile0, tile_stride); t.at < total_tiles; t.next()) {
       if (!sched.locate(args, t.at, tc)) break;
-      const int64_t row = tc.m0 + C::ROWS * rank + quarter * 32 + lane;
+      const int64_t row = tc.m0 + lane;
+      if (F::SPLIT > 1 && lane == 0) ctl->tile = tc;
       if (!__all_sync(0xffffffffu, mbar_wait_sleep(tfull_bar(acc), acc_phase, abort))) {
         if (lane == 0) give_up(args.err, abort);
         break;
       }
       tc_fence_after();
-      const uint32_t taddr = tmem_base + ((quarter * 32) << 16) + acc * C::BN;
+      const uint32_t taddr = tmem_base + acc * FEW_COLS;
       uint16_t* dst = Cmat + row * (int64_t)args.N + tc.n0;
       const int cols = args.N - tc.n0;  // that are left of the matrix
 #pragma unroll 1
-      for (int c = 0; c < C::BN; c += 32) {
+      for (int c = 0; c < FEW_COLS; c += 32) {
         uint32_t p[32];
         tmem_ld_32x32b_x32(taddr + c, p);
         tmem_ld_wait();
-        if (c + 32 == C::BN) {  // TMEM is read: the MMA thread may have it
-          tc_fence_before();
-          __syncwarp();
-          if (lane == 0)
-            mbar_arrive_cluster_or_local<C::CG>(C::CG == 2 ? mapa_shared(tempty_bar(acc), 0)
-                                                           : tempty_bar(acc));
-        }
-        if (row >= tc.m_end) continue;
+        if constexpr (F::SPLIT > 1) {
+          if (row >= tc.m_end) continue;
+          uint4* to = reinterpret_cast<uint4*>(smem + (lane * PART_STRIDE + c) * 4);
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          uint32_t v[8];
-#pragma unroll
-          for (int j = 0; j < 8; ++j) {
-            const float lo = __uint_as_float(p[16 * h + 2 * j]);
-            const float hi = __uint_as_float(p[16 * h + 2 * j + 1]);
-            v[j] = args.bf16 ? pack_bf16x2(lo, hi) : pack_f16x2(lo, hi);
+          for (int j = 0; j < 8; ++j)
+            to[j] = make_uint4(p[4 * j], p[4 * j + 1], p[4 * j + 2], p[4 * j + 3]);
+        } else {
+          if (c + 32 == FEW_COLS) {  // TMEM is read: the MMA thread may have it
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(tempty_bar(acc));
           }
-          const int at = c + 16 * h;
-          if (wide) {
-            if (at < cols) st_global_v8_hint(dst + at, v, pol_c);
-          } else {  // N is a multiple of 8
-            if (at < cols) st_global_v4_hint(dst + at, v[0], v[1], v[2], v[3], pol_c);
-            if (at + 8 < cols) st_global_v4_hint(dst + at + 8, v[4], v[5], v[6], v[7], pol_c);
+          if (row >= tc.m_end) continue;
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            uint32_t v[8];
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+              const float lo = __uint_as_float(p[16 * h + 2 * j]);
+              const float hi = __uint_as_float(p[16 * h + 2 * j + 1]);
+              v[j] = args.bf16 ? pack_bf16x2(lo, hi) : pack_f16x2(lo, hi);
+            }
+            const int at = c + 16 * h;
+            if (wide) {
+              if (at < cols) st_global_v8_hint(dst + at, v, pol_c);
+            } else {  // N is a multiple of 8
+              if (at < cols) st_global_v4_hint(dst + at, v[0], v[1], v[2], v[3], pol_c);
+              if (at + 8 < cols) st_global_v4_hint(dst + at + 8, v[4], v[5], v[6], v[7], pol_c);
+            }
           }
         }
       }
@@ -308,27 +285,74 @@ product16_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant_
     }
   }
 
+  if constexpr (F::SPLIT > 1) {
+    // The parts of the one tile that the cluster has: each CTA adds up a stripe of its columns, in
+    // the CTAs' order.  (A CTA that gave up has said so, and the sums mean nothing.)
+    cluster_sync();
+    if (tile0 < total_tiles) {
+      tc = ctl->tile;
+      constexpr int kCols = FEW_COLS / F::SPLIT, kGroups = kCols / 4;
+      const uint32_t mine = smem_u32(smem);
+      for (int i = threadIdx.x; i < FEW_ROWS * kGroups; i += FEW_THREADS) {
+        const int r = i / kGroups, c = (int)part * kCols + i % kGroups * 4;
+        const int64_t row = tc.m0 + r;
+        const int n = tc.n0 + c;
+        if (row >= tc.m_end || n >= args.N) continue;  // N is a multiple of 8
+        float4 v[F::SPLIT];
+#pragma unroll
+        for (int s = 0; s < F::SPLIT; ++s)
+          v[s] = load_cluster_f4(mapa_shared(mine + (r * PART_STRIDE + c) * 4, s));
+#pragma unroll
+        for (int s = 1; s < F::SPLIT; ++s) {
+          v[0].x += v[s].x;
+          v[0].y += v[s].y;
+          v[0].z += v[s].z;
+          v[0].w += v[s].w;
+        }
+        uint2 w;
+        w.x = args.bf16 ? pack_bf16x2(v[0].x, v[0].y) : pack_f16x2(v[0].x, v[0].y);
+        w.y = args.bf16 ? pack_bf16x2(v[0].z, v[0].w) : pack_f16x2(v[0].z, v[0].w);
+        *reinterpret_cast<uint2*>(static_cast<uint16_t*>(args.C) + row * (int64_t)args.N + n) = w;
+      }
+    }
+    cluster_sync();  // the parts are read before any of them goes
+  }
   tc_fence_before();
   __syncthreads();
-  // the pair's MMAs and remote arrivals are finished before either CTA frees TMEM or exits
-  if constexpr (C::CG == 2) cluster_sync();
   if (warp == 1) {
     tc_fence_after();
-    tmem_dealloc<C::CG>(tmem_base, C::TMEM_COLS);
+    tmem_dealloc<1>(tmem_base, 2 * FEW_COLS);
   }
+}
+
+template <class F>
+cudaError_t launch_few(const Product16Args& args, int64_t max_tiles, int num_sms,
+                       cudaStream_t stream) {
+  static_assert(kFewSmem <= 227 * 1024, "shared memory per CTA");
+  CUtensorMap tmA, tmB;
+  const uint64_t a_dims[2] = {(uint64_t)args.K, (uint64_t)args.M_total};
+  const uint64_t b_dims[3] = {(uint64_t)(F::BT ? args.N : args.K),
+                              (uint64_t)(F::BT ? args.K : args.N), (uint64_t)args.num_experts};
+  if (!encode_swizzled(&tmA, false, args.A, 2, a_dims, FEW_ROWS) ||
+      !encode_swizzled(&tmB, false, args.B, 3, b_dims, F::BT ? BK : FEW_COLS))
+    return cudaErrorInvalidValue;
+  const cudaError_t e = allow_smem<product16_few_kernel<F>>(kFewSmem);
+  if (e != cudaSuccess) return e;
+  return launch_persistent(product16_few_kernel<F>, max_tiles < num_sms ? max_tiles : num_sms,
+                           F::SPLIT, FEW_THREADS, kFewSmem, stream, tmA, tmB, args);
 }
 
 // ---------------------------------------------------------------------------------------
 // CTA pairs: 256 columns of C (the MMA's M: weight rows, 128 per CTA) x up to 256 or 512 rows (its
 // N: one instruction, or two on the same weights)
 // ---------------------------------------------------------------------------------------
-// HALVES: of 256 rows that a tile may have.
-template <bool BT_, int HALVES_>
+// ROWS: that a tile may have.
+template <bool BT_, int ROWS_>
 struct Pair {
   static constexpr bool BT = BT_;  // B [E, K, N]
-  static constexpr int HALVES = HALVES_;
-  static constexpr int ROWS = 256 * HALVES;
-  static constexpr int BAND = HALVES == 2 ? 8 : 16;
+  static constexpr int ROWS = ROWS_;
+  static constexpr int HALVES = ROWS == 512 ? 2 : 1;  // of up to 256 rows
+  static constexpr int BAND = 4096 / ROWS;
 };
 constexpr uint32_t UNIT = 4096;              // 32 rows of 128 bytes: what a stage of the ring counts in
 constexpr uint32_t RING = 51;                // units
@@ -347,8 +371,6 @@ struct PairCtl {
   uint64_t mma_done;
   uint32_t tmem_base;
   int abort;
-  int valid;
-  int pad;
   long long total_tiles;
 };
 constexpr uint32_t kPairSmem = PAIR_EPI + 2 * EPI_BUF + sizeof(PairCtl) + 1024;  // + alignment slack
@@ -373,9 +395,11 @@ struct RingPlace {
 };
 
 // Rows of half h of a tile as the MMA counts them: a multiple of 16, or 0.
+template <class P>
 __device__ __forceinline__ int half_height(const TileCoord& tc, int h) {
+  constexpr int kMost = P::ROWS < 256 ? P::ROWS : 256;
   const int64_t left = tc.m_end - tc.m0 - 256 * h;
-  return left >= 256 ? 256 : left <= 0 ? 0 : ((int)left + 15) / 16 * 16;
+  return left >= kMost ? kMost : left <= 0 ? 0 : ((int)left + 15) / 16 * 16;
 }
 
 // Units of half h's rows in a stage: 128, 64 or 32 rows, the box of one load (several small ones
@@ -417,21 +441,6 @@ product16_pair_kernel(const __grid_constant__ CUtensorMap tmA,    // 128 rows of
   const int64_t tile0 = blockIdx.x / 2;
   const int64_t tile_stride = gridDim.x / 2;
 
-  if (warp == 0) {
-    int64_t row_tiles;
-    const int status = check_groups<P::ROWS>(args.offsets, args.expert_ids, args.E,
-                                             args.num_experts, args.M_total, row_tiles);
-    if (lane == 0) {
-      ctl->valid = status == 0;
-      ctl->total_tiles = row_tiles * ((args.N + 255) / 256);
-      ctl->abort = 0;
-      if (status && blockIdx.x == 0) atomicCAS(args.err, 0, status);
-    }
-  }
-  __syncthreads();
-  const int64_t total_tiles = ctl->total_tiles;
-  if (!ctl->valid || tile0 >= total_tiles) return;  // both CTAs of a pair agree
-
   const uint32_t base = smem_u32(smem);
   auto full_bar = [&](int s) { return smem_u32(&ctl->full[s]); };
   auto empty_bar = [&](int s) { return smem_u32(&ctl->empty[s]); };
@@ -451,19 +460,32 @@ product16_pair_kernel(const __grid_constant__ CUtensorMap tmA,    // 128 rows of
       mbar_init(tempty_bar(s), 16);  // every epilogue warp of the pair
     }
     mbar_init(smem_u32(&ctl->mma_done), 1);
+    ctl->abort = 0;
     fence_mbarrier_init();
   }
   if (warp == 1) {
     tmem_alloc<2>(smem_u32(&ctl->tmem_base), 512);
     tmem_relinquish<2>();
+    launch_dependents();
+  }
+  wait_for_previous();
+  if (warp == 2) {
+    int64_t row_tiles;
+    const int status = check_groups<P::ROWS>(args.offsets, args.expert_ids, args.E,
+                                             args.num_experts, args.M_total, row_tiles);
+    if (lane == 0) {
+      ctl->total_tiles = status ? 0 : row_tiles * ((args.N + 255) / 256);
+      if (status && blockIdx.x == 0) atomicCAS(args.err, 0, status);
+    }
   }
   tc_fence_before();
   __syncthreads();
   cluster_sync();  // the peer's barriers before any use
   tc_fence_after();
   const uint32_t tmem_base = ctl->tmem_base;
+  const int64_t total_tiles = ctl->total_tiles;  // both CTAs of a pair agree
 
-  GroupedScheduler<P::ROWS, 256, P::BAND> sched;
+  GroupedScheduler<P::ROWS, 256, P::BAND, false> sched;
   TileCoord tc;
   if (warp == 0) {
     if (lane == 0) {
@@ -494,7 +516,7 @@ product16_pair_kernel(const __grid_constant__ CUtensorMap tmA,    // 128 rows of
         uint32_t part[P::HALVES], units = W_UNITS;
 #pragma unroll
         for (int h = 0; h < P::HALVES; ++h) {
-          const int height = half_height(tc, h);
+          const int height = half_height<P>(tc, h);
           row[h] = (int32_t)tc.m0 + 256 * h + height / 2 * (int)rank;
           part[h] = half_units(height);
           units += part[h];
@@ -554,7 +576,7 @@ product16_pair_kernel(const __grid_constant__ CUtensorMap tmA,    // 128 rows of
       bool ok = true;
       for (Turns t(tile0, tile_stride); ok && t.at < total_tiles; t.next()) {
         if (!sched.locate(args, t.at, tc)) break;
-        const uint32_t n0 = half_height(tc, 0), n1 = P::HALVES == 2 ? half_height(tc, 1) : 0;
+        const uint32_t n0 = half_height<P>(tc, 0), n1 = P::HALVES == 2 ? half_height<P>(tc, 1) : 0;
         const uint32_t units0 = half_units(n0), units = W_UNITS + units0 + half_units(n1);
         const uint32_t d0 = tmem_base + acc * 256, d1 = tmem_base + (acc ^ 1) * 256;
         ok = mbar_wait_sleep(tempty_bar(acc), acc_phase ^ 1, abort);
@@ -612,7 +634,7 @@ product16_pair_kernel(const __grid_constant__ CUtensorMap tmA,    // 128 rows of
       const int n = tc.n0 + 128 * (int)rank + 8 * (int)(lane & 15);  // of what the lane stores
       bool ok = true;
       for (int h = 0; ok && h < P::HALVES; ++h) {
-        const int height = half_height(tc, h);
+        const int height = half_height<P>(tc, h);
         if (height == 0) break;
         // the group's warps have barriers between them: all leave, or none
         ok = all_of_group(group, mbar_wait_sleep(tfull_bar(acc), acc_phase, abort));
@@ -684,80 +706,38 @@ cudaError_t launch_pair(const Product16Args& args, int num_sms, cudaStream_t str
       !encode_swizzled(&tmA32, false, args.A, 2, a_dims, 32) ||
       !encode_swizzled(&tmB, false, args.B, 3, b_dims, P::BT ? BK : 128))
     return cudaErrorInvalidValue;
-  static std::atomic<bool> attr_set[64];  // per device; several host threads may launch
-  int dev = 0;
-  cudaGetDevice(&dev);
-  if (dev >= 64 || !attr_set[dev].load(std::memory_order_acquire)) {
-    const cudaError_t e = cudaFuncSetAttribute(product16_pair_kernel<P>,
-                                               cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                               (int)kPairSmem);
-    if (e != cudaSuccess) return e;
-    if (dev < 64) attr_set[dev].store(true, std::memory_order_release);
-  }
+  const cudaError_t e = allow_smem<product16_pair_kernel<P>>(kPairSmem);
+  if (e != cudaSuccess) return e;
   // more tiles than this there are not (the offsets live on the device)
   const int64_t max_tiles = ((args.M_total + P::ROWS - 1) / P::ROWS + args.E) * ((args.N + 255) / 256);
   const int64_t units = num_sms / 2;
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)((max_tiles < units ? max_tiles : units) * 2));
-  cfg.blockDim = dim3(PAIR_THREADS);
-  cfg.dynamicSmemBytes = kPairSmem;
-  cfg.stream = stream;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeClusterDimension;
-  attr[0].val.clusterDim.x = 2;
-  attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, product16_pair_kernel<P>, tmA, tmA64, tmA32, tmB, args);
-}
-
-template <class C>
-cudaError_t launch(const Product16Args& args, int num_sms, cudaStream_t stream) {
-  static_assert(smem_bytes<C>() <= 227 * 1024, "shared memory per CTA");
-  CUtensorMap tmA, tmB;
-  const uint64_t a_dims[2] = {(uint64_t)args.K, (uint64_t)args.M_total};
-  const uint64_t inner = C::BT ? args.N : args.K, outer = C::BT ? args.K : args.N;
-  const uint64_t b_dims[3] = {inner, outer, (uint64_t)args.num_experts};
-  if (!encode_swizzled(&tmA, false, args.A, 2, a_dims, C::ROWS) ||
-      !encode_swizzled(&tmB, false, args.B, 3, b_dims, C::BT ? BK : C::B_ROWS))
-    return cudaErrorInvalidValue;
-  static std::atomic<bool> attr_set[64];  // per device; several host threads may launch
-  int dev = 0;
-  cudaGetDevice(&dev);
-  if (dev >= 64 || !attr_set[dev].load(std::memory_order_acquire)) {
-    const cudaError_t e = cudaFuncSetAttribute(product16_kernel<C>,
-                                               cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                               (int)smem_bytes<C>());
-    if (e != cudaSuccess) return e;
-    if (dev < 64) attr_set[dev].store(true, std::memory_order_release);
-  }
-  // more tiles than this there are not (the offsets live on the device)
-  const int64_t max_row_tiles = (args.M_total + C::BM - 1) / C::BM + args.E;
-  const int64_t max_tiles = max_row_tiles * ((args.N + C::BN - 1) / C::BN);
-  const int64_t units = num_sms / C::CG;
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)((max_tiles < units ? max_tiles : units) * C::CG));
-  cfg.blockDim = dim3(THREADS);
-  cfg.dynamicSmemBytes = smem_bytes<C>();
-  cfg.stream = stream;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeClusterDimension;
-  attr[0].val.clusterDim.x = C::CG;
-  attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, product16_kernel<C>, tmA, tmB, args);
+  return launch_persistent(product16_pair_kernel<P>, max_tiles < units ? max_tiles : units, 2,
+                           PAIR_THREADS, kPairSmem, stream, tmA, tmA64, tmA32, tmB, args);
 }
 
 template <bool BT>
 cudaError_t choose(const Product16Args& a, int num_sms, cudaStream_t stream) {
-  if (a.M_total <= (int64_t)32 * a.E)
-    return launch<Cfg<1, 128, 32, BT, 9>>(a, num_sms, stream);
-  if (a.M_total <= (int64_t)128 * a.E)
-    return launch<Cfg<1, 256, 128, BT, 4>>(a, num_sms, stream);
-  const int64_t tall = (a.M_total / 512 + a.E / 2) * ((a.N + 255) / 256);
-  return tall >= 6 * (num_sms / 2) ? launch_pair<Pair<BT, 2>>(a, num_sms, stream)
-                                   : launch_pair<Pair<BT, 1>>(a, num_sms, stream);
+  if (a.M_total <= (int64_t)32 * a.E) {
+    // more tiles than this there are not (the offsets live on the device); a tile's K is shared
+    // where that leaves each of the tile's CTAs a part and an SM
+    const int64_t row_tiles = a.M_total / FEW_ROWS + (a.M_total < a.E ? a.M_total : a.E);
+    const int64_t tiles = row_tiles * ((a.N + FEW_COLS - 1) / FEW_COLS);
+    const int64_t blocks = (a.K + BK - 1) / BK;
+    if (tiles * 8 <= num_sms && blocks >= 16) return launch_few<Few<BT, 8>>(a, tiles, num_sms, stream);
+    if (tiles * 4 <= num_sms && blocks >= 8) return launch_few<Few<BT, 4>>(a, tiles, num_sms, stream);
+    if (tiles * 2 <= num_sms && blocks >= 4) return launch_few<Few<BT, 2>>(a, tiles, num_sms, stream);
+    return launch_few<Few<BT, 1>>(a, tiles, num_sms, stream);
+  }
+  // Of tiles of 512, 256, 128 or 64 rows the highest that give every pair of SMs some to do; 512
+  // where groups are mostly over 256 or near it (64 groups of 260 rows, 7168 x 2048: 413 us, 509
+  // with 256; groups of 128: 311 and 297) and there are enough of them to even out.
+  auto tiles = [&](int rows) { return (a.M_total / rows + a.E / 2) * ((a.N + 255) / 256); };
+  const int64_t units = num_sms / 2;
+  if (a.M_total >= (int64_t)192 * a.E && tiles(512) >= 6 * units)
+    return launch_pair<Pair<BT, 512>>(a, num_sms, stream);
+  if (tiles(256) >= units) return launch_pair<Pair<BT, 256>>(a, num_sms, stream);
+  if (tiles(128) >= units) return launch_pair<Pair<BT, 128>>(a, num_sms, stream);
+  return launch_pair<Pair<BT, 64>>(a, num_sms, stream);
 }
 
 }  // namespace g16

@@ -36,7 +36,6 @@
 // Roles (12 warps): warp 0 TMA producer; warp 1 TMEM owner and, in CTA 0 of a pair, the MMA thread;
 // warp 2 fixer; warps 4-11 epilogue (TMEM lanes 32 * (w % 4)..: columns n of dC; half of the tile's
 // columns k each).
-#include <atomic>
 #include "expert_ops.cuh"
 #include "ptx.cuh"
 
@@ -48,11 +47,13 @@ constexpr int EPI_WARP0 = 4;
 constexpr int BN = 256;  // columns k of a tile
 constexpr uint32_t TMEM_COLS = 512;
 
-// CHUNK: stages of 64 rows that accumulate in TMEM, of 16-bit operands
-template <bool FP8_, int CG_, int STAGES_, int CHUNK_>
+// CHUNK: stages of 64 rows that accumulate in TMEM, of 16-bit operands.  SPLIT: pairs, in one cluster,
+// that share a tile's rows, each cluster one tile.
+template <bool FP8_, int CG_, int STAGES_, int CHUNK_, int SPLIT_ = 1>
 struct Cfg {
   static constexpr bool FP8 = FP8_;
   static constexpr int CG = CG_;
+  static constexpr int SPLIT = SPLIT_;
   static constexpr int BM = 128 * CG;             // columns n of a tile
   static constexpr int ROWS = FP8 ? 128 : 64;     // rows of the operands in a stage
   static constexpr int STEP = ROWS / 4;           // rows of an MMA (K = 32 or 16)
@@ -68,6 +69,8 @@ struct Cfg {
   // registers of the role warps and of the epilogue warps, of the 168 each is launched with
   static constexpr int ROLE_REGS = 40;
   static constexpr int SUM_REGS = 232;
+  // a split tile's part of the sums, 128 x 256 in fp32, takes the operands' ring when that is done
+  static_assert(SPLIT == 1 || 128 * BN * 4 <= STAGES * STAGE, "part");
   static_assert(4 * ROLE_REGS + 8 * SUM_REGS <= 12 * 168, "the launch's registers");
   static constexpr uint32_t IDESC =
       (FP8 ? idesc_f8f6f4_e4m3(BM, BN) : idesc_f16_f32(BM, BN)) | IDESC_A_MN | IDESC_B_MN;
@@ -117,7 +120,18 @@ struct Walk {
     }
     return e < s.experts;
   }
-  __device__ int rows(const WgradArgs& a) const { return a.offsets[e + 1] - a.offsets[e]; }
+  // The rows of the tile's group that a pair takes: all, or of SPLIT parts one, whole blocks of 128.
+  template <int SPLIT>
+  __device__ void rows(const WgradArgs& a, uint32_t part, int& begin, int& end) const {
+    const int all = a.offsets[e + 1] - a.offsets[e];
+    begin = 0;
+    end = all;
+    if constexpr (SPLIT > 1) {
+      const int64_t blocks = (all + 127) / 128;
+      begin = (int)(blocks * part / SPLIT) * 128;
+      if (part + 1 < SPLIT) end = (int)(blocks * (part + 1) / SPLIT) * 128;
+    }
+  }
   template <int BM>
   __device__ void corner(const Shape& s, int& n0, int& k0) const {
     constexpr uint32_t BAND = 8;
@@ -176,11 +190,29 @@ __device__ __forceinline__ void load8(const void* add, int64_t at, float2 (&v)[4
   }
 }
 
-// Eight columns of a row of dB.
+// The same of words.
+__device__ __forceinline__ void quad_transpose(uint32_t (&v)[4], uint32_t lane) {
+#pragma unroll
+  for (int d = 1; d <= 2; d *= 2) {
+    const bool up = (lane & d) != 0;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      if (j & d) continue;
+      const uint32_t out = __shfl_xor_sync(0xffffffffu, up ? v[j] : v[j + d], d);
+      if (up) v[j] = out;
+      else v[j + d] = out;
+    }
+  }
+}
+
+// Pairs of columns 8 j + 2 (lane % 4).. of a row, j < 4, exchanged between the four lanes that hold
+// the row and stored, eight columns 8 (lane % 4).. by each; 16-bit values are rounded first.
 template <int OUT>
-__device__ __forceinline__ void store8(void* dB, int64_t at, const float2 (&v)[4], bool wide,
-                                       uint64_t pol) {
+__device__ __forceinline__ void store_row(void* dB, int64_t at, float2 (&v)[4], bool in, bool wide,
+                                          uint32_t lane, uint64_t pol) {
   if constexpr (OUT == GRAD_FP32) {
+    quad_transpose(v, lane);
+    if (!in) return;
     uint32_t w[8];
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
@@ -199,7 +231,8 @@ __device__ __forceinline__ void store8(void* dB, int64_t at, const float2 (&v)[4
 #pragma unroll
     for (int j = 0; j < 4; ++j)
       w[j] = OUT == GRAD_BF16 ? pack_bf16x2(v[j].x, v[j].y) : pack_f16x2(v[j].x, v[j].y);
-    st_global_v4_hint(static_cast<uint16_t*>(dB) + at, w[0], w[1], w[2], w[3], pol);
+    quad_transpose(w, lane);
+    if (in) st_global_v4_hint(static_cast<uint16_t*>(dB) + at, w[0], w[1], w[2], w[3], pol);
   }
 }
 
@@ -215,21 +248,13 @@ wgrad_kernel(const __grid_constant__ CUtensorMap tmC, const __grid_constant__ CU
   volatile int* abort = &ctl->abort;
   const uint32_t warp = threadIdx.x >> 5;
   const uint32_t lane = threadIdx.x & 31;
-  const uint32_t rank = C::CG == 2 ? cluster_ctarank() : 0;
-  const uint32_t tile0 = blockIdx.x / C::CG;  // the grid has no more pairs than there are tiles
-  const uint32_t tile_stride = gridDim.x / C::CG;
-
-  if (warp == 0) {
-    int64_t unused;
-    const int status = check_groups<1>(args.offsets, nullptr, args.E, args.E, args.M_total, unused);
-    if (lane == 0) {
-      ctl->valid = status == 0;
-      ctl->abort = 0;
-      if (status && blockIdx.x == 0) atomicCAS(args.err, 0, status);
-    }
-  }
-  __syncthreads();
-  if (!ctl->valid) return;
+  // of the CTA in its pair, its pair's leader in the cluster, and the pair's share of a split tile
+  const uint32_t cta = C::CG * C::SPLIT > 1 ? cluster_ctarank() : 0;
+  const uint32_t rank = cta % C::CG, leader = cta - rank, part = cta / C::CG;
+  const uint16_t both = (uint16_t)(0x3 << leader);
+  // the grid has no more clusters than there are tiles (as many, where they are split)
+  const uint32_t tile0 = blockIdx.x / (C::CG * C::SPLIT);
+  const uint32_t tile_stride = gridDim.x / (C::CG * C::SPLIT);
 
   const uint32_t base = smem_u32(smem);
   auto full_bar = [&](int s) { return smem_u32(&ctl->full[s]); };
@@ -252,19 +277,34 @@ wgrad_kernel(const __grid_constant__ CUtensorMap tmC, const __grid_constant__ CU
       mbar_init(tempty_bar(s), 8 * C::CG);  // every epilogue warp of the pair
     }
     mbar_init(smem_u32(&ctl->mma_done), 1);
+    ctl->abort = 0;
     fence_mbarrier_init();
   }
   if (warp == 1) {
     tmem_alloc<C::CG>(smem_u32(&ctl->tmem_base), TMEM_COLS);
     tmem_relinquish<C::CG>();
+    launch_dependents();
+  }
+  wait_for_previous();
+  if (warp == 2) {
+    int64_t unused;
+    const int status = check_groups<1>(args.offsets, nullptr, args.E, args.E, args.M_total, unused);
+    if (lane == 0) {
+      ctl->valid = status == 0;
+      if (status && blockIdx.x == 0) atomicCAS(args.err, 0, status);
+    }
   }
   tc_fence_before();
   __syncthreads();
-  if constexpr (C::CG == 2) cluster_sync();  // the peer's barriers before any use
+  if constexpr (C::CG * C::SPLIT > 1) cluster_sync();  // the peer's barriers before any use
   tc_fence_after();
   const uint32_t tmem_base = ctl->tmem_base;
+  const bool valid = ctl->valid;  // both CTAs of a pair agree
 
-  if (warp < EPI_WARP0) {
+  // (of a split tile, every warp is in the cluster's barrier between the parts and their sum)
+  if (!valid) {
+    if constexpr (C::SPLIT > 1) cluster_sync();
+  } else if (warp < EPI_WARP0) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(C::ROLE_REGS));
     if (warp == 0 && lane == 0) {
       // ------------------------------- TMA producer -------------------------------
@@ -276,11 +316,13 @@ wgrad_kernel(const __grid_constant__ CUtensorMap tmC, const __grid_constant__ CU
       int64_t issued = 0;
       bool ok = true;
       for (Walk t(tile0); ok && t.inside(shape); t.local += tile_stride) {
-        const int rows = t.rows(args), r0 = args.offsets[t.e];
+        int begin, rows;  // (of the group: up to the pair's last)
+        t.rows<C::SPLIT>(args, part, begin, rows);
+        const int r0 = args.offsets[t.e];
         int n0, k0;
         t.corner<C::BM>(shape, n0, k0);
         const int col_m = n0 + 128 * rank, col_n = k0 + (BN / C::CG) * rank;
-        for (int r = 0; r < rows; r += C::ROWS) {
+        for (int r = begin; r < rows; r += C::ROWS) {
           if (!mbar_wait_sleep(empty_bar(stage), phase ^ 1, abort)) {
             give_up(args.err, abort);
             ok = false;
@@ -306,7 +348,7 @@ wgrad_kernel(const __grid_constant__ CUtensorMap tmC, const __grid_constant__ CU
             }
           } else {
             // both CTAs' bytes are counted on the leader's barrier
-            const uint32_t bar = mapa_shared(full_bar(stage), 0);
+            const uint32_t bar = mapa_shared(full_bar(stage), leader);
             if (rank == 0) mbar_arrive_expect_tx(full_bar(stage), 2 * C::STAGE_TX);
 #pragma unroll
             for (int i = 0; i < C::M_BOXES; ++i)
@@ -340,9 +382,10 @@ wgrad_kernel(const __grid_constant__ CUtensorMap tmC, const __grid_constant__ CU
       uint32_t stage = 0, phase = 0, acc = 0, acc_phase = 0;
       bool ok = true;
       for (Walk t(tile0); ok && t.inside(shape); t.local += tile_stride) {
-        const int rows = t.rows(args);
+        int begin, rows;
+        t.rows<C::SPLIT>(args, part, begin, rows);
         int in_chunk = 0;
-        for (int r = 0; r < rows; r += C::ROWS) {
+        for (int r = begin; r < rows; r += C::ROWS) {
           if (!mbar_wait_sleep(full_bar(stage), phase, abort)) {
             give_up(args.err, abort);
             ok = false;
@@ -369,11 +412,11 @@ wgrad_kernel(const __grid_constant__ CUtensorMap tmC, const __grid_constant__ CU
             }
           }
           if constexpr (C::CG == 1) umma_commit(empty_bar(stage));
-          else umma_commit_pair(empty_bar(stage), 0x3);
+          else umma_commit_pair(empty_bar(stage), both);
           if (++stage == C::STAGES) { stage = 0; phase ^= 1; }
           if (++in_chunk == C::CHUNK || r + C::ROWS >= rows) {
             if constexpr (C::CG == 1) umma_commit(tfull_bar(acc));
-            else umma_commit_pair(tfull_bar(acc), 0x3);
+            else umma_commit_pair(tfull_bar(acc), both);
             in_chunk = 0;
             if (++acc == 2) { acc = 0; acc_phase ^= 1; }
           }
@@ -381,7 +424,7 @@ wgrad_kernel(const __grid_constant__ CUtensorMap tmC, const __grid_constant__ CU
       }
       // every MMA has finished before TMEM is released
       if constexpr (C::CG == 1) umma_commit(smem_u32(&ctl->mma_done));
-      else umma_commit_pair(smem_u32(&ctl->mma_done), 0x1);
+      else umma_commit_pair(smem_u32(&ctl->mma_done), (uint16_t)(1 << leader));
       if (!mbar_wait_timed(smem_u32(&ctl->mma_done), 0)) give_up(args.err, abort);
     } else if (warp == 2) {
       // ----------------------------------- fixer -----------------------------------
@@ -390,9 +433,10 @@ wgrad_kernel(const __grid_constant__ CUtensorMap tmC, const __grid_constant__ CU
       uint32_t stage = 0;
       uint32_t seen = 0;  // parity of every stage's tail barrier, a bit each
       for (Walk t(tile0); t.inside(shape); t.local += tile_stride) {
-        const int rows = t.rows(args);
-        const int stages = (rows + C::ROWS - 1) / C::ROWS;
-        const int left = rows % C::ROWS;
+        int begin, rows;
+        t.rows<C::SPLIT>(args, part, begin, rows);
+        const int stages = (rows - begin + C::ROWS - 1) / C::ROWS;
+        const int left = (rows - begin) % C::ROWS;
         const uint32_t last = (stage + stages + C::STAGES - 1) % C::STAGES;
         stage = (stage + stages) % C::STAGES;
         if (left == 0) continue;
@@ -411,7 +455,7 @@ wgrad_kernel(const __grid_constant__ CUtensorMap tmC, const __grid_constant__ CU
         __syncwarp();
         if (lane == 0) {
           if (rank == 1) {
-            mbar_arrive_release_cluster(mapa_shared(peer_bar(last), 0));
+            mbar_arrive_release_cluster(mapa_shared(peer_bar(last), leader));
           } else {
             if (C::CG == 2 && !mbar_wait_cluster(peer_bar(last), parity, abort))
               give_up(args.err, abort);
@@ -423,6 +467,7 @@ wgrad_kernel(const __grid_constant__ CUtensorMap tmC, const __grid_constant__ CU
       }
     }
     __syncwarp();
+    if constexpr (C::SPLIT > 1) cluster_sync();
   } else {
     // --------------------------------- epilogue ---------------------------------
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(C::SUM_REGS));
@@ -438,11 +483,11 @@ wgrad_kernel(const __grid_constant__ CUtensorMap tmC, const __grid_constant__ CU
     auto wait = [&](uint32_t bar, uint32_t parity) {
       return C::FP8 ? mbar_wait(bar, parity, abort) : mbar_wait_sleep(bar, parity, abort);
     };
-    const uint32_t tempty_0 = C::CG == 2 ? mapa_shared(tempty_bar(0), 0) : tempty_bar(0);
-    const uint32_t tempty_1 = C::CG == 2 ? mapa_shared(tempty_bar(1), 0) : tempty_bar(1);
+    const uint32_t tempty_0 = C::CG == 2 ? mapa_shared(tempty_bar(0), leader) : tempty_bar(0);
+    const uint32_t tempty_1 = C::CG == 2 ? mapa_shared(tempty_bar(1), leader) : tempty_bar(1);
     for (Walk t(tile0); t.inside(shape); t.local += tile_stride) {
-      const int rows = t.rows(args);
-      int n0, k0;
+      int begin, rows, n0, k0;
+      t.rows<C::SPLIT>(args, part, begin, rows);
       t.corner<C::BM>(shape, n0, k0);
       // Rows n of lanes lane / 4 + 8 i, columns 8 g + 2 (lane % 4) and the next.  The sums begin
       // with add, whose loads need no registers of their own here: fp32 pairs go where they
@@ -458,7 +503,7 @@ wgrad_kernel(const __grid_constant__ CUtensorMap tmC, const __grid_constant__ CU
         for (int g = 0; g < 4; ++g)
 #pragma unroll
           for (int j = 0; j < 4; ++j) sum[i][g][j] = make_float2(0.0f, 0.0f);
-      if (args.add) {
+      if (args.add && part == 0) {
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
           const int64_t row = ((int64_t)t.e * args.N + n0 + 8 * i) * args.K;
@@ -516,8 +561,8 @@ wgrad_kernel(const __grid_constant__ CUtensorMap tmC, const __grid_constant__ CU
         tc_fence_after();
         load(0);
       };
-      if (rows > 0) start();
-      for (int r = 0; r < rows; r += C::ROWS * C::CHUNK) {
+      if (rows > begin) start();
+      for (int r = begin; r < rows; r += C::ROWS * C::CHUNK) {
         float sc[4];
         float2 sa[4];
         const float* scales = reinterpret_cast<const float*>(smem + C::SMEM_SF + slot * C::SLOT);
@@ -560,16 +605,50 @@ wgrad_kernel(const __grid_constant__ CUtensorMap tmC, const __grid_constant__ CU
       }
       if (!__all_sync(0xffffffffu, ok)) {
         if (lane == 0) give_up(args.err, abort);
+        if constexpr (C::SPLIT > 1) cluster_sync();
         break;
+      }
+      // A split tile: the parts go into shared memory, and each pair adds up a stripe of rows, in
+      // the pairs' order.  (A pair that gave up has said so, and the sums mean nothing.)
+      const uint32_t mine = base + (warp - EPI_WARP0) * (64 * 32 * 8) + lane * 8;
+      if constexpr (C::SPLIT > 1) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+#pragma unroll
+          for (int g = 0; g < 4; ++g)
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+              asm volatile("st.shared.v2.f32 [%0], {%1, %2};" ::"r"(mine + (16 * i + 4 * g + j) * 256),
+                           "f"(sum[i][g][j].x), "f"(sum[i][g][j].y)
+                           : "memory");
+        cluster_sync();
       }
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
+        if (C::SPLIT > 1 && i * C::SPLIT / 4 != (int)part) continue;
         const int64_t at = ((int64_t)t.e * args.N + n0 + 8 * i) * args.K + k8;
 #pragma unroll
         for (int g = 0; g < 4; ++g) {
-          quad_transpose(sum[i][g], lane);
-          if (n0 + 8 * i < args.N && k8 + 32 * g < args.K)
-            store8<OUT>(args.dB, at + 32 * g, sum[i][g], wide, pol);
+          if constexpr (C::SPLIT > 1) {
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+              float2 v[C::SPLIT];
+#pragma unroll
+              for (int q = 0; q < C::SPLIT; ++q)
+                asm volatile("ld.shared::cluster.v2.f32 {%0, %1}, [%2];"
+                             : "=f"(v[q].x), "=f"(v[q].y)
+                             : "r"(mapa_shared(mine + (16 * i + 4 * g + j) * 256, q * C::CG + rank))
+                             : "memory");
+#pragma unroll
+              for (int q = 1; q < C::SPLIT; ++q) {
+                v[0].x += v[q].x;
+                v[0].y += v[q].y;
+              }
+              sum[i][g][j] = v[0];
+            }
+          }
+          store_row<OUT>(args.dB, at + 32 * g, sum[i][g], n0 + 8 * i < args.N && k8 + 32 * g < args.K,
+                         wide, lane, pol);
         }
       }
     }
@@ -578,7 +657,7 @@ wgrad_kernel(const __grid_constant__ CUtensorMap tmC, const __grid_constant__ CU
   tc_fence_before();
   __syncthreads();
   // the pair's MMAs and remote arrivals are finished before either CTA frees TMEM or exits
-  if constexpr (C::CG == 2) cluster_sync();
+  if constexpr (C::CG * C::SPLIT > 1) cluster_sync();
   if (warp == 1) {
     tc_fence_after();
     tmem_dealloc<C::CG>(tmem_base, TMEM_COLS);
@@ -603,32 +682,15 @@ cudaError_t launch(const WgradArgs& args, int num_sms, cudaStream_t stream) {
         !encode_rows_f32(&tmSA, any ? args.a_scales : args.dB, args.K, any ? blocks : 1, BN))
       return cudaErrorInvalidValue;
   }
-  static std::atomic<bool> attr_set[64];  // per device; several host threads may launch
-  int dev = 0;
-  cudaGetDevice(&dev);
-  if (dev >= 64 || !attr_set[dev].load(std::memory_order_acquire)) {
-    const cudaError_t e = cudaFuncSetAttribute(wgrad_kernel<C, OUT>,
-                                               cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                               (int)smem_bytes<C>());
-    if (e != cudaSuccess) return e;
-    if (dev < 64) attr_set[dev].store(true, std::memory_order_release);
-  }
+  const cudaError_t e = allow_smem<wgrad_kernel<C, OUT>>(smem_bytes<C>());
+  if (e != cudaSuccess) return e;
   const Shape shape = {(uint32_t)args.E, (uint32_t)((args.N + C::BM - 1) / C::BM),
                        (uint32_t)((args.K + BN - 1) / BN)};
   const int64_t tiles = (int64_t)shape.experts * shape.nt * shape.kt;
   const int64_t units = num_sms / C::CG;
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)((tiles < units ? tiles : units) * C::CG));
-  cfg.blockDim = dim3(THREADS);
-  cfg.dynamicSmemBytes = smem_bytes<C>();
-  cfg.stream = stream;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeClusterDimension;
-  attr[0].val.clusterDim.x = C::CG;
-  attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, wgrad_kernel<C, OUT>, tmC, tmA, tmSC, tmSA, args, shape);
+  return launch_persistent(wgrad_kernel<C, OUT>, C::SPLIT > 1 || tiles < units ? tiles : units,
+                           C::CG * C::SPLIT, THREADS, smem_bytes<C>(), stream, tmC, tmA, tmSC, tmSA,
+                           args, shape);
 }
 
 template <class C>
@@ -643,7 +705,13 @@ cudaError_t by_type(const WgradArgs& a, int num_sms, cudaStream_t stream) {
 }  // namespace wg
 
 cudaError_t launch_wgrad(const WgradArgs& a, int num_sms, cudaStream_t stream) {
-  return a.fp8 ? wg::by_type<wg::Cfg<true, 2, 4, 1>>(a, num_sms, stream)
+  // Few tiles and many rows: four pairs share a tile's rows (8192 rows, 512 x 512: 54 -> 21 us).
+  const int64_t tiles = (int64_t)a.E * ((a.N + 255) / 256) * ((a.K + 255) / 256);
+  const bool split = tiles * 9 <= num_sms && a.M_total >= (int64_t)1024 * a.E;
+  if (a.fp8)
+    return split ? wg::by_type<wg::Cfg<true, 2, 4, 1, 4>>(a, num_sms, stream)
+                 : wg::by_type<wg::Cfg<true, 2, 4, 1>>(a, num_sms, stream);
+  return split ? wg::by_type<wg::Cfg<false, 2, 4, 8, 4>>(a, num_sms, stream)
                : wg::by_type<wg::Cfg<false, 2, 4, 8>>(a, num_sms, stream);
 }
 

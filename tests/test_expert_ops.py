@@ -87,6 +87,18 @@ def test_product_odd_sides(sizes, N, K, transposed):
     _product(sizes, N, K, BF16, transposed, seed=N)
 
 
+@pytest.mark.parametrize("transposed", [False, True])
+@pytest.mark.parametrize("sizes,N,K", [
+    ([1], 128, 256), ([1], 128, 512), ([3, 2], 136, 1024), ([1], 2048, 1024), ([20, 12, 32], 256, 1032),  # K shared by 2, 4, 8
+    ([65, 500], 264, 640), ([100], 1024, 4096), ([700], 520, 1024),  # tiles of 64 rows
+    ([1300, 1200], 1536, 136), ([2600], 1600, 72),  # of 128
+    ([2500, 2440], 2048, 72), ([2000, 1, 3000], 2568, 136),  # of 256
+    ([520, 1000, 3, 255, 256, 257, 511, 513, 0, 2500, 700, 900], 17416, 72),  # of 512
+], ids=str)
+def test_product_every_tile(sizes, N, K, transposed):
+    _product(sizes, N, K, BF16, transposed, seed=3)
+
+
 @pytest.mark.parametrize("sizes", [[9, 0, 20], [90, 0, 100], [300, 0, 280]], ids=str)
 def test_product_behind_the_last_group(sizes):
     _product(sizes, 136, 264, spare=40)
@@ -193,6 +205,16 @@ def test_wgrad_rows_behind_the_last_group(sizes):
     _wgrad(sizes, 136, 264, spare=90)
 
 
+# few tiles and many rows: the rows of a tile are shared by several pairs of SMs
+MANY_ROWS = [[1024], [1025], [1400], [4097], [2900, 3, 0, 1300], [0, 2100], [9000]]
+
+
+@pytest.mark.parametrize("dtype,out,add", [(BF16, FP32, False), (FP16, FP16, True), (BF16, BF16, False), (BF16, FP32, True)])
+@pytest.mark.parametrize("sizes", MANY_ROWS, ids=str)
+def test_wgrad_many_rows_few_tiles(sizes, dtype, out, add):
+    _wgrad(sizes, 264, 136, dtype, out, add=add, spare=33)
+
+
 @pytest.mark.parametrize("offset", [8, 16])
 def test_wgrad_output_alignment(offset):
     _wgrad([70, 30], 136, 264, BF16, FP32, add=True, in_place=True, offset=offset // 2)
@@ -256,6 +278,12 @@ def _wgrad8(sizes, N, K, out=FP32, add=False, spare=0, in_place=False):
 @pytest.mark.parametrize("N,K", [(128, 128), (384, 640)])
 def test_wgrad8(sizes, N, K, out):
     _wgrad8(sizes, N, K, out)
+
+
+@pytest.mark.parametrize("out,add", [(FP32, False), (FP16, True), (BF16, False), (FP32, True)])
+@pytest.mark.parametrize("sizes", MANY_ROWS, ids=str)
+def test_wgrad8_many_rows_few_tiles(sizes, out, add):
+    _wgrad8(sizes, 384, 128, out, add=add, spare=33)
 
 
 @pytest.mark.parametrize("out", [FP32, BF16])
