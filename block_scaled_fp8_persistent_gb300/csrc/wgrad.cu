@@ -20,7 +20,7 @@
 // a plain fp32 sum; chunks of 512 cost 3 % of the time of one.  Two chunks are in TMEM at a time,
 // so that the MMAs of the next run meanwhile.
 //
-// What bounds it: 16-bit, the tensor core (65536 rows, 2048 x 4608: 795 us, 1555 TFLOP/s with 144
+// What bounds it: 16-bit, the tensor core (65536 rows, 2048 x 4608: 726 us, 1704 TFLOP/s with 144
 // tiles for 76 pairs) or, with few rows per expert, the gradients' bytes (16384 rows over 64
 // experts of 2048 x 7168 to fp32: 617 us, 6.6 TB/s).  8 bits, the epilogue: 2 operations for each
 // element of a 128-row block on the FMA pipe beside 512 clocks of MMA (the same rows: 579 us, 2136
@@ -47,17 +47,18 @@ constexpr int EPI_WARP0 = 4;
 constexpr int BN = 256;  // columns k of a tile
 constexpr uint32_t TMEM_COLS = 512;
 
-// CHUNK: stages of 64 rows that accumulate in TMEM, of 16-bit operands.  SPLIT: pairs, in one cluster,
-// that share a tile's rows, each cluster one tile.
-template <bool FP8_, int CG_, int STAGES_, int CHUNK_, int SPLIT_ = 1>
+// ROWS: of the operands in a stage.  SPLIT: pairs, in one cluster, that share a tile's rows, each
+// cluster one tile.
+template <bool FP8_, int ROWS_, int STAGES_, int SPLIT_ = 1>
 struct Cfg {
   static constexpr bool FP8 = FP8_;
-  static constexpr int CG = CG_;
+  static constexpr int CG = 2;
   static constexpr int SPLIT = SPLIT_;
-  static constexpr int BM = 128 * CG;             // columns n of a tile
-  static constexpr int ROWS = FP8 ? 128 : 64;     // rows of the operands in a stage
-  static constexpr int STEP = ROWS / 4;           // rows of an MMA (K = 32 or 16)
-  static constexpr int CHUNK = FP8 ? 1 : CHUNK_;  // stages that accumulate in TMEM
+  static constexpr int BM = 128 * CG;  // columns n of a tile
+  static constexpr int ROWS = ROWS_;
+  static constexpr int STEP = FP8 ? 32 : 16;  // rows of an MMA
+  static constexpr int STEPS = ROWS / STEP;
+  static constexpr int CHUNK = (FP8 ? 128 : 512) / ROWS;  // stages that accumulate in TMEM
   static constexpr int STAGES = STAGES_;
   static constexpr int BOX_COLS = FP8 ? 128 : 64;  // columns of a box: 128 bytes
   static constexpr uint32_t BOX = ROWS * 128;
@@ -400,9 +401,9 @@ wgrad_kernel(const __grid_constant__ CUtensorMap tmC, const __grid_constant__ CU
           const uint32_t d = tmem_base + acc * BN;
           const uint64_t mdesc = mdesc0 + ((stage * C::STAGE) >> 4);
           const uint64_t ndesc = ndesc0 + ((stage * C::STAGE) >> 4);
-          const int steps = rows - r >= C::ROWS ? 4 : (rows - r + C::STEP - 1) / C::STEP;
+          const int steps = rows - r >= C::ROWS ? C::STEPS : (rows - r + C::STEP - 1) / C::STEP;
 #pragma unroll
-          for (int k = 0; k < 4; ++k) {
+          for (int k = 0; k < C::STEPS; ++k) {
             if (k < steps) {
               const uint64_t go = (uint64_t)(k * C::STEP_BYTES) >> 4;
               if constexpr (C::FP8)
@@ -709,10 +710,15 @@ cudaError_t launch_wgrad(const WgradArgs& a, int num_sms, cudaStream_t stream) {
   const int64_t tiles = (int64_t)a.E * ((a.N + 255) / 256) * ((a.K + 255) / 256);
   const bool split = tiles * 9 <= num_sms && a.M_total >= (int64_t)1024 * a.E;
   if (a.fp8)
-    return split ? wg::by_type<wg::Cfg<true, 2, 4, 1, 4>>(a, num_sms, stream)
-                 : wg::by_type<wg::Cfg<true, 2, 4, 1>>(a, num_sms, stream);
-  return split ? wg::by_type<wg::Cfg<false, 2, 4, 8, 4>>(a, num_sms, stream)
-               : wg::by_type<wg::Cfg<false, 2, 4, 8>>(a, num_sms, stream);
+    return split ? wg::by_type<wg::Cfg<true, 128, 4, 4>>(a, num_sms, stream)
+                 : wg::by_type<wg::Cfg<true, 128, 4>>(a, num_sms, stream);
+  // Long groups take three stages of 128 rows: each stage has a round of barriers (16 groups of
+  // 2048 x 7168 to fp32, with stages of 64 rows and of 128: 384 rows each 219 and 184 us, 1024 rows
+  // 397 and 375, 2048 rows 692 and 635).  With short ones the gradients' bytes count, and what is
+  // loaded past a group's end (256 rows each 159 and 172 us, 8 groups of 40 rows 13.9 and 16.3).
+  if (split) return wg::by_type<wg::Cfg<false, 128, 3, 4>>(a, num_sms, stream);
+  return a.M_total >= (int64_t)384 * a.E ? wg::by_type<wg::Cfg<false, 128, 3>>(a, num_sms, stream)
+                                         : wg::by_type<wg::Cfg<false, 64, 4>>(a, num_sms, stream);
 }
 
 }  // namespace bsfp8
