@@ -20,11 +20,14 @@
 // a plain fp32 sum; chunks of 512 cost 3 % of the time of one.  Two chunks are in TMEM at a time,
 // so that the MMAs of the next run meanwhile.
 //
-// What bounds it: 16-bit, the tensor core (65536 rows, 2048 x 4608: 726 us, 1704 TFLOP/s with 144
-// tiles for 76 pairs) or, with few rows per expert, the gradients' bytes (16384 rows over 64
-// experts of 2048 x 7168 to fp32: 617 us, 6.6 TB/s).  8 bits, the epilogue: 2 operations for each
-// element of a 128-row block on the FMA pipe beside 512 clocks of MMA (the same rows: 579 us, 2136
-// TFLOP/s; without the scales' products 500, without any sums 440).  What made it so: the scales
+// What bounds it: 16-bit, the tensor core and the operands' way from L2 (65536 rows, 2048 x 4608:
+// 702 us, 1762 TFLOP/s with 144 tiles for 76 pairs; the loads alone 525) or, with few rows per
+// expert, the gradients' bytes (16384 rows over 64 experts of 2048 x 7168 to fp32: 637 us, 6.4
+// TB/s).  8 bits, the sums' way out of TMEM: every block of 128 rows has its own scales, so its sums
+// are handed to the epilogue after 512 clocks of MMA, and half of TMEM is taken until they are read
+// and their 2 operations per element under way (the same rows: 590 us, 2095 TFLOP/s; if 256 rows
+// made a block 438, without the scales' products 511, the loads alone 333).  The stage's commit is
+// the hand-over's too (16 groups of 2048 rows 594 -> 576).  What made it so: the scales
 // land with the operands, counted on their barrier (read from global memory two blocks ahead, the
 // epilogue waited for them: 826 us); a warp reads TMEM as 16 x 256-bit pieces, of which a thread
 // gets 4 rows x 32 columns, 36 scales, and not a row of 128 columns, 129 (shared memory is what the
@@ -76,7 +79,7 @@ struct Cfg {
   static constexpr uint32_t IDESC =
       (FP8 ? idesc_f8f6f4_e4m3(BM, BN) : idesc_f16_f32(BM, BN)) | IDESC_A_MN | IDESC_B_MN;
   // fp8: slots of a stage's scales, [256 columns k | 128 columns n] (see the producer)
-  static constexpr int SLOTS = 8;
+  static constexpr int SLOTS = 2 * STAGES;
   static constexpr uint32_t SLOT = (BN + 128) * 4;
   static constexpr uint32_t SMEM_SF = STAGES * STAGE;
   static constexpr uint32_t SMEM_CTL = SMEM_SF + (FP8 ? SLOTS * SLOT : 0);
@@ -250,7 +253,7 @@ wgrad_kernel(const __grid_constant__ CUtensorMap tmC, const __grid_constant__ CU
   const uint32_t warp = threadIdx.x >> 5;
   const uint32_t lane = threadIdx.x & 31;
   // of the CTA in its pair, its pair's leader in the cluster, and the pair's share of a split tile
-  const uint32_t cta = C::CG * C::SPLIT > 1 ? cluster_ctarank() : 0;
+  const uint32_t cta = cluster_ctarank();
   const uint32_t rank = cta % C::CG, leader = cta - rank, part = cta / C::CG;
   const uint16_t both = (uint16_t)(0x3 << leader);
   // the grid has no more clusters than there are tiles (as many, where they are split)
@@ -297,7 +300,7 @@ wgrad_kernel(const __grid_constant__ CUtensorMap tmC, const __grid_constant__ CU
   }
   tc_fence_before();
   __syncthreads();
-  if constexpr (C::CG * C::SPLIT > 1) cluster_sync();  // the peer's barriers before any use
+  cluster_sync();  // the peer's barriers before any use
   tc_fence_after();
   const uint32_t tmem_base = ctl->tmem_base;
   const bool valid = ctl->valid;  // both CTAs of a pair agree
@@ -333,9 +336,9 @@ wgrad_kernel(const __grid_constant__ CUtensorMap tmC, const __grid_constant__ CU
           const int32_t row = r0 + r;
           const int32_t at = r0 / 128 + (int)t.e + r / 128;  // fp8: its scales' row
           const uint32_t dst = base + C::SMEM_SF + slot * C::SLOT;
-          if (C::CG == 1 || r + C::ROWS > rows) {
-            // counted in this CTA: the fixer comes first where the group ends inside
-            const uint32_t bar = r + C::ROWS > rows ? tail_bar(stage) : full_bar(stage);
+          if (r + C::ROWS > rows) {
+            // the group ends inside: counted in this CTA, whose fixer comes first
+            const uint32_t bar = tail_bar(stage);
             mbar_arrive_expect_tx(bar, C::STAGE_TX);
 #pragma unroll
             for (int i = 0; i < C::M_BOXES; ++i)
@@ -382,17 +385,20 @@ wgrad_kernel(const __grid_constant__ CUtensorMap tmC, const __grid_constant__ CU
       const uint64_t ndesc0 = mnmajor_sw128_desc(base + C::M_BOXES * C::BOX, C::BOX);
       uint32_t stage = 0, phase = 0, acc = 0, acc_phase = 0;
       bool ok = true;
+      auto wait = [&](uint32_t bar, uint32_t parity) {
+        return C::FP8 ? mbar_wait(bar, parity, abort) : mbar_wait_sleep(bar, parity, abort);
+      };
       for (Walk t(tile0); ok && t.inside(shape); t.local += tile_stride) {
         int begin, rows;
         t.rows<C::SPLIT>(args, part, begin, rows);
         int in_chunk = 0;
         for (int r = begin; r < rows; r += C::ROWS) {
-          if (!mbar_wait_sleep(full_bar(stage), phase, abort)) {
+          if (!wait(full_bar(stage), phase)) {
             give_up(args.err, abort);
             ok = false;
             break;
           }
-          if (in_chunk == 0 && !mbar_wait_sleep(tempty_bar(acc), acc_phase ^ 1, abort)) {
+          if (in_chunk == 0 && !wait(tempty_bar(acc), acc_phase ^ 1)) {
             give_up(args.err, abort);
             ok = false;
             break;
@@ -412,20 +418,17 @@ wgrad_kernel(const __grid_constant__ CUtensorMap tmC, const __grid_constant__ CU
                 umma_f16<C::CG>(d, mdesc + go, ndesc + go, idesc, (in_chunk | k) > 0);
             }
           }
-          if constexpr (C::CG == 1) umma_commit(empty_bar(stage));
-          else umma_commit_pair(empty_bar(stage), both);
+          umma_commit_pair(empty_bar(stage), both);
           if (++stage == C::STAGES) { stage = 0; phase ^= 1; }
           if (++in_chunk == C::CHUNK || r + C::ROWS >= rows) {
-            if constexpr (C::CG == 1) umma_commit(tfull_bar(acc));
-            else umma_commit_pair(tfull_bar(acc), both);
+            if constexpr (!C::FP8) umma_commit_pair(tfull_bar(acc), both);
             in_chunk = 0;
             if (++acc == 2) { acc = 0; acc_phase ^= 1; }
           }
         }
       }
       // every MMA has finished before TMEM is released
-      if constexpr (C::CG == 1) umma_commit(smem_u32(&ctl->mma_done));
-      else umma_commit_pair(smem_u32(&ctl->mma_done), (uint16_t)(1 << leader));
+      umma_commit_pair(smem_u32(&ctl->mma_done), (uint16_t)(1 << leader));
       if (!mbar_wait_timed(smem_u32(&ctl->mma_done), 0)) give_up(args.err, abort);
     } else if (warp == 2) {
       // ----------------------------------- fixer -----------------------------------
@@ -458,7 +461,7 @@ wgrad_kernel(const __grid_constant__ CUtensorMap tmC, const __grid_constant__ CU
           if (rank == 1) {
             mbar_arrive_release_cluster(mapa_shared(peer_bar(last), leader));
           } else {
-            if (C::CG == 2 && !mbar_wait_cluster(peer_bar(last), parity, abort))
+            if (!mbar_wait_cluster(peer_bar(last), parity, abort))
               give_up(args.err, abort);
             else
               mbar_arrive(full_bar(last));
@@ -480,12 +483,13 @@ wgrad_kernel(const __grid_constant__ CUtensorMap tmC, const __grid_constant__ CU
     bool ok = true;
 
     uint32_t slot = 0;
-    // 16-bit chunks are long: the warps sleep, so as not to poll beside the MMA thread
+    // 16-bit chunks are long: the warps sleep, so as not to poll beside the MMA thread (8 bits: a
+    // wake-up counts at each block; as there, 597 -> 588 us)
     auto wait = [&](uint32_t bar, uint32_t parity) {
       return C::FP8 ? mbar_wait(bar, parity, abort) : mbar_wait_sleep(bar, parity, abort);
     };
-    const uint32_t tempty_0 = C::CG == 2 ? mapa_shared(tempty_bar(0), leader) : tempty_bar(0);
-    const uint32_t tempty_1 = C::CG == 2 ? mapa_shared(tempty_bar(1), leader) : tempty_bar(1);
+    const uint32_t tempty_0 = mapa_shared(tempty_bar(0), leader);
+    const uint32_t tempty_1 = mapa_shared(tempty_bar(1), leader);
     for (Walk t(tile0); t.inside(shape); t.local += tile_stride) {
       int begin, rows, n0, k0;
       t.rows<C::SPLIT>(args, part, begin, rows);
@@ -556,13 +560,13 @@ wgrad_kernel(const __grid_constant__ CUtensorMap tmC, const __grid_constant__ CU
         tmem_ld_16x256b_x4(taddr0 + acc * BN + 32 * q, p[q % 2][0]);
         tmem_ld_16x256b_x4(taddr0 + (16 << 16) + acc * BN + 32 * q, p[q % 2][1]);
       };
-      auto start = [&]() {
-        ok &= wait(tfull_bar(acc), acc_phase);
+      auto start = [&](uint32_t s) {  // fp8: a chunk is a stage, whose commit says so
+        ok &= C::FP8 ? wait(empty_bar(s % C::STAGES), s / C::STAGES) : wait(tfull_bar(acc), acc_phase);
         __syncwarp();
         tc_fence_after();
         load(0);
       };
-      if (rows > begin) start();
+      if (rows > begin) start(slot);
       for (int r = begin; r < rows; r += C::ROWS * C::CHUNK) {
         float sc[4];
         float2 sa[4];
@@ -586,7 +590,7 @@ wgrad_kernel(const __grid_constant__ CUtensorMap tmC, const __grid_constant__ CU
             __syncwarp();
             if (lane == 0) mbar_arrive_cluster_or_local<C::CG>(acc ? tempty_1 : tempty_0);
             if (++acc == 2) { acc = 0; acc_phase ^= 1; }
-            if (r + C::ROWS * C::CHUNK < rows) start();
+            if (r + C::ROWS * C::CHUNK < rows) start((slot + 1) % C::SLOTS);
           }
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
@@ -658,7 +662,7 @@ wgrad_kernel(const __grid_constant__ CUtensorMap tmC, const __grid_constant__ CU
   tc_fence_before();
   __syncthreads();
   // the pair's MMAs and remote arrivals are finished before either CTA frees TMEM or exits
-  if constexpr (C::CG * C::SPLIT > 1) cluster_sync();
+  cluster_sync();
   if (warp == 1) {
     tc_fence_after();
     tmem_dealloc<C::CG>(tmem_base, TMEM_COLS);
