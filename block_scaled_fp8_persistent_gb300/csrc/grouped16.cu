@@ -12,9 +12,9 @@
 // Two kernels, for what bounds them:
 //   few rows per expert: the weights' bytes.  One CTA takes 32 rows x 128 columns, and what counts is
 //   how many bytes are in flight: 9 stages of 16 KB of weights per SM.  The MMA (M = 128 rows of A)
-//   computes 96 rows that nobody reads.  2091 rows over 128 experts of 4096 x 2048: 323 us, 6.7 TB/s,
-//   99 % of the measured copy.  Where the tiles are fewer than the SMs, clusters of CTAs share a
-//   tile's K and add up their parts through distributed shared memory.
+//   computes 96 rows that nobody reads.  512 rows over 128 experts of 4096 x 2048: 307 us, 7.0 TB/s,
+//   more than a copy's rate, as next to nothing is written.  Where the tiles are fewer than the SMs,
+//   clusters of CTAs share a tile's K and add up their parts through distributed shared memory.
 //   more rows: the tensor core, and the way from L2 to it.  A CTA pair takes 256 columns x up to 512
 //   rows; the rows are the MMA's N, which goes by 16, so that a group's last rows cost what they are.
 //   8192^3: 560 us, 1960 TFLOP/s (a library product 557).
@@ -717,17 +717,23 @@ cudaError_t launch_pair(const Product16Args& args, int num_sms, cudaStream_t str
 
 template <bool BT>
 cudaError_t choose(const Product16Args& a, int num_sms, cudaStream_t stream) {
+  // More tiles of few rows than this there are not (the offsets live on the device); a tile's K is
+  // shared where that leaves each of the tile's CTAs a part and an SM.
+  const int64_t row_tiles = a.M_total / FEW_ROWS + (a.M_total < a.E ? a.M_total : a.E);
+  const int64_t few_tiles = row_tiles * ((a.N + FEW_COLS - 1) / FEW_COLS);
+  const int64_t blocks = (a.K + BK - 1) / BK;
   if (a.M_total <= (int64_t)32 * a.E) {
-    // more tiles than this there are not (the offsets live on the device); a tile's K is shared
-    // where that leaves each of the tile's CTAs a part and an SM
-    const int64_t row_tiles = a.M_total / FEW_ROWS + (a.M_total < a.E ? a.M_total : a.E);
-    const int64_t tiles = row_tiles * ((a.N + FEW_COLS - 1) / FEW_COLS);
-    const int64_t blocks = (a.K + BK - 1) / BK;
-    if (tiles * 8 <= num_sms && blocks >= 16) return launch_few<Few<BT, 8>>(a, tiles, num_sms, stream);
-    if (tiles * 4 <= num_sms && blocks >= 8) return launch_few<Few<BT, 4>>(a, tiles, num_sms, stream);
-    if (tiles * 2 <= num_sms && blocks >= 4) return launch_few<Few<BT, 2>>(a, tiles, num_sms, stream);
-    return launch_few<Few<BT, 1>>(a, tiles, num_sms, stream);
+    if (few_tiles * 8 <= num_sms && blocks >= 16) return launch_few<Few<BT, 8>>(a, few_tiles, num_sms, stream);
+    if (few_tiles * 4 <= num_sms && blocks >= 8) return launch_few<Few<BT, 4>>(a, few_tiles, num_sms, stream);
+    if (few_tiles * 2 <= num_sms && blocks >= 4) return launch_few<Few<BT, 2>>(a, few_tiles, num_sms, stream);
   }
+  // Up to 8 rows per group on average, most groups are one tile of 32 rows: less to load and to
+  // set up than in tiles of pairs (64 groups of 1 row, 2048 x 2048: 81 us against 88; 16 of 8, 2048
+  // x 4096: 45 and 48).  With more of them a few groups can hold many, and each reads its weights
+  // once per 32 rows (4027 rows over 128 groups, the largest 753, 4096 x 2048: 422 us against 330;
+  // 4096 rows in one of them 222 and 51; 16 rows in each 327 and 322).
+  if (a.M_total <= FEW_ROWS || a.M_total <= (int64_t)8 * a.E)
+    return launch_few<Few<BT, 1>>(a, few_tiles, num_sms, stream);
   // Of tiles of 512, 256, 128 or 64 rows the highest that give every pair of SMs some to do; 512
   // where groups are mostly over 256 or near it (64 groups of 260 rows, 7168 x 2048: 413 us, 509
   // with 256; groups of 128: 311 and 297) and there are enough of them to even out.
