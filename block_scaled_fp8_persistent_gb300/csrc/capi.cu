@@ -51,6 +51,22 @@ EncodeTiledFn encode_fn() {
   return fn;
 }
 
+// Whether the calling thread has a context (where the driver cannot be asked: not).
+bool has_context() {
+  using Fn = CUresult (*)(CUcontext*);
+  static const Fn fn = [] {
+    void* p = nullptr;
+    cudaDriverEntryPointQueryResult q;
+    if (cudaGetDriverEntryPointByVersion("cuCtxGetCurrent", &p, 12000, cudaEnableDefault, &q) !=
+            cudaSuccess ||
+        q != cudaDriverEntryPointSuccess)
+      p = nullptr;
+    return reinterpret_cast<Fn>(p);
+  }();
+  CUcontext c = nullptr;
+  return fn && fn(&c) == CUDA_SUCCESS && c;
+}
+
 constexpr int kMaxDevices = 64;
 
 struct DeviceInfo {
@@ -71,7 +87,7 @@ bsfp8_status device_info(DeviceInfo** out) {
   // are encoded by the driver, which wants one.
   static thread_local int bound = -1;
   if (bound != dev) {
-    if (cudaSetDevice(dev) != cudaSuccess) return BSFP8_ERR_CUDA;
+    if (!has_context() && cudaSetDevice(dev) != cudaSuccess) return BSFP8_ERR_CUDA;
     bound = dev;
   }
   std::lock_guard<std::mutex> lock(g_dev_mu);

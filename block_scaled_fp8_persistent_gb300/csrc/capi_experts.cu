@@ -11,6 +11,8 @@ namespace {
 bool aligned(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
 
 bool rows_ok(int64_t rows) { return rows >= 0 && rows <= INT32_MAX; }
+// of groups: a row past a group's last tile is still an int
+bool grouped_rows_ok(int64_t rows) { return rows >= 0 && rows <= INT32_MAX - 1024; }
 
 constexpr int kMaxWidth = 1 << 24;
 constexpr int kMaxGroups = 1 << 20;
@@ -30,7 +32,7 @@ bsfp8_status wgrad(const WgradArgs& a, int step, cudaStream_t stream) {
   if (!a.offsets || !a.dB ||
       (a.M_total > 0 && (!a.dC || !a.A || (a.fp8 && (!a.dc_scales || !a.a_scales)))))
     return BSFP8_ERR_NULL;
-  if (!rows_ok(a.M_total) || !matrix_ok(a.N, a.K, step) || !groups_ok(a.E)) return BSFP8_ERR_SHAPE;
+  if (!grouped_rows_ok(a.M_total) || !matrix_ok(a.N, a.K, step) || !groups_ok(a.E)) return BSFP8_ERR_SHAPE;
   if (!aligned(a.dC, 16) || !aligned(a.A, 16) || !aligned(a.dB, 16) || !aligned(a.add, 16) ||
       !aligned(a.dc_scales, 16) || !aligned(a.a_scales, 16) || !aligned(a.offsets, 4))
     return BSFP8_ERR_ALIGN;
@@ -49,7 +51,7 @@ extern "C" bsfp8_status bs16_grouped_gemm(int type, int transposed, const void* 
                                           int num_experts, cudaStream_t stream) {
   if (!half_type(type)) return BSFP8_ERR_FORMAT;
   if (!group_offsets || !B || (M_total > 0 && (!A || !C))) return BSFP8_ERR_NULL;
-  if (!rows_ok(M_total) || !matrix_ok(N, K, 8) || !groups_ok(num_groups) ||
+  if (!grouped_rows_ok(M_total) || !matrix_ok(N, K, 8) || !groups_ok(num_groups) ||
       !groups_ok(num_experts) || (!expert_ids && num_groups > num_experts))
     return BSFP8_ERR_SHAPE;
   if (!aligned(A, 16) || !aligned(B, 16) || !aligned(C, 16) || !aligned(group_offsets, 4) ||
@@ -95,7 +97,7 @@ extern "C" bsfp8_status bsfp8_quantize_columns(int x_type, const void* x,
   if (x_type < BSMX_BF16 || x_type > BSMX_FP32) return BSFP8_ERR_FORMAT;
   if (!group_offsets || (M_total > 0 && (!q || !scales || (x_rows > 0 && !x))))
     return BSFP8_ERR_NULL;
-  if (!rows_ok(M_total) || !rows_ok(x_rows) || K < 128 || K % 128 != 0 || K > (1 << 22) ||
+  if (!grouped_rows_ok(M_total) || !rows_ok(x_rows) || K < 128 || K % 128 != 0 || K > (1 << 22) ||
       !groups_ok(num_groups) || top_k < 1 || top_k > 64 ||
       (!slot_of_row && (top_k != 1 || x_rows != M_total)))
     return BSFP8_ERR_SHAPE;

@@ -134,7 +134,7 @@ __device__ __forceinline__ int check_groups(const int32_t* off, const int32_t* i
   for (int e = (int)lane; e < E; e += 32) {
     const int a = off[e], b = off[e + 1];
     if (a < 0 || b < a || b > M_total || (e == 0 && a != 0)) good = 0;
-    else tiles += (b - a + BM - 1) / BM;
+    else tiles += ((int64_t)b - a + BM - 1) / BM;
     if (ids) {
       const int x = ids[e];
       if (x < 0 || x >= num_experts) good_ids = 0;

@@ -162,7 +162,9 @@ __global__ void __launch_bounds__(kThreads, kResident<XT, GATHER>)
       }
     }
     bytes[j] = row < 0 ? 0 : 16;
-    from[j] = static_cast<const char*>(a.x) + ((row < 0 ? 0 : row) * a.K + tile0 * kTileCols + 8 * c) * kBytes;
+    // (an address for none: x may be NULL where it has no rows)
+    from[j] = row < 0 ? reinterpret_cast<const char*>(a.q)
+                      : static_cast<const char*>(a.x) + (row * a.K + tile0 * kTileCols + 8 * c) * kBytes;
   }
   uint8_t* const mine = stages + threadIdx.x * kEightBytes<XT>;  // + stage, + row j
   const uint32_t mine_u32 = smem_u32(mine);

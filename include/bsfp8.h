@@ -409,7 +409,8 @@ bsfp8_status bsmx_moe_combine_backward(const void* d_out, const void* C,
  *                  M_total = rows * top_k, whether slots were dropped or not.  Offsets that are
  *                  not so are recorded as BSFP8_ERR_DEVICE_OFFSETS.
  *
- * Groups may be empty; num_groups and num_experts are at most 2^20; M_total, N and K as below.
+ * Groups may be empty; num_groups and num_experts are at most 2^20, M_total at most 2^31 - 1025
+ * (BSFP8_ERR_SHAPE); N and K as below.
  * Sums are held in fp32.  The same inputs give the same bits every time: each sum has one order.
  */
 

@@ -610,3 +610,28 @@ def test_expert_ids_out_of_range(ids):
                             expert_ids=torch.tensor(ids, dtype=torch.int32, device="cuda"))
     assert bsfp8.bsfp8_get_device_error() == IDS_ERROR
     assert torch.all(C == 7)
+
+
+@pytest.mark.parametrize("transposed", [False, True])
+@pytest.mark.parametrize("sizes", [[0] * 60 + [70, 3], [1] * 40 + [33, 64, 200], [16] * 20 + [600, 0, 5], [31, 1, 0, 0, 0, 0, 0, 40]], ids=str)
+@pytest.mark.parametrize("N,K", [(264, 200), (1032, 520)])
+def test_product_groups_of_very_different_sizes(sizes, N, K, transposed):
+    _product(sizes, N, K, BF16, transposed, seed=N)
+
+
+@pytest.mark.parametrize("dtype,out", [(BF16, FP32), (FP16, FP16)])
+def test_wgrad_many_rows_added_in_place(dtype, out):
+    _wgrad([4000, 0, 3001], 264, 200, dtype, out, add=True, in_place=True)
+
+
+def test_wgrad8_many_rows_added_in_place():
+    _wgrad8([4000, 0, 3001], 256, 128, FP32, add=True, in_place=True)
+
+
+def test_columns_of_no_tokens():
+    rows, K = 150, 256
+    off, slots = ref.offsets_of([100, 50]).cuda(), torch.full((rows,), -1, dtype=torch.int32, device="cuda")
+    q, s = torch.ones(rows, K, dtype=torch.uint8, device="cuda"), torch.zeros(rows // 128 + 2, K, device="cuda")
+    bsfp8.bsfp8_quantize_columns(None, off, q, s, rows, K, 2, slot_of_row=slots, top_k=2, x_rows=0, x_type="bf16")
+    _no_error()
+    assert torch.all(q == 0) and torch.all(s[:2] == 1)

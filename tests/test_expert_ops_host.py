@@ -168,3 +168,13 @@ def test_columns_by_hand():
     q, s = ref.quantise_columns(x, ref.offsets_of([130]))
     v = q.view(ref.E4M3).float()
     assert s[0, 0] == 1 and s[0, 1] == 1 and s[1, 1] == 2 and v[0, 0] == 448 and v[5, 0] == -1 and v[129, 1] == 448
+
+
+@pytest.mark.parametrize("M,status", [((1 << 31) - 1, SHAPE), ((1 << 31) - 1024, SHAPE), ((1 << 31) - 1025, ALIGN)])
+def test_rows_end_before_the_last_tile_would_pass_an_int(lib, M, status):
+    # (what is accepted goes on to the alignment)
+    bad = FAKE + 8
+    assert lib.bs16_grouped_gemm(0, 0, bad, FAKE, FAKE, None, FAKE, M, 8, 8, 1, 1, None) == status
+    assert lib.bs16_grouped_wgrad(0, 2, bad, FAKE, FAKE, None, FAKE, M, 8, 8, 1, None) == status
+    assert lib.bsfp8_grouped_wgrad(2, bad, FAKE, FAKE, FAKE, FAKE, None, FAKE, M, 128, 128, 1, None) == status
+    assert lib.bsfp8_quantize_columns(0, bad, None, 1, FAKE, FAKE, FAKE, M, M, 128, 1, None) == status
