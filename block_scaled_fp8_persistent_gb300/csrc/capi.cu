@@ -296,18 +296,20 @@ int bsfp8::device_error_word_and_sms(int** err, int* num_sms) {
   return st;
 }
 
-bool bsfp8::encode_swizzled(CUtensorMap* map, bool bytes, const void* base, int rank,
+bool bsfp8::encode_swizzled(CUtensorMap* map, int size, const void* base, int rank,
                             const uint64_t* dims, uint32_t box_rows) {
   EncodeTiledFn fn = encode_fn();
   if (!fn || rank < 2 || rank > 3) return false;
-  const cuuint64_t size = bytes ? 1 : 2;
   cuuint64_t d[3], strides[2];
   for (int i = 0; i < rank; ++i) {
     d[i] = dims[i];
-    if (i > 0) strides[i - 1] = (i > 1 ? strides[i - 2] : size) * dims[i - 1];
+    if (i > 0) strides[i - 1] = (i > 1 ? strides[i - 2] : (cuuint64_t)size) * dims[i - 1];
   }
   const cuuint32_t box[3] = {(cuuint32_t)(128 / size), box_rows, 1}, one[3] = {1, 1, 1};
-  return fn(map, bytes ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_UINT16,
+  return fn(map,
+            size == 1   ? CU_TENSOR_MAP_DATA_TYPE_UINT8
+            : size == 2 ? CU_TENSOR_MAP_DATA_TYPE_UINT16
+                        : CU_TENSOR_MAP_DATA_TYPE_FLOAT32,
             (cuuint32_t)rank, const_cast<void*>(base), d, strides, box, one,
             CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
             CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;

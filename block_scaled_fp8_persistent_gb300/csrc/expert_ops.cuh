@@ -18,9 +18,9 @@ namespace bsfp8 {
 int device_error_word_and_sms(int** err, int* num_sms);
 
 // Tensor map of a row-major array of `rank` dimensions, innermost first, whose box is 128 bytes
-// wide and swizzled over them; what lies outside reads as zero.  bytes: elements of one byte,
-// else of two.  False if the driver refuses it.  capi.cu.
-bool encode_swizzled(CUtensorMap* map, bool bytes, const void* base, int rank,
+// wide and swizzled over them; what lies outside reads as zero and is not written.  Elements of
+// `size` bytes: 1, 2 or 4 (fp32).  False if the driver refuses it.  capi.cu.
+bool encode_swizzled(CUtensorMap* map, int size, const void* base, int rank,
                      const uint64_t* dims, uint32_t box_rows);
 
 // Tensor map of an fp32 array [rows, cols] whose box is one row of box_cols, not swizzled.

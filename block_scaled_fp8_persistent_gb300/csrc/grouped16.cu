@@ -333,8 +333,8 @@ cudaError_t launch_few(const Product16Args& args, int64_t max_tiles, int num_sms
   const uint64_t a_dims[2] = {(uint64_t)args.K, (uint64_t)args.M_total};
   const uint64_t b_dims[3] = {(uint64_t)(F::BT ? args.N : args.K),
                               (uint64_t)(F::BT ? args.K : args.N), (uint64_t)args.num_experts};
-  if (!encode_swizzled(&tmA, false, args.A, 2, a_dims, FEW_ROWS) ||
-      !encode_swizzled(&tmB, false, args.B, 3, b_dims, F::BT ? BK : FEW_COLS))
+  if (!encode_swizzled(&tmA, 2, args.A, 2, a_dims, FEW_ROWS) ||
+      !encode_swizzled(&tmB, 2, args.B, 3, b_dims, F::BT ? BK : FEW_COLS))
     return cudaErrorInvalidValue;
   const cudaError_t e = allow_smem<product16_few_kernel<F>>(kFewSmem);
   if (e != cudaSuccess) return e;
@@ -701,10 +701,10 @@ cudaError_t launch_pair(const Product16Args& args, int num_sms, cudaStream_t str
   const uint64_t a_dims[2] = {(uint64_t)args.K, (uint64_t)args.M_total};
   const uint64_t b_dims[3] = {(uint64_t)(P::BT ? args.N : args.K),
                               (uint64_t)(P::BT ? args.K : args.N), (uint64_t)args.num_experts};
-  if (!encode_swizzled(&tmA, false, args.A, 2, a_dims, 128) ||
-      !encode_swizzled(&tmA64, false, args.A, 2, a_dims, 64) ||
-      !encode_swizzled(&tmA32, false, args.A, 2, a_dims, 32) ||
-      !encode_swizzled(&tmB, false, args.B, 3, b_dims, P::BT ? BK : 128))
+  if (!encode_swizzled(&tmA, 2, args.A, 2, a_dims, 128) ||
+      !encode_swizzled(&tmA64, 2, args.A, 2, a_dims, 64) ||
+      !encode_swizzled(&tmA32, 2, args.A, 2, a_dims, 32) ||
+      !encode_swizzled(&tmB, 2, args.B, 3, b_dims, P::BT ? BK : 128))
     return cudaErrorInvalidValue;
   const cudaError_t e = allow_smem<product16_pair_kernel<P>>(kPairSmem);
   if (e != cudaSuccess) return e;

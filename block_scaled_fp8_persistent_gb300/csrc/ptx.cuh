@@ -284,6 +284,31 @@ __device__ __forceinline__ void tma_load_2d_mc_pair_hint(uint32_t dst, const voi
       : "memory");
 }
 
+// A box of shared memory to a tensor, whose part outside the tensor is not written; counted in the
+// thread's bulk groups.
+__device__ __forceinline__ void tma_store_3d_hint(const void* map, uint32_t src, int32_t x,
+                                                  int32_t y, int32_t z, uint64_t policy) {
+  asm volatile(
+      "cp.async.bulk.tensor.3d.global.shared::cta.bulk_group.L2::cache_hint [%0, {%2, %3, %4}], "
+      "[%1], %5;" ::"l"(map), "r"(src), "r"(x), "r"(y), "r"(z), "l"(policy)
+      : "memory");
+}
+
+__device__ __forceinline__ void bulk_commit() {
+  asm volatile("cp.async.bulk.commit_group;" ::: "memory");
+}
+
+// All but the last N groups of this thread have read their shared memory.
+template <int N>
+__device__ __forceinline__ void bulk_wait_read() {
+  asm volatile("cp.async.bulk.wait_group.read %0;" ::"n"(N) : "memory");
+}
+
+// Every group of this thread is written.
+__device__ __forceinline__ void bulk_wait_all() {
+  asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
+}
+
 // Non-tensor bulk copy global -> this CTA's shared memory, completion counted on `bar`
 // (bytes).  dst, src and bytes must be multiples of 16.
 __device__ __forceinline__ void bulk_copy_g2s_hint(uint32_t dst, const void* src, uint32_t bytes,

@@ -22,12 +22,12 @@
 //
 // What bounds it: 16-bit, the tensor core and the operands' way from L2 (65536 rows, 2048 x 4608:
 // 702 us, 1762 TFLOP/s with 144 tiles for 76 pairs; the loads alone 525) or, with few rows per
-// expert, the gradients' bytes (16384 rows over 64 experts of 2048 x 7168 to fp32: 637 us, 6.4
+// expert, the gradients' bytes (16384 rows over 64 experts of 2048 x 7168 to fp32: 612 us, 6.6
 // TB/s).  8 bits, the sums' way out of TMEM: every block of 128 rows has its own scales, so its sums
 // are handed to the epilogue after 512 clocks of MMA, and half of TMEM is taken until they are read
-// and their 2 operations per element under way (the same rows: 590 us, 2095 TFLOP/s; if 256 rows
+// and their 2 operations per element under way (the same rows: 589 us, 2099 TFLOP/s; if 256 rows
 // made a block 438, without the scales' products 511, the loads alone 333).  The stage's commit is
-// the hand-over's too (16 groups of 2048 rows 594 -> 576).  What made it so: the scales
+// the hand-over's too (16 groups of 2048 rows 594 -> 576), and the sums go out by TMA (565).  What made it so: the scales
 // land with the operands, counted on their barrier (read from global memory two blocks ahead, the
 // epilogue waited for them: 826 us); a warp reads TMEM as 16 x 256-bit pieces, of which a thread
 // gets 4 rows x 32 columns, 36 scales, and not a row of 128 columns, 129 (shared memory is what the
@@ -51,8 +51,8 @@ constexpr int BN = 256;  // columns k of a tile
 constexpr uint32_t TMEM_COLS = 512;
 
 // ROWS: of the operands in a stage.  SPLIT: pairs, in one cluster, that share a tile's rows, each
-// cluster one tile.
-template <bool FP8_, int ROWS_, int STAGES_, int SPLIT_ = 1>
+// cluster one tile.  STAGED: the gradients are stored by TMA, out of shared memory.
+template <bool FP8_, int ROWS_, int STAGES_, bool STAGED_, int SPLIT_ = 1>
 struct Cfg {
   static constexpr bool FP8 = FP8_;
   static constexpr int CG = 2;
@@ -81,8 +81,14 @@ struct Cfg {
   // fp8: slots of a stage's scales, [256 columns k | 128 columns n] (see the producer)
   static constexpr int SLOTS = 2 * STAGES;
   static constexpr uint32_t SLOT = (BN + 128) * 4;
-  static constexpr uint32_t SMEM_SF = STAGES * STAGE;
+  // where a warp of the epilogue puts 32 rows of 128 bytes for TMA to store: twice, where it fits
+  static constexpr uint32_t OUT_BOX = 4096;
+  static constexpr int OUT_BOXES =
+      !STAGED_ ? 0 : STAGES * STAGE + 16 * OUT_BOX + (FP8 ? SLOTS * SLOT : 0) <= 224 * 1024 ? 2 : 1;
+  static constexpr uint32_t SMEM_OUT = STAGES * STAGE;
+  static constexpr uint32_t SMEM_SF = SMEM_OUT + 8 * OUT_BOXES * OUT_BOX;
   static constexpr uint32_t SMEM_CTL = SMEM_SF + (FP8 ? SLOTS * SLOT : 0);
+  static_assert(SPLIT == 1 || !STAGED_, "a split tile's stripes are stored by their threads");
   static_assert(!FP8 || SLOTS >= STAGES + 2, "a slot is read to the end before it is filled again");
 };
 
@@ -240,10 +246,45 @@ __device__ __forceinline__ void store_row(void* dB, int64_t at, float2 (&v)[4], 
   }
 }
 
+// A box for TMA to store, of a warp's 32 rows and their columns 32 g.. (fp32) or 64 g..: 128 bytes of
+// each row, 16-byte chunk c of row r at c ^ r % 8.  The lanes of odd rows begin with other columns,
+// so that no two of a half-warp meet in a bank.
+template <int OUT>
+__device__ __forceinline__ void fill_box(uint32_t box, const float2 (&sum)[4][4][4], int g, uint32_t lane) {
+  const uint32_t r = lane / 4, q = lane % 4;
+  const uint32_t at = box + r * 128;
+  if constexpr (OUT == GRAD_FP32) {
+    const bool odd = r % 2;
+    const uint32_t chunk = (q / 2) ^ r ^ (odd ? 4 : 0);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+#pragma unroll
+      for (int s = 0; s < 4; ++s) {
+        const float2 v = odd ? sum[i][g][s ^ 2] : sum[i][g][s];
+        asm volatile("st.shared.v2.f32 [%0], {%1, %2};" ::"r"(at + i * 1024 + ((chunk ^ (2 * s)) << 4) + 8 * (q % 2)),
+                     "f"(v.x), "f"(v.y)
+                     : "memory");
+      }
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+#pragma unroll
+      for (int c = 0; c < 8; ++c) {
+        const float2 v = sum[i][2 * g + c / 4][c % 4];
+        asm volatile("st.shared.b32 [%0], %1;" ::"r"(at + i * 1024 + ((r ^ c) << 4) + 4 * q),
+                     "r"(OUT == GRAD_BF16 ? pack_bf16x2(v.x, v.y) : pack_f16x2(v.x, v.y))
+                     : "memory");
+      }
+    }
+  }
+}
+
 template <class C, int OUT>
 __global__ void __launch_bounds__(THREADS, 1)
 wgrad_kernel(const __grid_constant__ CUtensorMap tmC, const __grid_constant__ CUtensorMap tmA,
              const __grid_constant__ CUtensorMap tmSC, const __grid_constant__ CUtensorMap tmSA,
+             const __grid_constant__ CUtensorMap tmD,  // dB, to be stored
              const WgradArgs args, const Shape shape) {
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
@@ -528,10 +569,13 @@ wgrad_kernel(const __grid_constant__ CUtensorMap tmC, const __grid_constant__ CU
             }
           }
         }
-        if constexpr (OUT != GRAD_FP32) {
-          // The exchange waits for the values: the next tile's go into L2 meanwhile, a line at a
-          // time (64 experts of 2048 x 7168, 256 rows each, bf16 added: 1319 -> 1058 us; fp32
-          // pairs are waited for by the first sums only, and lose by it, 1309 -> 1500).
+        // The next tile's go into L2 meanwhile, a line at a time.  16-bit values are waited for by the
+        // exchange (64 experts of 2048 x 7168, 256 rows each, bf16 added: 1319 -> 1058 us).  fp32
+        // pairs are waited for by the first sums only: 8 bits gain by it where a tile takes long
+        // enough to hide the lines (32 experts, 384 rows each 873 -> 735 us, 256 rows 627 -> 697), 16
+        // bits lose (384 rows 643 -> 771, 1024 rows 825 -> 830).
+        if (OUT != GRAD_FP32 || (C::FP8 && rows - begin >= 384)) {
+          constexpr int SIZE = OUT == GRAD_FP32 ? 4 : 2;
           Walk next = t;
           next.local += tile_stride;
           if (next.inside(shape)) {
@@ -539,12 +583,14 @@ wgrad_kernel(const __grid_constant__ CUtensorMap tmC, const __grid_constant__ CU
             next.corner<C::BM>(shape, n, k);
             n += 128 * (int)rank + (int)quarter * 32 + (int)lane;
             k += (int)half * 128;
-            const uint16_t* p = static_cast<const uint16_t*>(args.add) +
-                                ((int64_t)next.e * args.N + n) * args.K + k;
+            const uint8_t* p = static_cast<const uint8_t*>(args.add) +
+                               (((int64_t)next.e * args.N + n) * args.K + k) * SIZE;
 #pragma unroll
-            for (int c = 0; c < 128; c += 64)
-              if (n < args.N && k + c < args.K) prefetch_l2(p + c);
+            for (int c = 0; c < 128; c += 128 / SIZE)
+              if (n < args.N && k + c < args.K) prefetch_l2(p + c * SIZE);
           }
+        }
+        if constexpr (OUT != GRAD_FP32) {
 #pragma unroll
           for (int i = 0; i < 4; ++i)
 #pragma unroll
@@ -613,6 +659,27 @@ wgrad_kernel(const __grid_constant__ CUtensorMap tmC, const __grid_constant__ CU
         if constexpr (C::SPLIT > 1) cluster_sync();
         break;
       }
+      if constexpr (C::OUT_BOXES > 0) {
+        // The sums go out by way of shared memory, and the next tile's begin meanwhile.
+        constexpr int COLS = OUT == GRAD_FP32 ? 32 : 64;
+        const uint32_t out = base + C::SMEM_OUT + (warp - EPI_WARP0) * (C::OUT_BOXES * C::OUT_BOX);
+        const int row = n0 - (int)lane / 4;
+#pragma unroll
+        for (int g = 0; g < 128 / COLS; ++g) {
+          const uint32_t box = out + g % C::OUT_BOXES * C::OUT_BOX;
+          if (lane == 0) bulk_wait_read<C::OUT_BOXES - 1>();
+          __syncwarp();
+          fill_box<OUT>(box, sum, g, lane);
+          fence_proxy_async_smem();
+          __syncwarp();
+          if (lane == 0) {
+            if (row < args.N && k0 + g * COLS < args.K)
+              tma_store_3d_hint(&tmD, box, k0 + g * COLS, row, (int)t.e, pol);
+            bulk_commit();
+          }
+        }
+        continue;
+      }
       // A split tile: the parts go into shared memory, and each pair adds up a stripe of rows, in
       // the pairs' order.  (A pair that gave up has said so, and the sums mean nothing.)
       const uint32_t mine = base + (warp - EPI_WARP0) * (64 * 32 * 8) + lane * 8;
@@ -657,6 +724,7 @@ wgrad_kernel(const __grid_constant__ CUtensorMap tmC, const __grid_constant__ CU
         }
       }
     }
+    if (lane == 0) bulk_wait_all();
   }
 
   tc_fence_before();
@@ -672,12 +740,15 @@ wgrad_kernel(const __grid_constant__ CUtensorMap tmC, const __grid_constant__ CU
 template <class C, int OUT>
 cudaError_t launch(const WgradArgs& args, int num_sms, cudaStream_t stream) {
   static_assert(smem_bytes<C>() <= 227 * 1024, "shared memory per CTA");
-  CUtensorMap tmC, tmA;
+  CUtensorMap tmC, tmA, tmD = {};
   // with no rows nothing is loaded; a map still needs a row
   const uint64_t rows = args.M_total > 0 ? (uint64_t)args.M_total : 1;
   const uint64_t c_dims[2] = {(uint64_t)args.N, rows}, a_dims[2] = {(uint64_t)args.K, rows};
-  if (!encode_swizzled(&tmC, C::FP8, args.M_total > 0 ? args.dC : args.dB, 2, c_dims, C::ROWS) ||
-      !encode_swizzled(&tmA, C::FP8, args.M_total > 0 ? args.A : args.dB, 2, a_dims, C::ROWS))
+  if (!encode_swizzled(&tmC, C::FP8 ? 1 : 2, args.M_total > 0 ? args.dC : args.dB, 2, c_dims, C::ROWS) ||
+      !encode_swizzled(&tmA, C::FP8 ? 1 : 2, args.M_total > 0 ? args.A : args.dB, 2, a_dims, C::ROWS))
+    return cudaErrorInvalidValue;
+  const uint64_t d_dims[3] = {(uint64_t)args.K, (uint64_t)args.N, (uint64_t)args.E};
+  if (C::OUT_BOXES > 0 && !encode_swizzled(&tmD, OUT == GRAD_FP32 ? 4 : 2, args.dB, 3, d_dims, 32))
     return cudaErrorInvalidValue;
   CUtensorMap tmSC = {}, tmSA = {};
   if constexpr (C::FP8) {
@@ -694,7 +765,7 @@ cudaError_t launch(const WgradArgs& args, int num_sms, cudaStream_t stream) {
   const int64_t tiles = (int64_t)shape.experts * shape.nt * shape.kt;
   const int64_t units = num_sms / C::CG;
   return launch_persistent(wgrad_kernel<C, OUT>, C::SPLIT > 1 || tiles < units ? tiles : units,
-                           C::CG * C::SPLIT, THREADS, smem_bytes<C>(), stream, tmC, tmA, tmSC, tmSA,
+                           C::CG * C::SPLIT, THREADS, smem_bytes<C>(), stream, tmC, tmA, tmSC, tmSA, tmD,
                            args, shape);
 }
 
@@ -713,16 +784,33 @@ cudaError_t launch_wgrad(const WgradArgs& a, int num_sms, cudaStream_t stream) {
   // Few tiles and many rows: four pairs share a tile's rows (8192 rows, 512 x 512: 54 -> 21 us).
   const int64_t tiles = (int64_t)a.E * ((a.N + 255) / 256) * ((a.K + 255) / 256);
   const bool split = tiles * 9 <= num_sms && a.M_total >= (int64_t)1024 * a.E;
-  if (a.fp8)
-    return split ? wg::by_type<wg::Cfg<true, 128, 4, 4>>(a, num_sms, stream)
-                 : wg::by_type<wg::Cfg<true, 128, 4>>(a, num_sms, stream);
-  // Long groups take three stages of 128 rows: each stage has a round of barriers (16 groups of
-  // 2048 x 7168 to fp32, with stages of 64 rows and of 128: 384 rows each 219 and 184 us, 1024 rows
-  // 397 and 375, 2048 rows 692 and 635).  With short ones the gradients' bytes count, and what is
-  // loaded past a group's end (256 rows each 159 and 172 us, 8 groups of 40 rows 13.9 and 16.3).
-  if (split) return wg::by_type<wg::Cfg<false, 128, 3, 4>>(a, num_sms, stream);
-  return a.M_total >= (int64_t)384 * a.E ? wg::by_type<wg::Cfg<false, 128, 3>>(a, num_sms, stream)
-                                         : wg::by_type<wg::Cfg<false, 64, 4>>(a, num_sms, stream);
+  // The gradients go out through shared memory and TMA, so that the epilogue takes up the next tile's
+  // sums at once, or straight from the threads, in whole lines.  Which is faster was measured (32
+  // experts of 2048 x 7168, us straight and by TMA):
+  //   fp32 added to: straight, as the sums wait for what is added anyway and the stores then come
+  //     evenly (8 bits, 256 rows each 627 and 765; 16 bits, 384 rows 643 and 730)
+  //   fp32, short groups: straight, as the stores are what bounds it and mix worse with the operands'
+  //     loads the further those run ahead (256 rows: 311 and 337, 8 bits 322 and 334); long groups or
+  //     few tiles: TMA (512 rows 486 and 452, 8 bits 506 and 475; 8 experts of 2048 x 1024, 40 rows
+  //     each, in 8 bits 18.0 and 16.0, 20 rows to bf16 12.6 and 11.5)
+  //   16 bits out, half the bytes: TMA in 8 bits (256 rows 235 and 203) and where it is added to (464
+  //     and 366), else straight (512 rows 380 and 391)
+  const int64_t rounds = (tiles * 2 + num_sms - 1) / num_sms;
+  const bool wide = a.out_type == GRAD_FP32;
+  if (a.fp8) {
+    if (split) return wg::by_type<wg::Cfg<true, 128, 4, false, 4>>(a, num_sms, stream);
+    const bool staged = !wide || (!a.add && (rounds <= 4 || a.M_total >= (int64_t)384 * a.E));
+    return staged ? wg::by_type<wg::Cfg<true, 128, 4, true>>(a, num_sms, stream)
+                  : wg::launch<wg::Cfg<true, 128, 4, false>, GRAD_FP32>(a, num_sms, stream);
+  }
+  if (split) return wg::by_type<wg::Cfg<false, 128, 3, false, 4>>(a, num_sms, stream);
+  const bool long_groups = a.M_total >= (int64_t)384 * a.E;
+  const bool staged = a.add ? !wide : rounds <= 4 || (wide && long_groups);
+  if (long_groups)
+    return staged ? wg::by_type<wg::Cfg<false, 128, 3, true>>(a, num_sms, stream)
+                  : wg::by_type<wg::Cfg<false, 128, 3, false>>(a, num_sms, stream);
+  return staged ? wg::by_type<wg::Cfg<false, 64, 4, true>>(a, num_sms, stream)
+                : wg::by_type<wg::Cfg<false, 64, 4, false>>(a, num_sms, stream);
 }
 
 }  // namespace bsfp8
