@@ -63,8 +63,8 @@ extern "C" bsfp8_status bs16_grouped_gemm(int type, int transposed, const void* 
   if (st != BSFP8_OK) return st;
   if (M_total == 0) return BSFP8_OK;
   return launched(launch_product16(
-      Product16Args{group_offsets, expert_ids, M_total, N, K, num_groups, num_experts, 0, INT64_MAX,
-                    err, A, B, C, type == BSMX_BF16, transposed != 0},
+      Product16Args{group_offsets, expert_ids, M_total, N, K, num_groups, num_experts, err,
+                    A, B, C, type == BSMX_BF16, transposed != 0},
       sms, stream));
 }
 

@@ -27,8 +27,7 @@ bool encode_swizzled(CUtensorMap* map, int size, const void* base, int rank,
 bool encode_rows_f32(CUtensorMap* map, const void* base, uint64_t cols, uint64_t rows,
                      uint32_t box_cols);
 
-// C[m, n] = sum_k A[m, k] B[e, n, k], or B[e, k, n] (transposed), in bf16 or fp16; the members
-// up to `err` are those that the tile scheduler and the offsets' check read.
+// C[m, n] = sum_k A[m, k] B[e, n, k], or B[e, k, n] (transposed), in bf16 or fp16.
 struct Product16Args {
   const int32_t* offsets;     // [E + 1]
   const int32_t* expert_ids;  // [E], or nullptr: group e multiplies expert e
@@ -36,7 +35,6 @@ struct Product16Args {
   int N, K;
   int E;            // groups
   int num_experts;  // experts in B
-  int64_t min_group_rows, max_group_rows;
   int* err;
   const void* A;
   const void* B;
@@ -115,6 +113,34 @@ cudaError_t allow_smem(size_t bytes) {
       cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
   if (e == cudaSuccess && dev < 64) set[dev].store(true, std::memory_order_release);
   return e;
+}
+
+// How many clusters of `cluster` blocks of a kernel the device holds at once (SMs of a cluster are
+// of one GPC, so some stay over: of 152 SMs 36 clusters of 4, 15 of 8), asked once per device.
+template <auto kernel>
+int64_t clusters_at_once(int cluster, int threads, size_t smem) {
+  static std::atomic<int> known[64];
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess) return 0;
+  if (dev < 64) {
+    const int n = known[dev].load(std::memory_order_relaxed);
+    if (n > 0) return n - 1;
+  }
+  if (allow_smem<kernel>(smem) != cudaSuccess) return 0;
+  cudaLaunchAttribute attr = {};
+  attr.id = cudaLaunchAttributeClusterDimension;
+  attr.val.clusterDim.x = cluster;
+  attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(cluster);
+  cfg.blockDim = dim3(threads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+  int n = 0;
+  if (cudaOccupancyMaxActiveClusters(&n, kernel, &cfg) != cudaSuccess) return 0;
+  if (dev < 64) known[dev].store(n + 1, std::memory_order_relaxed);
+  return n;
 }
 
 // ---------------------------------------------------------------------------------------

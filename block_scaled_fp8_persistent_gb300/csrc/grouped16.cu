@@ -46,6 +46,114 @@ struct Turns {
   }
 };
 
+// The groups that have rows, in shared memory: the first row and the expert of each, and behind them
+// the last one's end.  A walk over the offsets themselves waits for L2 at every group, empty ones too
+// (9 rows in 128 groups, 168 x 864: 17.9 us, listed 6.2).  Above LISTED of them the walk does that.
+constexpr int LISTED = 192;
+struct GroupList {
+  int count;  // or -1: too many
+  int2 at[LISTED + 1];
+};
+
+// One full warp lists the groups, checks them and counts their tiles of BM rows (check_groups).
+template <int BM>
+__device__ __forceinline__ int list_groups(const Product16Args& a, GroupList& list, int64_t& row_tiles) {
+  constexpr int kAhead = 4;  // loads of 32 groups each, under way together
+  const uint32_t lane = lane_id();
+  int good = 1, good_ids = 1, count = 0;
+  long long tiles = 0;
+  for (int e0 = 0; e0 < a.E; e0 += 32 * kAhead) {
+    int lo[kAhead], hi[kAhead], be[kAhead];
+#pragma unroll
+    for (int i = 0; i < kAhead; ++i) {
+      const int e = e0 + 32 * i + (int)lane;
+      const bool in = e < a.E;
+      lo[i] = in ? a.offsets[e] : 0;
+      hi[i] = in ? a.offsets[e + 1] : 0;
+      be[i] = in && a.expert_ids ? a.expert_ids[e] : e;
+    }
+#pragma unroll
+    for (int i = 0; i < kAhead; ++i) {
+      const int e = e0 + 32 * i + (int)lane;
+      if (lo[i] < 0 || hi[i] < lo[i] || hi[i] > a.M_total || (e == 0 && lo[i] != 0)) good = 0;
+      if (e < a.E && (be[i] < 0 || be[i] >= a.num_experts)) good_ids = 0;
+      const bool some = hi[i] > lo[i];
+      if (some) tiles += ((int64_t)hi[i] - lo[i] + BM - 1) / BM;
+      const uint32_t others = __ballot_sync(0xffffffffu, some);
+      const int at = count + __popc(others & ((1u << lane) - 1));
+      if (some && at < LISTED) list.at[at] = make_int2(lo[i], be[i]);
+      count += __popc(others);
+    }
+  }
+  for (int s = 16; s > 0; s >>= 1) tiles += __shfl_xor_sync(0xffffffffu, tiles, s);
+  row_tiles = tiles;
+  if (lane == 0) {
+    list.count = count <= LISTED ? count : -1;
+    list.at[count < LISTED ? count : LISTED] = make_int2(a.offsets[a.E], 0);
+  }
+  return !__all_sync(0xffffffffu, good)       ? DEV_BAD_OFFSETS
+         : !__all_sync(0xffffffffu, good_ids) ? DEV_BAD_EXPERT_IDS
+                                              : 0;
+}
+
+// The tiles, group by group, of BM rows x BN columns; in a group by bands of BAND row tiles, in a
+// band column by column (sched.cuh's order).
+template <int BM, int BN, int BAND>
+struct GroupWalk {
+  int g = -1, be = 0;
+  int64_t base = 0, tiles = 0;  // the first tile of group g, and how many it has
+  int r0 = 0, r1 = 0;
+
+  // t must not decrease between calls.  Returns false past the last tile.
+  __device__ bool locate(const Product16Args& a, const GroupList& list, int64_t t, TileCoord& c) {
+    const int nt = (a.N + BN - 1) / BN;  // the last column tile may be partial
+    const bool listed = list.count >= 0;
+    while (t >= base + tiles) {
+      base += tiles;
+      ++g;
+      if (g >= (listed ? list.count : a.E)) return false;
+      if (listed) {
+        const int2 at = list.at[g];
+        r0 = at.x;
+        be = at.y;
+        r1 = list.at[g + 1].x;
+      } else {
+        r0 = a.offsets[g];
+        r1 = a.offsets[g + 1];
+        be = a.expert_ids ? a.expert_ids[g] : g;
+      }
+      tiles = ((int64_t)r1 - r0 + BM - 1) / BM * nt;
+    }
+    c.e = g;
+    c.be = be;
+    c.m_end = r1;
+    const uint32_t rows = (uint32_t)(((int64_t)r1 - r0 + BM - 1) / BM);
+    if (tiles <= UINT32_MAX) {  // divisions in 64 bits take half a microsecond
+      const uint32_t local = (uint32_t)(t - base);
+      const uint32_t band = local / (BAND * (uint32_t)nt), in_band = local - band * (BAND * (uint32_t)nt);
+      const uint32_t band_rows = rows - band * BAND < BAND ? rows - band * BAND : BAND;
+      const uint32_t col = in_band / band_rows;
+      c.m0 = r0 + (int64_t)(band * BAND + (in_band - col * band_rows)) * BM;
+      c.n0 = (int)(col * BN);
+    } else {
+      const int64_t local = t - base;
+      const int64_t band = local / ((int64_t)BAND * nt), in_band = local - band * BAND * nt;
+      const int64_t band_rows = rows - band * BAND < BAND ? rows - band * BAND : BAND;
+      c.m0 = r0 + (band * BAND + in_band % band_rows) * BM;
+      c.n0 = (int)(in_band / band_rows) * BN;
+    }
+    if constexpr (BSFP8_DEBUG) {
+      const bool inside = c.m0 >= r0 && c.m0 < r1 && r1 <= a.M_total && c.n0 >= 0 && c.n0 < a.N &&
+                          c.be >= 0 && c.be < a.num_experts;
+      if (!inside) {
+        atomicCAS(a.err, 0, (int)DEV_BOUNDS);
+        return false;
+      }
+    }
+    return true;
+  }
+};
+
 // ---------------------------------------------------------------------------------------
 // Few rows: 32 rows x 128 columns per CTA, or per cluster of SPLIT CTAs that share its K
 // ---------------------------------------------------------------------------------------
@@ -75,6 +183,7 @@ struct FewCtl {
   int abort;
   long long total_tiles;
   TileCoord tile;  // that a cluster shares
+  GroupList list;
 };
 constexpr uint32_t kFewSmem = FEW_CTL + sizeof(FewCtl) + 1024;  // + alignment slack
 
@@ -134,8 +243,7 @@ product16_few_kernel(const __grid_constant__ CUtensorMap tmA,
   wait_for_previous();
   if (warp == 2) {
     int64_t row_tiles;
-    const int status = check_groups<FEW_ROWS>(args.offsets, args.expert_ids, args.E,
-                                              args.num_experts, args.M_total, row_tiles);
+    const int status = list_groups<FEW_ROWS>(args, ctl->list, row_tiles);
     if (lane == 0) {
       ctl->total_tiles = status ? 0 : row_tiles * ((args.N + FEW_COLS - 1) / FEW_COLS);
       if (status && blockIdx.x == 0) atomicCAS(args.err, 0, status);
@@ -147,7 +255,7 @@ product16_few_kernel(const __grid_constant__ CUtensorMap tmA,
   const uint32_t tmem_base = ctl->tmem_base;
   const int64_t total_tiles = ctl->total_tiles;
 
-  GroupedScheduler<FEW_ROWS, FEW_COLS, 1, false> sched;
+  GroupWalk<FEW_ROWS, FEW_COLS, 1> sched;
   TileCoord tc;
   if (warp == 0) {
     if (lane == 0) {
@@ -157,7 +265,7 @@ product16_few_kernel(const __grid_constant__ CUtensorMap tmA,
       int64_t issued = 0;
       bool ok = true;
       for (Turns t(tile0, tile_stride); ok && t.at < total_tiles; t.next()) {
-        if (!sched.locate(args, t.at, tc)) break;
+        if (!sched.locate(args, ctl->list, t.at, tc)) break;
         for (int kb = kb0; kb < kb1; ++kb) {
           if (!mbar_wait_sleep(empty_bar(stage), phase ^ 1, abort)) {
             give_up(args.err, abort);
@@ -199,7 +307,7 @@ product16_few_kernel(const __grid_constant__ CUtensorMap tmA,
       uint32_t stage = 0, phase = 0, acc = 0, acc_phase = 0;
       bool ok = true;
       for (Turns t(tile0, tile_stride); ok && t.at < total_tiles; t.next()) {
-        if (!sched.locate(args, t.at, tc)) break;
+        if (!sched.locate(args, ctl->list, t.at, tc)) break;
         ok = mbar_wait_sleep(tempty_bar(acc), acc_phase ^ 1, abort);
         const uint32_t d = tmem_base + acc * FEW_COLS;
         for (int kb = kb0; ok && kb < kb1; ++kb) {
@@ -233,7 +341,7 @@ product16_few_kernel(const __grid_constant__ CUtensorMap tmA,
     const uint64_t pol_c = l2_policy_evict_first();
     uint32_t acc = 0, acc_phase = 0;
     for (Turns t(tile0, tile_stride); t.at < total_tiles; t.next()) {
-      if (!sched.locate(args, t.at, tc)) break;
+      if (!sched.locate(args, ctl->list, t.at, tc)) break;
       const int64_t row = tc.m0 + lane;
       if (F::SPLIT > 1 && lane == 0) ctl->tile = tc;
       if (!__all_sync(0xffffffffu, mbar_wait_sleep(tfull_bar(acc), acc_phase, abort))) {
@@ -325,6 +433,13 @@ product16_few_kernel(const __grid_constant__ CUtensorMap tmA,
   }
 }
 
+// More tiles than this there are not (the offsets live on the device): full ones and one of each
+// group's last rows.
+inline int64_t most_tiles(const Product16Args& a, int rows, int cols) {
+  const int64_t most_last = a.M_total < a.E ? a.M_total : a.E;
+  return (a.M_total / rows + most_last) * (((int64_t)a.N + cols - 1) / cols);
+}
+
 template <class F>
 cudaError_t launch_few(const Product16Args& args, int64_t max_tiles, int num_sms,
                        cudaStream_t stream) {
@@ -346,11 +461,13 @@ cudaError_t launch_few(const Product16Args& args, int64_t max_tiles, int num_sms
 // CTA pairs: 256 columns of C (the MMA's M: weight rows, 128 per CTA) x up to 256 or 512 rows (its
 // N: one instruction, or two on the same weights)
 // ---------------------------------------------------------------------------------------
-// ROWS: that a tile may have.
-template <bool BT_, int ROWS_>
+// ROWS: that a tile may have.  SPLIT: pairs, in one cluster, that share a tile's K, each cluster one
+// tile.
+template <bool BT_, int ROWS_, int SPLIT_ = 1>
 struct Pair {
   static constexpr bool BT = BT_;  // B [E, K, N]
   static constexpr int ROWS = ROWS_;
+  static constexpr int SPLIT = SPLIT_;
   static constexpr int HALVES = ROWS == 512 ? 2 : 1;  // of up to 256 rows
   static constexpr int BAND = 4096 / ROWS;
 };
@@ -362,6 +479,7 @@ constexpr uint32_t PAIR_EPI = RING * UNIT;
 constexpr int PAIR_THREADS = 320;
 constexpr uint32_t EPI_ROW = 256 + 64;      // staged row of C: 128 columns, and an offset of 16 banks
 constexpr uint32_t EPI_BUF = 32 * EPI_ROW;  // 32 rows, for each of two groups of warps
+constexpr uint32_t PART_ROW = 128 * 4;      // of a split tile's sums
 
 struct PairCtl {
   uint64_t full[MAX_STAGES];
@@ -372,6 +490,7 @@ struct PairCtl {
   uint32_t tmem_base;
   int abort;
   long long total_tiles;
+  GroupList list;
 };
 constexpr uint32_t kPairSmem = PAIR_EPI + 2 * EPI_BUF + sizeof(PairCtl) + 1024;  // + alignment slack
 
@@ -437,9 +556,14 @@ product16_pair_kernel(const __grid_constant__ CUtensorMap tmA,    // 128 rows of
   const uint32_t warp = threadIdx.x >> 5;
   const uint32_t lane = threadIdx.x & 31;
   const int KB = (args.K + BK - 1) / BK;
-  const uint32_t rank = cluster_ctarank();
-  const int64_t tile0 = blockIdx.x / 2;
-  const int64_t tile_stride = gridDim.x / 2;
+  // of the CTA in its pair, its pair's leader in the cluster, and the pair's share of the tile's K
+  const uint32_t cta = cluster_ctarank();
+  const uint32_t rank = cta % 2, leader = cta - rank, part = cta / 2;
+  const uint16_t both = (uint16_t)(0x3 << leader);
+  const int kb0 = (int)((int64_t)KB * part / P::SPLIT);
+  const int kb1 = (int)((int64_t)KB * (part + 1) / P::SPLIT);
+  const int64_t tile0 = blockIdx.x / (2 * P::SPLIT);
+  const int64_t tile_stride = gridDim.x / (2 * P::SPLIT);
 
   const uint32_t base = smem_u32(smem);
   auto full_bar = [&](int s) { return smem_u32(&ctl->full[s]); };
@@ -471,8 +595,7 @@ product16_pair_kernel(const __grid_constant__ CUtensorMap tmA,    // 128 rows of
   wait_for_previous();
   if (warp == 2) {
     int64_t row_tiles;
-    const int status = check_groups<P::ROWS>(args.offsets, args.expert_ids, args.E,
-                                             args.num_experts, args.M_total, row_tiles);
+    const int status = list_groups<P::ROWS>(args, ctl->list, row_tiles);
     if (lane == 0) {
       ctl->total_tiles = status ? 0 : row_tiles * ((args.N + 255) / 256);
       if (status && blockIdx.x == 0) atomicCAS(args.err, 0, status);
@@ -485,7 +608,7 @@ product16_pair_kernel(const __grid_constant__ CUtensorMap tmA,    // 128 rows of
   const uint32_t tmem_base = ctl->tmem_base;
   const int64_t total_tiles = ctl->total_tiles;  // both CTAs of a pair agree
 
-  GroupedScheduler<P::ROWS, 256, P::BAND, false> sched;
+  GroupWalk<P::ROWS, 256, P::BAND> sched;
   TileCoord tc;
   if (warp == 0) {
     if (lane == 0) {
@@ -509,7 +632,7 @@ product16_pair_kernel(const __grid_constant__ CUtensorMap tmA,    // 128 rows of
         return true;
       };
       for (Turns t(tile0, tile_stride); ok && t.at < total_tiles; t.next()) {
-        if (!sched.locate(args, t.at, tc)) break;
+        if (!sched.locate(args, ctl->list, t.at, tc)) break;
         const int32_t col = tc.n0 + 128 * (int)rank;
         // of each half: this CTA's first row, and its units of rows
         int32_t row[P::HALVES];
@@ -521,7 +644,7 @@ product16_pair_kernel(const __grid_constant__ CUtensorMap tmA,    // 128 rows of
           part[h] = half_units(height);
           units += part[h];
         }
-        for (int kb = 0; kb < KB; ++kb) {
+        for (int kb = kb0; kb < kb1; ++kb) {
           uint32_t skipped;
           const uint32_t at = ring.take(units, skipped);
           while (ok && (used + units + skipped > RING || stages + 1 == MAX_STAGES))
@@ -535,7 +658,7 @@ product16_pair_kernel(const __grid_constant__ CUtensorMap tmA,    // 128 rows of
           ++stages;
           const uint32_t w = base + at * UNIT;
           // both CTAs' bytes are counted on the leader's barrier
-          const uint32_t bar = mapa_shared(full_bar(ring.slot), 0);
+          const uint32_t bar = mapa_shared(full_bar(ring.slot), leader);
           if (rank == 0) mbar_arrive_expect_tx(full_bar(ring.slot), 2 * units * UNIT);
           if constexpr (P::BT) {
             tma_load_3d_pair_hint(w, &tmB, col, kb * BK, tc.be, bar, pol_b);
@@ -575,14 +698,14 @@ product16_pair_kernel(const __grid_constant__ CUtensorMap tmA,    // 128 rows of
       uint32_t acc = 0, acc_phase = 0;  // TMEM's half that the tile's first half takes
       bool ok = true;
       for (Turns t(tile0, tile_stride); ok && t.at < total_tiles; t.next()) {
-        if (!sched.locate(args, t.at, tc)) break;
+        if (!sched.locate(args, ctl->list, t.at, tc)) break;
         const uint32_t n0 = half_height<P>(tc, 0), n1 = P::HALVES == 2 ? half_height<P>(tc, 1) : 0;
         const uint32_t units0 = half_units(n0), units = W_UNITS + units0 + half_units(n1);
         const uint32_t d0 = tmem_base + acc * 256, d1 = tmem_base + (acc ^ 1) * 256;
         ok = mbar_wait_sleep(tempty_bar(acc), acc_phase ^ 1, abort);
         if (n1 && ok)  // (a second half that wraps around to TMEM's first is a turn later)
           ok = mbar_wait_sleep(tempty_bar(acc ^ 1), acc ? acc_phase : acc_phase ^ 1, abort);
-        for (int kb = 0; ok && kb < KB; ++kb) {
+        for (int kb = kb0; ok && kb < kb1; ++kb) {
           ok = mbar_wait_sleep(full_bar(ring.slot), ring.phase, abort);
           if (!ok) break;
           tc_fence_after();
@@ -592,15 +715,15 @@ product16_pair_kernel(const __grid_constant__ CUtensorMap tmA,    // 128 rows of
 #pragma unroll
           for (int k = 0; k < BK / 16; ++k)
             umma_f16<2>(d0, wdesc + k * kStepW, adesc + k * kStepA, idesc0 | (n0 >> 3) << 17,
-                        (kb | k) > 0);
+                        kb > kb0 || k > 0);
           if (n1) {
             const uint64_t adesc1 = adesc + ((units0 * UNIT) >> 4);
 #pragma unroll
             for (int k = 0; k < BK / 16; ++k)
               umma_f16<2>(d1, wdesc + k * kStepW, adesc1 + k * kStepA, idesc0 | (n1 >> 3) << 17,
-                          (kb | k) > 0);
+                          kb > kb0 || k > 0);
           }
-          umma_commit_pair(empty_bar(ring.slot), 0x3);
+          umma_commit_pair(empty_bar(ring.slot), both);
           ring.next();
         }
         if (!ok) {
@@ -608,12 +731,12 @@ product16_pair_kernel(const __grid_constant__ CUtensorMap tmA,    // 128 rows of
           break;
         }
         for (uint32_t h = 0; h < (n1 ? 2u : 1u); ++h) {
-          umma_commit_pair(tfull_bar(acc), 0x3);
+          umma_commit_pair(tfull_bar(acc), both);
           if (++acc == 2) { acc = 0; acc_phase ^= 1; }
         }
       }
       // every MMA has finished before TMEM is released
-      umma_commit_pair(smem_u32(&ctl->mma_done), 0x1);
+      umma_commit_pair(smem_u32(&ctl->mma_done), (uint16_t)(1 << leader));
       if (!mbar_wait_timed(smem_u32(&ctl->mma_done), 0)) give_up(args.err, abort);
     }
     __syncwarp();
@@ -625,12 +748,13 @@ product16_pair_kernel(const __grid_constant__ CUtensorMap tmA,    // 128 rows of
     const uint32_t quarter = warp & 3, group = (warp - 2) >> 2;
     uint16_t* Cmat = static_cast<uint16_t*>(args.C);
     const uint64_t pol_c = l2_policy_evict_first();
-    const uint32_t tempty_0 = mapa_shared(tempty_bar(0), 0), tempty_1 = mapa_shared(tempty_bar(1), 0);
+    const uint32_t tempty_0 = mapa_shared(tempty_bar(0), leader);
+    const uint32_t tempty_1 = mapa_shared(tempty_bar(1), leader);
     uint8_t* const staged = smem + PAIR_EPI + group * EPI_BUF;
     uint32_t acc = 0, acc_phase = 0;
     const bool odd = lane & 1;
     for (Turns t(tile0, tile_stride); t.at < total_tiles; t.next()) {
-      if (!sched.locate(args, t.at, tc)) break;
+      if (!sched.locate(args, ctl->list, t.at, tc)) break;
       const int n = tc.n0 + 128 * (int)rank + 8 * (int)(lane & 15);  // of what the lane stores
       bool ok = true;
       for (int h = 0; ok && h < P::HALVES; ++h) {
@@ -652,28 +776,34 @@ product16_pair_kernel(const __grid_constant__ CUtensorMap tmA,    // 128 rows of
           tmem_ld_32x32b_x32(taddr + c, p);  // (past the height: whatever is there, not stored)
           tmem_ld_wait();
           if (c + 64 >= height) release();
+          if constexpr (P::SPLIT > 1) {  // the part, rows of 128 columns, in the ring: it is done with
 #pragma unroll
-          for (int j = 0; j < 32; j += 2) {
-            const float lo = __uint_as_float(p[j]), hi = __uint_as_float(p[j + 1]);
-            const uint32_t own = args.bf16 ? pack_bf16x2(lo, hi) : pack_f16x2(lo, hi);
-            const uint32_t other = __shfl_xor_sync(0xffffffffu, own, 1);
-            // even lanes: row j of columns n, n + 1; odd lanes: row j + 1 of columns n - 1, n
-            const uint32_t v =
-                odd ? __byte_perm(other, own, 0x7632) : __byte_perm(own, other, 0x5410);
-            *reinterpret_cast<uint32_t*>(staged + (j + odd) * EPI_ROW +
-                                         (quarter * 32 + (lane & ~1u)) * 2) = v;
-          }
-          group_sync(group);
-          const int row0 = quarter * 8 + (int)(lane >> 4);
+            for (int j = 0; j < 32; ++j)
+              *reinterpret_cast<uint32_t*>(smem + (c + j) * PART_ROW + (quarter * 32 + lane) * 4) = p[j];
+          } else {
 #pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            const int r = row0 + 2 * i;
-            const int64_t row = tc.m0 + 256 * h + c + r;
-            const uint4 v = *reinterpret_cast<const uint4*>(staged + r * EPI_ROW + 16 * (lane & 15));
-            if (row < tc.m_end && n < args.N)
-              st_global_v4_hint(Cmat + row * (int64_t)args.N + n, v.x, v.y, v.z, v.w, pol_c);
+            for (int j = 0; j < 32; j += 2) {
+              const float lo = __uint_as_float(p[j]), hi = __uint_as_float(p[j + 1]);
+              const uint32_t own = args.bf16 ? pack_bf16x2(lo, hi) : pack_f16x2(lo, hi);
+              const uint32_t other = __shfl_xor_sync(0xffffffffu, own, 1);
+              // even lanes: row j of columns n, n + 1; odd lanes: row j + 1 of columns n - 1, n
+              const uint32_t v =
+                  odd ? __byte_perm(other, own, 0x7632) : __byte_perm(own, other, 0x5410);
+              *reinterpret_cast<uint32_t*>(staged + (j + odd) * EPI_ROW +
+                                           (quarter * 32 + (lane & ~1u)) * 2) = v;
+            }
+            group_sync(group);
+            const int row0 = quarter * 8 + (int)(lane >> 4);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              const int r = row0 + 2 * i;
+              const int64_t row = tc.m0 + 256 * h + c + r;
+              const uint4 v = *reinterpret_cast<const uint4*>(staged + r * EPI_ROW + 16 * (lane & 15));
+              if (row < tc.m_end && n < args.N)
+                st_global_v4_hint(Cmat + row * (int64_t)args.N + n, v.x, v.y, v.z, v.w, pol_c);
+            }
+            group_sync(group);  // read before it is written again
           }
-          group_sync(group);  // read before it is written again
         }
         if (++acc == 2) { acc = 0; acc_phase ^= 1; }
       }
@@ -684,6 +814,47 @@ product16_pair_kernel(const __grid_constant__ CUtensorMap tmA,    // 128 rows of
     }
   }
 
+  if constexpr (P::SPLIT > 1) {
+    // Each pair adds up some of the tile's rows, in the pairs' order.  (A pair that gave up has said
+    // so, and the sums mean nothing.)  The cluster's barrier below is the one before any CTA goes.
+    static_assert(P::ROWS * PART_ROW <= RING * UNIT && P::HALVES == 1, "part");
+    __syncwarp();
+    cluster_sync();
+    if (warp >= 2 && tile0 < total_tiles) {
+      GroupWalk<P::ROWS, 256, P::BAND> again;
+      again.locate(args, ctl->list, tile0, tc);
+      const int height = half_height<P>(tc, 0);
+      const int n = tc.n0 + 128 * (int)rank + 8 * (int)(lane & 15);
+      const int first = (int)part + P::SPLIT * (int)((threadIdx.x - 64) / 16);
+      for (int r = first; r < height; r += P::SPLIT * (PAIR_THREADS - 64) / 16) {
+        const int64_t row = tc.m0 + r;
+        if (row >= tc.m_end || n >= args.N) continue;  // N is a multiple of 8
+        float4 v[2][P::SPLIT];
+#pragma unroll
+        for (int s = 0; s < P::SPLIT; ++s)
+#pragma unroll
+          for (int h = 0; h < 2; ++h)
+            v[h][s] = load_cluster_f4(
+                mapa_shared(base + r * PART_ROW + 32 * (lane & 15) + 16 * h, 2 * s + rank));
+        uint32_t w[4];
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+#pragma unroll
+          for (int s = 1; s < P::SPLIT; ++s) {
+            v[h][0].x += v[h][s].x;
+            v[h][0].y += v[h][s].y;
+            v[h][0].z += v[h][s].z;
+            v[h][0].w += v[h][s].w;
+          }
+          const float4 x = v[h][0];
+          w[2 * h] = args.bf16 ? pack_bf16x2(x.x, x.y) : pack_f16x2(x.x, x.y);
+          w[2 * h + 1] = args.bf16 ? pack_bf16x2(x.z, x.w) : pack_f16x2(x.z, x.w);
+        }
+        *reinterpret_cast<uint4*>(static_cast<uint16_t*>(args.C) + row * (int64_t)args.N + n) =
+            make_uint4(w[0], w[1], w[2], w[3]);
+      }
+    }
+  }
   tc_fence_before();
   __syncthreads();
   // the pair's MMAs and remote arrivals are finished before either CTA frees TMEM or exits
@@ -708,25 +879,33 @@ cudaError_t launch_pair(const Product16Args& args, int num_sms, cudaStream_t str
     return cudaErrorInvalidValue;
   const cudaError_t e = allow_smem<product16_pair_kernel<P>>(kPairSmem);
   if (e != cudaSuccess) return e;
-  // more tiles than this there are not (the offsets live on the device)
-  const int64_t max_tiles = ((args.M_total + P::ROWS - 1) / P::ROWS + args.E) * ((args.N + 255) / 256);
-  const int64_t units = num_sms / 2;
-  return launch_persistent(product16_pair_kernel<P>, max_tiles < units ? max_tiles : units, 2,
+  const int64_t tiles = most_tiles(args, P::ROWS, 256), units = num_sms / (2 * P::SPLIT);
+  return launch_persistent(product16_pair_kernel<P>, tiles < units ? tiles : units, 2 * P::SPLIT,
                            PAIR_THREADS, kPairSmem, stream, tmA, tmA64, tmA32, tmB, args);
+}
+
+template <class F>
+int64_t few_at_once() {
+  return clusters_at_once<product16_few_kernel<F>>(F::SPLIT, FEW_THREADS, kFewSmem);
+}
+template <class P>
+int64_t pairs_at_once() {
+  return clusters_at_once<product16_pair_kernel<P>>(2 * P::SPLIT, PAIR_THREADS, kPairSmem);
 }
 
 template <bool BT>
 cudaError_t choose(const Product16Args& a, int num_sms, cudaStream_t stream) {
-  // More tiles of few rows than this there are not (the offsets live on the device); a tile's K is
-  // shared where that leaves each of the tile's CTAs a part and an SM.
-  const int64_t row_tiles = a.M_total / FEW_ROWS + (a.M_total < a.E ? a.M_total : a.E);
-  const int64_t few_tiles = row_tiles * ((a.N + FEW_COLS - 1) / FEW_COLS);
+  // A tile's K is shared where that leaves each of the tile's CTAs a part and an SM (a second round of
+  // clusters costs more than sharing gains: 1000 rows, 512 x 2048, shared by four pairs 20.7 us, by two
+  // 12.8).
+  const int64_t few_tiles = most_tiles(a, FEW_ROWS, FEW_COLS);
   const int64_t blocks = (a.K + BK - 1) / BK;
-  if (a.M_total <= (int64_t)32 * a.E) {
-    if (few_tiles * 8 <= num_sms && blocks >= 16) return launch_few<Few<BT, 8>>(a, few_tiles, num_sms, stream);
-    if (few_tiles * 4 <= num_sms && blocks >= 8) return launch_few<Few<BT, 4>>(a, few_tiles, num_sms, stream);
-    if (few_tiles * 2 <= num_sms && blocks >= 4) return launch_few<Few<BT, 2>>(a, few_tiles, num_sms, stream);
-  }
+  if (blocks >= 16 && few_tiles <= few_at_once<Few<BT, 8>>())
+    return launch_few<Few<BT, 8>>(a, few_tiles, num_sms, stream);
+  if (blocks >= 8 && few_tiles <= few_at_once<Few<BT, 4>>())
+    return launch_few<Few<BT, 4>>(a, few_tiles, num_sms, stream);
+  if (blocks >= 4 && few_tiles <= few_at_once<Few<BT, 2>>())
+    return launch_few<Few<BT, 2>>(a, few_tiles, num_sms, stream);
   // Up to 8 rows per group on average, most groups are one tile of 32 rows: less to load and to
   // set up than in tiles of pairs (64 groups of 1 row, 2048 x 2048: 81 us against 88; 16 of 8, 2048
   // x 4096: 45 and 48).  With more of them a few groups can hold many, and each reads its weights
@@ -734,16 +913,38 @@ cudaError_t choose(const Product16Args& a, int num_sms, cudaStream_t stream) {
   // 4096 rows in one of them 222 and 51; 16 rows in each 327 and 322).
   if (a.M_total <= FEW_ROWS || a.M_total <= (int64_t)8 * a.E)
     return launch_few<Few<BT, 1>>(a, few_tiles, num_sms, stream);
-  // Of tiles of 512, 256, 128 or 64 rows the highest that give every pair of SMs some to do; 512
-  // where groups are mostly over 256 or near it (64 groups of 260 rows, 7168 x 2048: 413 us, 509
-  // with 256; groups of 128: 311 and 297) and there are enough of them to even out.
-  auto tiles = [&](int rows) { return (a.M_total / rows + a.E / 2) * ((a.N + 255) / 256); };
   const int64_t units = num_sms / 2;
+  // about how many tiles there are: the last of a group is half full
+  auto tiles = [&](int rows) {
+    const int64_t row_tiles =
+        a.E == 1 ? (a.M_total + rows - 1) / rows : a.M_total / rows + (a.E + 1) / 2;
+    return (row_tiles > a.E ? row_tiles : a.E) * ((a.N + 255) / 256);
+  };
+  // Tiles of 512 rows where groups are mostly over 256 or near it (64 groups of 260 rows, 7168 x
+  // 2048: 413 us, 509 with 256; groups of 128: 311 and 297) and there are enough of them to even out.
   if (a.M_total >= (int64_t)192 * a.E && tiles(512) >= 6 * units)
     return launch_pair<Pair<BT, 512>>(a, num_sms, stream);
-  if (tiles(256) >= units) return launch_pair<Pair<BT, 256>>(a, num_sms, stream);
-  if (tiles(128) >= units) return launch_pair<Pair<BT, 128>>(a, num_sms, stream);
-  return launch_pair<Pair<BT, 64>>(a, num_sms, stream);
+  // Else what takes least of 256, 128 or 64 rows, or of 128 whose K two or four pairs share: rounds of
+  // tiles, each of so many units of 4 KB per block of 64 K, and about 48 units to start and end it.
+  // Against the best of the others (us): 545 rows, 3000 x 1256, with 128 rows 13.3 and 14.7; 1024
+  // rows, 4096 x 4096, with 256 26.0 and 39.6; 8 groups of 158, 952 x 3120, with 128 19.8 and 20.2;
+  // 128 rows, 4096 x 4096, shared by two 16.8 and 21.4.
+  auto cost = [&](int rows, int split) {
+    const int64_t n = tiles(rows), rounds = (n + units / split - 1) / (units / split);
+    const double height = (double)a.M_total * ((a.N + 255) / 256) / n;
+    return rounds * ((blocks + split - 1) / split * (4 + height / 64) + 48 + (split == 1 ? 0 : split == 2 ? 48 : 80));
+  };
+  const double c64 = cost(64, 1), c128 = cost(128, 1), c256 = cost(256, 1);
+  const double least = c64 < c128 ? (c64 < c256 ? c64 : c256) : (c128 < c256 ? c128 : c256);
+  const int64_t most = most_tiles(a, 128, 256);
+  if (blocks >= 16 && cost(128, 4) < least && cost(128, 4) < cost(128, 2) &&
+      most <= pairs_at_once<Pair<BT, 128, 4>>())
+    return launch_pair<Pair<BT, 128, 4>>(a, num_sms, stream);
+  if (blocks >= 8 && cost(128, 2) < least && most <= pairs_at_once<Pair<BT, 128, 2>>())
+    return launch_pair<Pair<BT, 128, 2>>(a, num_sms, stream);
+  if (c256 == least) return launch_pair<Pair<BT, 256>>(a, num_sms, stream);
+  return c128 == least ? launch_pair<Pair<BT, 128>>(a, num_sms, stream)
+                       : launch_pair<Pair<BT, 64>>(a, num_sms, stream);
 }
 
 }  // namespace g16

@@ -32,9 +32,7 @@ struct TileCoord {
   int64_t m_end;   // one past the expert's last row (rows >= m_end are not this tile's)
 };
 
-// NC: the offsets and ids are read through the read-only cache, which a kernel that starts before
-// the one before it has ended may not do.
-template <int BM, int BN, int BAND = 1, bool NC = true>
+template <int BM, int BN, int BAND = 1>
 struct GroupedScheduler {
   // Only the cursor lives here; offsets, expert ids, group count and N are read from the
   // kernel's parameter block (constant memory) at each call, so they cost no registers.
@@ -54,32 +52,21 @@ struct GroupedScheduler {
       base += e_tiles;
       ++e;
       if (e >= a.E) return false;
-      r0 = NC ? ldg_s32(a.offsets + e) : a.offsets[e];
-      r1 = NC ? ldg_s32(a.offsets + e + 1) : a.offsets[e + 1];
+      r0 = ldg_s32(a.offsets + e);
+      r1 = ldg_s32(a.offsets + e + 1);
       const int64_t rows = r1 - r0;
       rt = (rows >= a.min_group_rows && rows < a.max_group_rows) ? (rows + BM - 1) / BM : 0;
       e_tiles = rt * (int64_t)n_tiles;
-      be = !a.expert_ids ? e : NC ? ldg_s32(a.expert_ids + e) : a.expert_ids[e];
+      be = a.expert_ids ? ldg_s32(a.expert_ids + e) : e;
     }
+    const int64_t local = t - base;
+    const int64_t band = local / ((int64_t)BAND * n_tiles);
+    const int64_t in_band = local - band * BAND * n_tiles;
+    const int64_t band_rows = rt - band * BAND < BAND ? rt - band * BAND : BAND;
     c.e = e;
     c.be = be;
-    if (!NC && e_tiles <= UINT32_MAX) {
-      // (the kernels without the read-only cache also serve calls of a few microseconds, of which
-      // the divisions in 64 bits take half of one)
-      const uint32_t nt = (uint32_t)n_tiles, local = (uint32_t)(t - base), rows = (uint32_t)rt;
-      const uint32_t band = local / (BAND * nt), in_band = local - band * (BAND * nt);
-      const uint32_t band_rows = rows - band * BAND < BAND ? rows - band * BAND : BAND;
-      const uint32_t col = in_band / band_rows;
-      c.m0 = r0 + (int64_t)(band * BAND + (in_band - col * band_rows)) * BM;
-      c.n0 = (int)(col * BN);
-    } else {
-      const int64_t local = t - base;
-      const int64_t band = local / ((int64_t)BAND * n_tiles);
-      const int64_t in_band = local - band * BAND * n_tiles;
-      const int64_t band_rows = rt - band * BAND < BAND ? rt - band * BAND : BAND;
-      c.m0 = r0 + (band * BAND + in_band % band_rows) * BM;
-      c.n0 = (int)(in_band / band_rows) * BN;
-    }
+    c.m0 = r0 + (band * BAND + in_band % band_rows) * BM;
+    c.n0 = (int)(in_band / band_rows) * BN;
     c.m_end = r1;
     if constexpr (BSFP8_DEBUG) {
       const bool inside = c.m0 >= r0 && c.m0 < r1 && r1 <= a.M_total && c.n0 >= 0 &&

@@ -770,6 +770,11 @@ cudaError_t launch(const WgradArgs& args, int num_sms, cudaStream_t stream) {
 }
 
 template <class C>
+int64_t at_once() {
+  return clusters_at_once<wgrad_kernel<C, GRAD_FP32>>(C::CG * C::SPLIT, THREADS, smem_bytes<C>());
+}
+
+template <class C>
 cudaError_t by_type(const WgradArgs& a, int num_sms, cudaStream_t stream) {
   switch (a.out_type) {
     case GRAD_BF16: return launch<C, GRAD_BF16>(a, num_sms, stream);
@@ -783,7 +788,11 @@ cudaError_t by_type(const WgradArgs& a, int num_sms, cudaStream_t stream) {
 cudaError_t launch_wgrad(const WgradArgs& a, int num_sms, cudaStream_t stream) {
   // Few tiles and many rows: four pairs share a tile's rows (8192 rows, 512 x 512: 54 -> 21 us).
   const int64_t tiles = (int64_t)a.E * ((a.N + 255) / 256) * ((a.K + 255) / 256);
-  const bool split = tiles * 9 <= num_sms && a.M_total >= (int64_t)1024 * a.E;
+  using Split8 = wg::Cfg<true, 128, 4, false, 4>;
+  using Split16 = wg::Cfg<false, 128, 3, false, 4>;
+  const bool split =
+      a.M_total >= (int64_t)1024 * a.E &&
+      tiles <= (a.fp8 ? wg::at_once<Split8>() : wg::at_once<Split16>());
   // The gradients go out through shared memory and TMA, so that the epilogue takes up the next tile's
   // sums at once, or straight from the threads, in whole lines.  Which is faster was measured (32
   // experts of 2048 x 7168, us straight and by TMA):
@@ -798,12 +807,12 @@ cudaError_t launch_wgrad(const WgradArgs& a, int num_sms, cudaStream_t stream) {
   const int64_t rounds = (tiles * 2 + num_sms - 1) / num_sms;
   const bool wide = a.out_type == GRAD_FP32;
   if (a.fp8) {
-    if (split) return wg::by_type<wg::Cfg<true, 128, 4, false, 4>>(a, num_sms, stream);
+    if (split) return wg::by_type<Split8>(a, num_sms, stream);
     const bool staged = !wide || (!a.add && (rounds <= 4 || a.M_total >= (int64_t)384 * a.E));
     return staged ? wg::by_type<wg::Cfg<true, 128, 4, true>>(a, num_sms, stream)
                   : wg::launch<wg::Cfg<true, 128, 4, false>, GRAD_FP32>(a, num_sms, stream);
   }
-  if (split) return wg::by_type<wg::Cfg<false, 128, 3, false, 4>>(a, num_sms, stream);
+  if (split) return wg::by_type<Split16>(a, num_sms, stream);
   const bool long_groups = a.M_total >= (int64_t)384 * a.E;
   const bool staged = a.add ? !wide : rounds <= 4 || (wide && long_groups);
   if (long_groups)

@@ -635,3 +635,20 @@ def test_columns_of_no_tokens():
     bsfp8.bsfp8_quantize_columns(None, off, q, s, rows, K, 2, slot_of_row=slots, top_k=2, x_rows=0, x_type="bf16")
     _no_error()
     assert torch.all(q == 0) and torch.all(s[:2] == 1)
+
+
+@pytest.mark.parametrize("transposed", [False, True])
+@pytest.mark.parametrize("sizes,N,K", [
+    ([49], 816, 2992), ([128], 2048, 1024), ([100], 4096, 520), ([129], 1032, 512), ([40, 0, 77], 1000, 1912),  # K shared by pairs
+    ([300], 2048, 1000), ([65, 64, 63, 1], 136, 1032),
+], ids=str)
+def test_product_tiles_that_share_k(sizes, N, K, transposed):
+    _product(sizes, N, K, FP16, transposed, seed=4)
+
+
+@pytest.mark.parametrize("groups", [191, 192, 193, 400])
+@pytest.mark.parametrize("each", [1, 20])
+def test_product_as_many_groups_as_are_listed(groups, each):
+    # groups with rows between empty ones, under expert ids that go round
+    sizes = [each if g % 2 else 0 for g in range(2 * groups)]
+    _product(sizes, 72, 136, ids=[g % 5 for g in range(2 * groups)], experts=5)
