@@ -49,7 +49,7 @@ struct Turns {
 // The groups that have rows, in shared memory: the first row and the expert of each, and behind them
 // the last one's end.  A walk over the offsets themselves waits for L2 at every group, empty ones too
 // (9 rows in 128 groups, 168 x 864: 17.9 us, listed 6.2).  Above LISTED of them the walk does that.
-constexpr int LISTED = 192;
+constexpr int LISTED = 128;
 struct GroupList {
   int count;  // or -1: too many
   int2 at[LISTED + 1];
@@ -476,7 +476,10 @@ constexpr uint32_t RING = 51;                // units
 constexpr uint32_t W_UNITS = 4;              // a CTA's 128 weight rows
 constexpr uint32_t MAX_STAGES = 10;          // barriers: one more than the smallest stages that fit
 constexpr uint32_t PAIR_EPI = RING * UNIT;
-constexpr int PAIR_THREADS = 320;
+constexpr int PAIR_THREADS = 352;  // warp 0 producer, 1 MMA thread, 2..9 epilogue, 10 plans tiles
+constexpr int PLAN_WARP = 10;
+constexpr uint32_t PLANNED = 4;      // tiles ahead
+constexpr int64_t MOST_PAIRS = 96;   // that a plan is made for, three to a lane
 constexpr uint32_t EPI_ROW = 256 + 64;      // staged row of C: 128 columns, and an offset of 16 banks
 constexpr uint32_t EPI_BUF = 32 * EPI_ROW;  // 32 rows, for each of two groups of warps
 constexpr uint32_t PART_ROW = 128 * 4;      // of a split tile's sums
@@ -487,6 +490,9 @@ struct PairCtl {
   uint64_t tfull[2];  // of TMEM's halves
   uint64_t tempty[2];
   uint64_t mma_done;
+  uint64_t planned[PLANNED];  // a tile is in the slot
+  uint64_t taken[PLANNED];    // all have read it
+  int4 plan[PLANNED];         // expert, first row, first column, end of the group; no expert: no more
   uint32_t tmem_base;
   int abort;
   long long total_tiles;
@@ -584,6 +590,10 @@ product16_pair_kernel(const __grid_constant__ CUtensorMap tmA,    // 128 rows of
       mbar_init(tempty_bar(s), 16);  // every epilogue warp of the pair
     }
     mbar_init(smem_u32(&ctl->mma_done), 1);
+    for (uint32_t s = 0; s < PLANNED; ++s) {
+      mbar_init(smem_u32(&ctl->planned[s]), 1);
+      mbar_init(smem_u32(&ctl->taken[s]), 9 + (rank == 0));  // producer, epilogue, and MMA thread
+    }
     ctl->abort = 0;
     fence_mbarrier_init();
   }
@@ -608,8 +618,37 @@ product16_pair_kernel(const __grid_constant__ CUtensorMap tmA,    // 128 rows of
   const uint32_t tmem_base = ctl->tmem_base;
   const int64_t total_tiles = ctl->total_tiles;  // both CTAs of a pair agree
 
-  GroupWalk<P::ROWS, 256, P::BAND> sched;
+  // The first tile is the pair's number in the order, the others are planned: false if there is none.
   TileCoord tc;
+  uint32_t slot = 0, slot_phase = 0;
+  auto first_tile = [&]() {
+    GroupWalk<P::ROWS, 256, P::BAND> walk;
+    return tile0 < total_tiles && walk.locate(args, ctl->list, tile0, tc);
+  };
+  auto wait_planned = [&]() {
+    return mbar_wait_sleep(smem_u32(&ctl->planned[slot]), slot_phase, abort);
+  };
+  auto read_planned = [&]() {  // by a thread, or a warp
+    const int4 p = ctl->plan[slot];
+    tc.be = p.x;
+    tc.m0 = p.y;
+    tc.n0 = p.z;
+    tc.m_end = p.w;
+    return p.x >= 0;
+  };
+  auto take_planned = [&]() {  // by one thread, after it (and its warp) has read
+    mbar_arrive(smem_u32(&ctl->taken[slot]));
+    if (++slot == PLANNED) { slot = 0; slot_phase ^= 1; }
+  };
+  // of one thread
+  auto next_tile = [&](bool& ok) {
+    if (P::SPLIT > 1 || total_tiles <= tile_stride) return false;
+    ok = wait_planned();
+    if (!ok) return false;
+    const bool some = read_planned();
+    take_planned();
+    return some;
+  };
   if (warp == 0) {
     if (lane == 0) {
       // ------------------------------- TMA producer -------------------------------
@@ -631,8 +670,7 @@ product16_pair_kernel(const __grid_constant__ CUtensorMap tmA,    // 128 rows of
         --stages;
         return true;
       };
-      for (Turns t(tile0, tile_stride); ok && t.at < total_tiles; t.next()) {
-        if (!sched.locate(args, ctl->list, t.at, tc)) break;
+      for (bool have = first_tile(); ok && have; have = ok && next_tile(ok)) {
         const int32_t col = tc.n0 + 128 * (int)rank;
         // of each half: this CTA's first row, and its units of rows
         int32_t row[P::HALVES];
@@ -678,6 +716,7 @@ product16_pair_kernel(const __grid_constant__ CUtensorMap tmA,    // 128 rows of
           ring.next();
         }
       }
+      if (!ok) give_up(args.err, abort);
       // This CTA's last loads land, and the MMAs that read them end, before it can exit (after
       // an abort the first wait runs out, which is time enough for the loads).
       while (stages > 0 && free_oldest(true)) {
@@ -697,8 +736,7 @@ product16_pair_kernel(const __grid_constant__ CUtensorMap tmA,    // 128 rows of
       RingPlace ring;
       uint32_t acc = 0, acc_phase = 0;  // TMEM's half that the tile's first half takes
       bool ok = true;
-      for (Turns t(tile0, tile_stride); ok && t.at < total_tiles; t.next()) {
-        if (!sched.locate(args, ctl->list, t.at, tc)) break;
+      for (bool have = first_tile(); ok && have; have = ok && next_tile(ok)) {
         const uint32_t n0 = half_height<P>(tc, 0), n1 = P::HALVES == 2 ? half_height<P>(tc, 1) : 0;
         const uint32_t units0 = half_units(n0), units = W_UNITS + units0 + half_units(n1);
         const uint32_t d0 = tmem_base + acc * 256, d1 = tmem_base + (acc ^ 1) * 256;
@@ -735,9 +773,89 @@ product16_pair_kernel(const __grid_constant__ CUtensorMap tmA,    // 128 rows of
           if (++acc == 2) { acc = 0; acc_phase ^= 1; }
         }
       }
+      if (!ok) give_up(args.err, abort);
       // every MMA has finished before TMEM is released
       umma_commit_pair(smem_u32(&ctl->mma_done), (uint16_t)(1 << leader));
       if (!mbar_wait_timed(smem_u32(&ctl->mma_done), 0)) give_up(args.err, abort);
+    }
+    __syncwarp();
+  } else if (warp == PLAN_WARP) {
+    // ----------------------------------- plan ------------------------------------
+    // Every pair follows the same plan, each for itself: the tiles in their order, each to the pair
+    // that is done first by what tiles cost.  (One of every `stride` to each, as many pairs got more
+    // of the full ones: 7 groups of 585 rows, 4096 x 7168, 190 us, so 174.)  In 82 clocks per unit of 4 KB of operands, or 2 per row of MMAs.
+    if (P::SPLIT == 1 && total_tiles > tile_stride) {
+      const uint32_t mine = (uint32_t)tile0, pairs = (uint32_t)tile_stride;
+      const uint32_t kb = (uint32_t)KB;
+      auto cost_of = [&](int height) {
+        const int n0 = height < 256 ? height : 256, n1 = height - n0;
+        const uint32_t loads = 82 * (W_UNITS + half_units(n0) + half_units(n1)), mma = 2 * height;
+        const uint32_t c = ((loads > mma ? loads : mma) * kb + 4000) >> 8;
+        return c << 7;
+      };
+      const uint32_t full = cost_of(P::ROWS);
+      // the pairs' loads above their numbers, those of pairs lane, lane + 32 and lane + 64
+      uint32_t load[3];
+#pragma unroll
+      for (int i = 0; i < 3; ++i) load[i] = lane + 32 * i < pairs ? lane + 32 * i : UINT32_MAX;
+      const int nt = (args.N + 255) / 256;
+      const bool listed = ctl->list.count >= 0;
+      const int groups = listed ? ctl->list.count : args.E;
+      int64_t t = 0;
+      bool ok = true;
+      auto push = [&](int be, int m0, int n0, int m_end) {
+        ok = __all_sync(0xffffffffu, mbar_wait_sleep(smem_u32(&ctl->taken[slot]), slot_phase ^ 1, abort));
+        if (!ok) return;
+        if (lane == 0) {
+          ctl->plan[slot] = make_int4(be, m0, n0, m_end);
+          mbar_arrive(smem_u32(&ctl->planned[slot]));
+        }
+        if (++slot == PLANNED) { slot = 0; slot_phase ^= 1; }
+      };
+      if (kb < 8) {  // (tiles come faster than such a plan: one of every `stride`)
+        GroupWalk<P::ROWS, 256, P::BAND> walk;
+        Turns turn(tile0, tile_stride);
+        turn.next();
+        for (; ok && turn.at < total_tiles && walk.locate(args, ctl->list, turn.at, tc); turn.next())
+          push(tc.be, (int)tc.m0, tc.n0, (int)tc.m_end);
+      }
+      for (int g = 0; kb >= 8 && ok && g < groups; ++g) {
+        int r0, r1, be;
+        if (listed) {
+          r0 = ctl->list.at[g].x;
+          be = ctl->list.at[g].y;
+          r1 = ctl->list.at[g + 1].x;
+        } else {
+          r0 = args.offsets[g];
+          r1 = args.offsets[g + 1];
+          be = args.expert_ids ? args.expert_ids[g] : g;
+        }
+        const int tall = (int)(((int64_t)r1 - r0) / P::ROWS), rest = r1 - r0 - tall * P::ROWS;
+        const int row_tiles = tall + (rest > 0);
+        const uint32_t last = rest > 0 ? cost_of((rest + 15) / 16 * 16) : full;
+        for (int band = 0; ok && band < row_tiles; band += P::BAND) {
+          const int end = row_tiles - band < P::BAND ? row_tiles : band + P::BAND;
+          for (int col = 0; ok && col < nt; ++col) {
+            for (int row = band; ok && row < end; ++row, ++t) {
+              const uint32_t a = load[0] < load[1] ? load[0] : load[1];
+              const uint32_t best = __reduce_min_sync(0xffffffffu, a < load[2] ? a : load[2]);
+              const uint32_t pair = best & 127, cost = row == row_tiles - 1 ? last : full;
+#pragma unroll
+              for (int i = 0; i < 3; ++i)
+                if (load[i] == best) load[i] += cost;
+              if (best >= (1u << 30)) {  // the least of all: taken off everywhere
+#pragma unroll
+                for (int i = 0; i < 3; ++i)
+                  if (load[i] != UINT32_MAX) load[i] -= best & ~127u;
+              }
+              // (the first of each pair it knows)
+              if (pair == mine && t >= (int64_t)pairs) push(be, r0 + row * P::ROWS, col * 256, r1);
+            }
+          }
+        }
+      }
+      if (ok) push(-1, 0, 0, 0);
+      if (!ok && lane == 0) give_up(args.err, abort);
     }
     __syncwarp();
   } else {
@@ -753,8 +871,20 @@ product16_pair_kernel(const __grid_constant__ CUtensorMap tmA,    // 128 rows of
     uint8_t* const staged = smem + PAIR_EPI + group * EPI_BUF;
     uint32_t acc = 0, acc_phase = 0;
     const bool odd = lane & 1;
-    for (Turns t(tile0, tile_stride); t.at < total_tiles; t.next()) {
-      if (!sched.locate(args, ctl->list, t.at, tc)) break;
+    // (the warps of a group have barriers between them: all go on to a tile, or none)
+    auto next_of_group = [&]() {
+      if (P::SPLIT > 1 || total_tiles <= tile_stride) return false;
+      if (!all_of_group(group, wait_planned())) {
+        give_up(args.err, abort);
+        return false;
+      }
+      const bool some = read_planned();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(smem_u32(&ctl->taken[slot]));
+      if (++slot == PLANNED) { slot = 0; slot_phase ^= 1; }
+      return some;
+    };
+    for (bool have = first_tile(); have; have = next_of_group()) {
       const int n = tc.n0 + 128 * (int)rank + 8 * (int)(lane & 15);  // of what the lane stores
       bool ok = true;
       for (int h = 0; ok && h < P::HALVES; ++h) {
@@ -820,13 +950,13 @@ product16_pair_kernel(const __grid_constant__ CUtensorMap tmA,    // 128 rows of
     static_assert(P::ROWS * PART_ROW <= RING * UNIT && P::HALVES == 1, "part");
     __syncwarp();
     cluster_sync();
-    if (warp >= 2 && tile0 < total_tiles) {
+    if (warp >= 2 && warp < PLAN_WARP && tile0 < total_tiles) {
       GroupWalk<P::ROWS, 256, P::BAND> again;
       again.locate(args, ctl->list, tile0, tc);
       const int height = half_height<P>(tc, 0);
       const int n = tc.n0 + 128 * (int)rank + 8 * (int)(lane & 15);
       const int first = (int)part + P::SPLIT * (int)((threadIdx.x - 64) / 16);
-      for (int r = first; r < height; r += P::SPLIT * (PAIR_THREADS - 64) / 16) {
+      for (int r = first; r < height; r += P::SPLIT * 16) {
         const int64_t row = tc.m0 + r;
         if (row >= tc.m_end || n >= args.N) continue;  // N is a multiple of 8
         float4 v[2][P::SPLIT];
@@ -879,7 +1009,9 @@ cudaError_t launch_pair(const Product16Args& args, int num_sms, cudaStream_t str
     return cudaErrorInvalidValue;
   const cudaError_t e = allow_smem<product16_pair_kernel<P>>(kPairSmem);
   if (e != cudaSuccess) return e;
-  const int64_t tiles = most_tiles(args, P::ROWS, 256), units = num_sms / (2 * P::SPLIT);
+  int64_t units = num_sms / (2 * P::SPLIT);
+  if (units > MOST_PAIRS) units = MOST_PAIRS;
+  const int64_t tiles = most_tiles(args, P::ROWS, 256);
   return launch_persistent(product16_pair_kernel<P>, tiles < units ? tiles : units, 2 * P::SPLIT,
                            PAIR_THREADS, kPairSmem, stream, tmA, tmA64, tmA32, tmB, args);
 }
@@ -920,22 +1052,26 @@ cudaError_t choose(const Product16Args& a, int num_sms, cudaStream_t stream) {
         a.E == 1 ? (a.M_total + rows - 1) / rows : a.M_total / rows + (a.E + 1) / 2;
     return (row_tiles > a.E ? row_tiles : a.E) * ((a.N + 255) / 256);
   };
-  // Tiles of 512 rows where groups are mostly over 256 or near it (64 groups of 260 rows, 7168 x
-  // 2048: 413 us, 509 with 256; groups of 128: 311 and 297) and there are enough of them to even out.
-  if (a.M_total >= (int64_t)192 * a.E && tiles(512) >= 6 * units)
-    return launch_pair<Pair<BT, 512>>(a, num_sms, stream);
-  // Else what takes least of 256, 128 or 64 rows, or of 128 whose K two or four pairs share: rounds of
-  // tiles, each of so many units of 4 KB per block of 64 K, and about 48 units to start and end it.
-  // Against the best of the others (us): 545 rows, 3000 x 1256, with 128 rows 13.3 and 14.7; 1024
-  // rows, 4096 x 4096, with 256 26.0 and 39.6; 8 groups of 158, 952 x 3120, with 128 19.8 and 20.2;
-  // 128 rows, 4096 x 4096, shared by two 16.8 and 21.4.
+  // What takes least of tiles of 512, 256, 128 or 64 rows, or of 128 whose K two or four pairs share: a
+  // tile so many units of 4 KB per block of 64 K, and about 48 units to start and end it; of more tiles
+  // than pairs the last ones leave some pairs idle, for half a tile or, of 512 rows, one.  Where little
+  // is between them the higher ones: groups of many rows read their weights less often.  With each
+  // height, us: 64 groups of 260 rows, 7168 x 2048: 496 in tiles of 256 and 400 of 512; 7 of 585, 4096 x
+  // 7168: 235 of 128, 174 of 256, 220 of 512; 8177 rows over 128 groups, the largest 1517, 4096 x 2048:
+  // 367 of 128, 345 of 256; 545 rows, 3000 x 1256: 18.9 of 64, 13.3 of 128, 14.7 of 256; 128 rows, 4096
+  // x 4096: 21.4, shared by two pairs 16.8; 1000 rows, 512 x 2048: 13.6, by two 12.8.
   auto cost = [&](int rows, int split) {
-    const int64_t n = tiles(rows), rounds = (n + units / split - 1) / (units / split);
+    const int64_t n = tiles(rows);
     const double height = (double)a.M_total * ((a.N + 255) / 256) / n;
-    return rounds * ((blocks + split - 1) / split * (4 + height / 64) + 48 + (split == 1 ? 0 : split == 2 ? 48 : 80));
+    const double kb = (double)((blocks + split - 1) / split), ends = split == 1 ? 48 : split == 2 ? 96 : 128;
+    const double one = kb * (4 + height / 64) + ends;
+    if (n * split <= units) return one;
+    return one * n * split / units + (rows == 512 ? 1.2 : 0.6) * (kb * (4 + rows / 64) + ends);
   };
-  const double c64 = cost(64, 1), c128 = cost(128, 1), c256 = cost(256, 1);
-  const double least = c64 < c128 ? (c64 < c256 ? c64 : c256) : (c128 < c256 ? c128 : c256);
+  const double c64 = 1.06 * cost(64, 1), c128 = 1.03 * cost(128, 1), c256 = cost(256, 1);
+  const double c512 = cost(512, 1);
+  const double low = c64 < c128 ? c64 : c128, high = c256 <= c512 ? c256 : c512;
+  const double least = low < high ? low : high;
   const int64_t most = most_tiles(a, 128, 256);
   if (blocks >= 16 && cost(128, 4) < least && cost(128, 4) < cost(128, 2) &&
       most <= pairs_at_once<Pair<BT, 128, 4>>())
@@ -943,6 +1079,7 @@ cudaError_t choose(const Product16Args& a, int num_sms, cudaStream_t stream) {
   if (blocks >= 8 && cost(128, 2) < least && most <= pairs_at_once<Pair<BT, 128, 2>>())
     return launch_pair<Pair<BT, 128, 2>>(a, num_sms, stream);
   if (c256 == least) return launch_pair<Pair<BT, 256>>(a, num_sms, stream);
+  if (c512 == least) return launch_pair<Pair<BT, 512>>(a, num_sms, stream);
   return c128 == least ? launch_pair<Pair<BT, 128>>(a, num_sms, stream)
                        : launch_pair<Pair<BT, 64>>(a, num_sms, stream);
 }
