@@ -26,15 +26,17 @@
 // TB/s).  8 bits, the sums' way out of TMEM: every block of 128 rows has its own scales, so its sums
 // are handed to the epilogue after 512 clocks of MMA, and half of TMEM is taken until they are read
 // and their 2 operations per element under way (the same rows: 589 us, 2099 TFLOP/s; if 256 rows
-// made a block 438, without the scales' products 511, the loads alone 333).  The stage's commit is
-// the hand-over's too (16 groups of 2048 rows 594 -> 576), and the sums go out by TMA (565).  What made it so: the scales
-// land with the operands, counted on their barrier (read from global memory two blocks ahead, the
-// epilogue waited for them: 826 us); a warp reads TMEM as 16 x 256-bit pieces, of which a thread
-// gets 4 rows x 32 columns, 36 scales, and not a row of 128 columns, 129 (shared memory is what the
-// MMA is fed from: 740 -> 646); the pieces are double-buffered, with registers to hold them (589);
-// the roles that wait beside the epilogue sleep in their barriers (16-bit: 880 -> 785).  Four
-// stages: with six the loads of operands run so far ahead that they stand in the way of the
-// gradients' stores (745 -> 617 us).
+// made a block 438, without the scales' products 511, the loads alone 333).
+//
+// What made it so: a stage's one commit is the hand-over's too (8 bits, 16 groups of 2048 rows, 2048 x
+// 7168: 594 -> 576 us), and the sums go out by TMA (565).  The scales land with the operands, counted
+// on their barrier (65536 rows, 2048 x 4608: read from global memory two blocks ahead, the epilogue
+// waited for them, 826); a warp reads TMEM as 16 x 256-bit pieces, of which a thread gets 4 rows x 32
+// columns, 36 scales, and not a row of 128 columns, 129 (shared memory is what the MMA is fed from:
+// 740 -> 646); the pieces are double-buffered, with registers to hold them (589); the 16-bit roles
+// that wait beside the epilogue sleep in their barriers (880 -> 785, then stages of 128 rows, 702).
+// Four stages: with six the loads of operands run so far ahead that they stand in the way of the
+// gradients' stores (16384 rows over 64 experts: 745 -> 617).
 //
 // Roles (12 warps): warp 0 TMA producer; warp 1 TMEM owner and, in CTA 0 of a pair, the MMA thread;
 // warp 2 fixer; warps 4-11 epilogue (TMEM lanes 32 * (w % 4)..: columns n of dC; half of the tile's
