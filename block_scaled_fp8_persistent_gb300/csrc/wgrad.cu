@@ -489,7 +489,9 @@ wgrad_kernel(const __grid_constant__ CUtensorMap tmC, const __grid_constant__ CU
         if (left == 0) continue;
         const uint32_t parity = (seen >> last) & 1;
         seen ^= 1u << last;
-        if (!__all_sync(0xffffffffu, mbar_wait_sleep(tail_bar(last), parity, abort))) {
+        // (the whole group goes by before its last stage: 8 ns for each row on top of the limit)
+        const uint64_t limit = BSFP8_WAIT_LIMIT_NS + 8ull * (uint32_t)(rows - begin);
+        if (!__all_sync(0xffffffffu, mbar_wait_sleep(tail_bar(last), parity, abort, limit))) {
           if (lane == 0) give_up(args.err, abort);
           break;
         }
