@@ -29,7 +29,10 @@ if __name__ == "__main__":
     sys.path.insert(0, os.path.dirname(os.path.dirname(os.path.abspath(__file__))))
     sys.path.insert(0, os.path.dirname(os.path.abspath(__file__)))
 import block_scaled_fp8_persistent_gb300 as bsfp8
-from moe_layer import operand, quantised_weights
+if __package__:
+    from .moe_layer import operand, quantised_weights
+else:
+    from moe_layer import operand, quantised_weights
 
 
 class TrainedExperts:
