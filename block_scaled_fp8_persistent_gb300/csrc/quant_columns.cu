@@ -7,13 +7,13 @@
 // the blockwise rule of quant.cuh turned by 90 degrees.  Rows may be gathered: row r of q comes
 // from the token whose slot lies in row r.  Each element is read once, kept in registers while its
 // block's largest magnitude is found, and written once: 65536 rows of 7168 take 216 us, 6.6 TB/s,
-// what HBM gives.  Gathered from 8192 tokens the same rows come out of L2, and at 172 us the
-// instructions bound it (with the loads left out 147).
+// what HBM gives.  Gathered from 8192 tokens the same rows come out of L2, and at 169 us
+// instructions and barriers bound it (with the loads left out 147).
 //
-// A block of threads takes the 128 rows of a scale block and walks over tiles of 128 columns, the
-// next two under way (cp.async; a thread reads back what it copied itself): thread (i, c) the 8
-// columns 8 c.. of the rows i, i + 16, .., so that 16 threads read 256 bytes of a row (16-bit) and
-// write 128.  Which rows those are the offsets say: block b of the scales belongs to the last
+// A block of threads takes the 128 rows of a scale block and walks over tiles of 128 or 64 columns, the
+// next ones under way (cp.async; a thread reads back what it copied itself): thread (i, c) the 8
+// columns 8 c.. of the rows i, i + 16, .., so that 16 (8) threads read 256 (128) bytes of a row
+// (16-bit) and write half as many.  Which rows those are the offsets say: block b of the scales belongs to the last
 // group e with offsets[e] / 128 + e <= b, which the threads count together, once for all tiles.
 #include <atomic>
 #include <cuda_fp16.h>
@@ -25,25 +25,28 @@
 namespace bsfp8 {
 namespace {
 
-constexpr int kBlockRows = 128, kTileCols = 128;
-constexpr int kThreads = 256;
-constexpr int kColumnThreads = kTileCols / 8;           // threads side by side
-constexpr int kRowThreads = kThreads / kColumnThreads;  // 16
-constexpr int kRowsEach = kBlockRows / kRowThreads;     // 8
-
-// Tiles in flight and blocks per SM.  Gathered rows come out of L2, and more threads are worth more
-// than more tiles: 65536 rows of 7168 by 8 of 8192 172 us, with 3 and 2 195; rows that lie side by
-// side come from HBM and want the depth (320 rows of 2048 3.5 us against 4.0).
-template <bool GATHER>
-constexpr int kStages = GATHER ? 2 : 3;
-template <int XT, bool GATHER>
-constexpr int kResident = XT == E_FP32 ? 1 : GATHER ? 3 : 2;
+constexpr int kBlockRows = 128;
+constexpr int kRowThreads = 16;                      // of a column of threads
+constexpr int kRowsEach = kBlockRows / kRowThreads;  // 8
 
 template <int XT>
 constexpr int kEightBytes = XT == E_FP32 ? 32 : 16;  // of 8 elements as they are stored
 
-template <int XT>
-constexpr int kStageBytes = kBlockRows * kColumnThreads * kEightBytes<XT>;
+// Columns of a tile, tiles in flight and blocks per SM.  16-bit rows that lie side by side come from
+// HBM and want long pieces and depth (65536 rows of 7168: 216 us, in tiles of 64 columns 242).  Gathered
+// rows come out of L2, and more blocks, whose barriers hold fewer threads, are worth more than more
+// tiles: of 8 of 8192 tokens 169 us (128 columns 172, with three tiles 195), 16384 rows by 8 of 2048
+// tokens 50 (58).  fp32 fills shared memory with twice the bytes: 16384 rows of 4096 61 us, 77 with
+// 128 columns.
+template <int XT, bool GATHER>
+struct Tile {
+  static constexpr int COLS = GATHER || XT == E_FP32 ? 64 : 128;
+  static constexpr int COLUMN_THREADS = COLS / 8;  // side by side
+  static constexpr int THREADS = kRowThreads * COLUMN_THREADS;
+  static constexpr int STAGES = GATHER ? 2 : 3;
+  static constexpr int RESIDENT = XT == E_FP32 ? 2 : GATHER ? 6 : 2;
+  static constexpr int STAGE_BYTES = kBlockRows * COLUMN_THREADS * kEightBytes<XT>;
+};
 
 // Eight elements as they are stored.
 template <int XT>
@@ -105,10 +108,12 @@ __device__ __forceinline__ float2 pair(const Eight<XT>& x, int j) {
 }
 
 template <int XT, bool GATHER>
-__global__ void __launch_bounds__(kThreads, kResident<XT, GATHER>)
+__global__ void __launch_bounds__(Tile<XT, GATHER>::THREADS, Tile<XT, GATHER>::RESIDENT)
     columns_kernel(ColumnsArgs a, int blocks, int each, bool early) {
   extern __shared__ __align__(16) uint8_t stages[];
-  constexpr int STAGES = kStages<GATHER>;
+  using T = Tile<XT, GATHER>;
+  constexpr int STAGES = T::STAGES, kTileCols = T::COLS, kThreads = T::THREADS;
+  constexpr int kColumnThreads = T::COLUMN_THREADS;
   constexpr int kWords = kEightBytes<XT> / 4;          // of a thread's eight columns
   constexpr int kTileWords = kWords * kColumnThreads;  // of a tile's row
   __shared__ __align__(16) uint32_t part[2][kThreads / 32][kTileWords];
@@ -170,7 +175,7 @@ __global__ void __launch_bounds__(kThreads, kResident<XT, GATHER>)
   const uint32_t mine_u32 = smem_u32(mine);
   auto fetch = [&](bool any, int stage) {
     if (any) {
-      const uint32_t dst = mine_u32 + stage * kStageBytes<XT>;
+      const uint32_t dst = mine_u32 + stage * T::STAGE_BYTES;
 #pragma unroll
       for (int j = 0; j < kRowsEach; ++j) {
 #pragma unroll
@@ -195,13 +200,15 @@ __global__ void __launch_bounds__(kThreads, kResident<XT, GATHER>)
     Eight<XT> x[kRowsEach], top = {};
 #pragma unroll
     for (int j = 0; j < kRowsEach; ++j)
-      x[j] = read8<XT>(mine + stage * kStageBytes<XT> + j * kThreads * kEightBytes<XT>);
+      x[j] = read8<XT>(mine + stage * T::STAGE_BYTES + j * kThreads * kEightBytes<XT>);
     if (++stage == STAGES) stage = 0;
 #pragma unroll
     for (int j = 0; j < kRowsEach; j += 2) take_max<XT>(top, x[j], x[j + 1]);
 #pragma unroll
     for (int i = 0; i < kWords; ++i)
-      top.w[i] = max_words<XT>(top.w[i], __shfl_xor_sync(0xffffffffu, top.w[i], 16));
+#pragma unroll
+      for (int d = 16; d >= kColumnThreads; d /= 2)
+        top.w[i] = max_words<XT>(top.w[i], __shfl_xor_sync(0xffffffffu, top.w[i], d));
     if (threadIdx.x % 32 < kColumnThreads) {
       uint4* p = reinterpret_cast<uint4*>(&part[side][threadIdx.x / 32][kWords * c]);
 #pragma unroll
@@ -257,7 +264,8 @@ cudaError_t columns_as(const ColumnsArgs& a, cudaStream_t stream) {
   // L2 that long.  A block's way to its rows (offsets, slots, rows) is three round trips to L2, so
   // stripes are no narrower than it takes to keep the SMs busy to the end.
   constexpr int64_t kBlocks = 2500;
-  constexpr int kSmem = kStages<GATHER> * kStageBytes<XT>;
+  using T = Tile<XT, GATHER>;
+  constexpr int kSmem = T::STAGES * T::STAGE_BYTES;
   static std::atomic<bool> attr_set[64];  // per device; several host threads may launch
   int dev = 0;
   cudaGetDevice(&dev);
@@ -268,12 +276,12 @@ cudaError_t columns_as(const ColumnsArgs& a, cudaStream_t stream) {
     if (dev < 64) attr_set[dev].store(true, std::memory_order_release);
   }
   const int64_t blocks = a.M_total / kBlockRows + a.E;
-  const int tiles = a.K / kTileCols;
+  const int tiles = a.K / T::COLS;
   const int64_t want = (kBlocks + blocks - 1) / blocks;
   const int each = (int)((tiles + want - 1) / want);
   const dim3 grid((unsigned)(blocks * ((tiles + each - 1) / each)));
-  const bool early = starts_early(grid, (int64_t)kBlockRows * kTileCols * 3 * each);
-  return launch(columns_kernel<XT, GATHER>, grid, kThreads, kSmem, early, stream, 1, a, (int)blocks, each, early);
+  const bool early = starts_early(grid, (int64_t)kBlockRows * T::COLS * 3 * each);
+  return launch(columns_kernel<XT, GATHER>, grid, T::THREADS, kSmem, early, stream, 1, a, (int)blocks, each, early);
 }
 
 }  // namespace

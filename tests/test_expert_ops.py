@@ -652,3 +652,17 @@ def test_product_as_many_groups_as_are_listed(groups, each):
     # groups with rows between empty ones, under expert ids that go round
     sizes = [each if g % 2 else 0 for g in range(2 * groups)]
     _product(sizes, 72, 136, ids=[g % 5 for g in range(2 * groups)], experts=5)
+
+
+@pytest.mark.parametrize("groups", [127, 128, 129])
+@pytest.mark.parametrize("each,spare", [(1, 0), (40, 3)])
+def test_product_about_as_many_groups_as_are_listed(groups, each, spare):
+    _product([each if g % 3 else 0 for g in range(groups * 3 // 2)] + [each], 520, 136, spare=spare)
+
+
+@pytest.mark.parametrize("transposed", [False, True])
+@pytest.mark.parametrize("sizes", [[700, 0, 420, 900, 1], [130] * 24, [2500, 16, 16, 16], [64] * 150], ids=["uneven", "even", "one large", "many"])
+@pytest.mark.parametrize("N,K", [(3080, 512), (3080, 200)])
+def test_product_planned_over_several_rounds(sizes, N, K, transposed):
+    # more tiles than pairs of SMs, with a plan (K of 8 blocks) and without
+    _product(sizes, N, K, BF16, transposed, seed=8)
