@@ -790,12 +790,13 @@ cudaError_t by_type(const WgradArgs& a, int num_sms, cudaStream_t stream) {
 }  // namespace wg
 
 cudaError_t launch_wgrad(const WgradArgs& a, int num_sms, cudaStream_t stream) {
-  // Few tiles and many rows: four pairs share a tile's rows (8192 rows, 512 x 512: 54 -> 21 us).
+  // Few tiles and many rows: four pairs share a tile's rows (512 x 512: 8192 rows 54 -> 21 us; 304 x 416:
+  // 1000 rows 12.6 -> 11.0, 3 groups of 900 12.4 -> 11.6, of 600 10.9 -> 11.5).
   const int64_t tiles = (int64_t)a.E * ((a.N + 255) / 256) * ((a.K + 255) / 256);
   using Split8 = wg::Cfg<true, 128, 4, false, 4>;
   using Split16 = wg::Cfg<false, 128, 3, false, 4>;
   const bool split =
-      a.M_total >= (int64_t)1024 * a.E &&
+      a.M_total >= (int64_t)768 * a.E &&
       tiles <= (a.fp8 ? wg::at_once<Split8>() : wg::at_once<Split16>());
   // The gradients go out through shared memory and TMA, so that the epilogue takes up the next tile's
   // sums at once, or straight from the threads, in whole lines.  Which is faster was measured (32

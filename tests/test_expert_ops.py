@@ -662,7 +662,7 @@ def test_product_about_as_many_groups_as_are_listed(groups, each, spare):
 
 @pytest.mark.parametrize("transposed", [False, True])
 @pytest.mark.parametrize("sizes", [[700, 0, 420, 900, 1], [130] * 24, [2500, 16, 16, 16], [64] * 150], ids=["uneven", "even", "one large", "many"])
-@pytest.mark.parametrize("N,K", [(3080, 512), (3080, 200)])
+@pytest.mark.parametrize("N,K", [(3080, 2048), (3080, 200)])
 def test_product_planned_over_several_rounds(sizes, N, K, transposed):
-    # more tiles than pairs of SMs, with a plan (K of 8 blocks) and without
+    # more tiles than pairs of SMs, with a plan (K of 32 blocks) and without
     _product(sizes, N, K, BF16, transposed, seed=8)
