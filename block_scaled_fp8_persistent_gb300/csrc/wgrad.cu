@@ -104,6 +104,7 @@ struct Ctl {
   uint64_t tempty[2];
   uint64_t mma_done;
   uint32_t tmem_base;
+  uint32_t issued;  // stages that this CTA's producer has sent for
   int abort;
   int valid;
 };
@@ -293,6 +294,7 @@ wgrad_kernel(const __grid_constant__ CUtensorMap tmC, const __grid_constant__ CU
                                              ~static_cast<uintptr_t>(1023));
   Ctl<C>* ctl = reinterpret_cast<Ctl<C>*>(smem + C::SMEM_CTL);
   volatile int* abort = &ctl->abort;
+  volatile uint32_t* sent = &ctl->issued;
   const uint32_t warp = threadIdx.x >> 5;
   const uint32_t lane = threadIdx.x & 31;
   // of the CTA in its pair, its pair's leader in the cluster, and the pair's share of a split tile
@@ -325,6 +327,7 @@ wgrad_kernel(const __grid_constant__ CUtensorMap tmC, const __grid_constant__ CU
     }
     mbar_init(smem_u32(&ctl->mma_done), 1);
     ctl->abort = 0;
+    ctl->issued = 0;
     fence_mbarrier_init();
   }
   if (warp == 1) {
@@ -409,7 +412,7 @@ wgrad_kernel(const __grid_constant__ CUtensorMap tmC, const __grid_constant__ CU
             }
           }
           if (++slot == C::SLOTS) slot = 0;
-          ++issued;
+          *sent = (uint32_t)++issued;
           if (++stage == C::STAGES) { stage = 0; phase ^= 1; }
         }
       }
@@ -479,6 +482,17 @@ wgrad_kernel(const __grid_constant__ CUtensorMap tmC, const __grid_constant__ CU
       // the end of the MMA step that holds it (whole 128-byte lines, whatever the swizzle).
       uint32_t stage = 0;
       uint32_t seen = 0;  // parity of every stage's tail barrier, a bit each
+      // Before a tail its whole group goes by, and every tile before it that had none: a wait has
+      // run out when for its limit the producer has sent for nothing either.
+      auto landed = [&](uint32_t bar, uint32_t parity) {
+        uint32_t before = *sent;
+        while (!mbar_wait_sleep(bar, parity, abort)) {
+          const uint32_t now = *sent;
+          if (*abort || now == before) return false;
+          before = now;
+        }
+        return true;
+      };
       for (Walk t(tile0); t.inside(shape); t.local += tile_stride) {
         int begin, rows;
         t.rows<C::SPLIT>(args, part, begin, rows);
@@ -489,9 +503,7 @@ wgrad_kernel(const __grid_constant__ CUtensorMap tmC, const __grid_constant__ CU
         if (left == 0) continue;
         const uint32_t parity = (seen >> last) & 1;
         seen ^= 1u << last;
-        // (the whole group goes by before its last stage: 8 ns for each row on top of the limit)
-        const uint64_t limit = BSFP8_WAIT_LIMIT_NS + 8ull * (uint32_t)(rows - begin);
-        if (!__all_sync(0xffffffffu, mbar_wait_sleep(tail_bar(last), parity, abort, limit))) {
+        if (!__all_sync(0xffffffffu, landed(tail_bar(last), parity))) {
           if (lane == 0) give_up(args.err, abort);
           break;
         }
