@@ -31,6 +31,15 @@ namespace g16 {
 
 constexpr int BK = 64;  // elements: 128 bytes
 
+// The tensor core's additions truncate: a sum of n terms of one sign in one accumulator comes out
+// 6.4e-9 n of it short.  So an accumulator takes parts of K of at most 16384 for fp16 results (1.05e-4 of
+// the sum, less than half of a rounding, which is 2.4e-4 to 4.9e-4) and 131072 for bf16 (8.4e-4; 2.0e-3 to
+// 3.9e-3), and longer parts are summed in chunks of 4096 that are added up in fp32 (2.6e-5 whatever K is;
+// in one accumulator a K of 2^20 lost 6.7e-3).  Chunks want a thread's sums in registers, in tiles of up to
+// 256 rows: 8192 x 8192 x 65536 in fp16 5.1-5.4 ms, in one accumulator 4.8.
+constexpr int MOST_BLOCKS_FP16 = 16384 / BK, MOST_BLOCKS_BF16 = 131072 / BK;
+constexpr int CHUNK_BLOCKS = 4096 / BK;
+
 // The tiles that CTA (or pair) `unit` of `units` takes: one of every `units`, in each round the next
 // place.  Row tiles of a group follow one another in the numbering, the last often a small one; at
 // a fixed place some units would get all the full ones (64 groups of 70 to 900 rows, 7168 x 2048:
@@ -464,12 +473,14 @@ cudaError_t launch_few(const Product16Args& args, int64_t max_tiles, int num_sms
 // N: one instruction, or two on the same weights)
 // ---------------------------------------------------------------------------------------
 // ROWS: that a tile may have.  SPLIT: pairs, in one cluster, that share a tile's K, each cluster one
-// tile.
-template <bool BT_, int ROWS_, int SPLIT_ = 1>
+// tile.  CHUNK: blocks of K that accumulate in TMEM, and are then added up in fp32; 0: all of them.
+template <bool BT_, int ROWS_, int SPLIT_ = 1, int CHUNK_ = 0>
 struct Pair {
   static constexpr bool BT = BT_;  // B [E, K, N]
   static constexpr int ROWS = ROWS_;
   static constexpr int SPLIT = SPLIT_;
+  static constexpr int CHUNK = CHUNK_;
+  static_assert(CHUNK == 0 || (ROWS <= 256 && SPLIT == 1), "a thread's sums");
   static constexpr int HALVES = ROWS == 512 ? 2 : 1;  // of up to 256 rows
   static constexpr int BAND = 4096 / ROWS;
 };
@@ -741,11 +752,23 @@ product16_pair_kernel(const __grid_constant__ CUtensorMap tmA,    // 128 rows of
       for (bool have = first_tile(); ok && have; have = ok && next_tile(ok)) {
         const uint32_t n0 = half_height<P>(tc, 0), n1 = P::HALVES == 2 ? half_height<P>(tc, 1) : 0;
         const uint32_t units0 = half_units(n0), units = W_UNITS + units0 + half_units(n1);
-        const uint32_t d0 = tmem_base + acc * 256, d1 = tmem_base + (acc ^ 1) * 256;
+        uint32_t d0 = tmem_base + acc * 256;
+        const uint32_t d1 = tmem_base + (acc ^ 1) * 256;
         ok = mbar_wait_sleep(tempty_bar(acc), acc_phase ^ 1, abort);
         if (n1 && ok)  // (a second half that wraps around to TMEM's first is a turn later)
           ok = mbar_wait_sleep(tempty_bar(acc ^ 1), acc ? acc_phase : acc_phase ^ 1, abort);
+        uint32_t more = 0;  // whether what is in TMEM is added to
         for (int kb = kb0; ok && kb < kb1; ++kb) {
+          if constexpr (P::CHUNK > 0) {
+            if (kb > kb0 && (kb - kb0) % P::CHUNK == 0) {  // on to the other half
+              umma_commit_pair(tfull_bar(acc), both);
+              if (++acc == 2) { acc = 0; acc_phase ^= 1; }
+              ok = mbar_wait_sleep(tempty_bar(acc), acc_phase ^ 1, abort);
+              if (!ok) break;
+              d0 = tmem_base + acc * 256;
+              more = 0;
+            }
+          }
           ok = mbar_wait_sleep(full_bar(ring.slot), ring.phase, abort);
           if (!ok) break;
           tc_fence_after();
@@ -755,14 +778,15 @@ product16_pair_kernel(const __grid_constant__ CUtensorMap tmA,    // 128 rows of
 #pragma unroll
           for (int k = 0; k < BK / 16; ++k)
             umma_f16<2>(d0, wdesc + k * kStepW, adesc + k * kStepA, idesc0 | (n0 >> 3) << 17,
-                        kb > kb0 || k > 0);
+                        more || k > 0);
           if (n1) {
             const uint64_t adesc1 = adesc + ((units0 * UNIT) >> 4);
 #pragma unroll
             for (int k = 0; k < BK / 16; ++k)
               umma_f16<2>(d1, wdesc + k * kStepW, adesc1 + k * kStepA, idesc0 | (n1 >> 3) << 17,
-                          kb > kb0 || k > 0);
+                          more || k > 0);
           }
+          more = 1;
           umma_commit_pair(empty_bar(ring.slot), both);
           ring.next();
         }
@@ -905,39 +929,81 @@ product16_pair_kernel(const __grid_constant__ CUtensorMap tmA,    // 128 rows of
           __syncwarp();
           if (lane == 0) mbar_arrive_cluster(acc ? tempty_1 : tempty_0);
         };
-        if (32 * (int)group >= height) release();
-        for (int c = 32 * (int)group; c < height; c += 64) {
-          uint32_t p[32];
-          tmem_ld_32x32b_x32(taddr + c, p);  // (past the height: whatever is there, not stored)
-          tmem_ld_wait();
-          if (c + 64 >= height) release();
-          if constexpr (P::SPLIT > 1) {  // the part, rows of 128 columns, in the ring: it is done with
+        auto store = [&](int c, const uint32_t (&p)[32]) {  // rows c.. of the half
 #pragma unroll
-            for (int j = 0; j < 32; ++j)
-              *reinterpret_cast<uint32_t*>(smem + (c + j) * PART_ROW + (quarter * 32 + lane) * 4) = p[j];
-          } else {
+          for (int j = 0; j < 32; j += 2) {
+            const float lo = __uint_as_float(p[j]), hi = __uint_as_float(p[j + 1]);
+            const uint32_t own = args.bf16 ? pack_bf16x2(lo, hi) : pack_f16x2(lo, hi);
+            const uint32_t other = __shfl_xor_sync(0xffffffffu, own, 1);
+            // even lanes: row j of columns n, n + 1; odd lanes: row j + 1 of columns n - 1, n
+            const uint32_t v =
+                odd ? __byte_perm(other, own, 0x7632) : __byte_perm(own, other, 0x5410);
+            *reinterpret_cast<uint32_t*>(staged + (j + odd) * EPI_ROW +
+                                         (quarter * 32 + (lane & ~1u)) * 2) = v;
+          }
+          group_sync(group);
+          const int row0 = quarter * 8 + (int)(lane >> 4);
 #pragma unroll
-            for (int j = 0; j < 32; j += 2) {
-              const float lo = __uint_as_float(p[j]), hi = __uint_as_float(p[j + 1]);
-              const uint32_t own = args.bf16 ? pack_bf16x2(lo, hi) : pack_f16x2(lo, hi);
-              const uint32_t other = __shfl_xor_sync(0xffffffffu, own, 1);
-              // even lanes: row j of columns n, n + 1; odd lanes: row j + 1 of columns n - 1, n
-              const uint32_t v =
-                  odd ? __byte_perm(other, own, 0x7632) : __byte_perm(own, other, 0x5410);
-              *reinterpret_cast<uint32_t*>(staged + (j + odd) * EPI_ROW +
-                                           (quarter * 32 + (lane & ~1u)) * 2) = v;
+          for (int i = 0; i < 4; ++i) {
+            const int r = row0 + 2 * i;
+            const int64_t row = tc.m0 + 256 * h + c + r;
+            const uint4 v = *reinterpret_cast<const uint4*>(staged + r * EPI_ROW + 16 * (lane & 15));
+            if (row < tc.m_end && n < args.N)
+              st_global_v4_hint(Cmat + row * (int64_t)args.N + n, v.x, v.y, v.z, v.w, pol_c);
+          }
+          group_sync(group);  // read before it is written again
+        };
+        if constexpr (P::CHUNK > 0) {
+          // (the first chunk has been waited for, and the last one's turn is taken below)
+          constexpr int PIECES = P::ROWS / 64;
+          float sum[PIECES][32] = {};
+          for (int kb = kb0;;) {
+            const uint32_t from = tmem_base + ((quarter * 32) << 16) + acc * 256;
+#pragma unroll
+            for (int i = 0; i < PIECES; ++i) {
+              const int c = 32 * (int)group + 64 * i;
+              if (c >= height) break;
+#pragma unroll
+              for (int j0 = 0; j0 < 32; j0 += 16) {
+                uint32_t p[16];
+                tmem_ld_32x32b_x16(from + c + j0, p);
+                tmem_ld_wait();
+#pragma unroll
+                for (int j = 0; j < 16; ++j) sum[i][j0 + j] += __uint_as_float(p[j]);
+              }
             }
-            group_sync(group);
-            const int row0 = quarter * 8 + (int)(lane >> 4);
+            release();
+            kb += P::CHUNK;
+            if (kb >= kb1) break;
+            if (++acc == 2) { acc = 0; acc_phase ^= 1; }
+            ok = all_of_group(group, mbar_wait_sleep(tfull_bar(acc), acc_phase, abort));
+            if (!ok) break;
+            tc_fence_after();
+          }
+          if (!ok) break;
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              const int r = row0 + 2 * i;
-              const int64_t row = tc.m0 + 256 * h + c + r;
-              const uint4 v = *reinterpret_cast<const uint4*>(staged + r * EPI_ROW + 16 * (lane & 15));
-              if (row < tc.m_end && n < args.N)
-                st_global_v4_hint(Cmat + row * (int64_t)args.N + n, v.x, v.y, v.z, v.w, pol_c);
+          for (int i = 0; i < PIECES; ++i) {
+            const int c = 32 * (int)group + 64 * i;
+            if (c >= height) break;
+            uint32_t p[32];
+#pragma unroll
+            for (int j = 0; j < 32; ++j) p[j] = __float_as_uint(sum[i][j]);
+            store(c, p);
+          }
+        } else {
+          if (32 * (int)group >= height) release();
+          for (int c = 32 * (int)group; c < height; c += 64) {
+            uint32_t p[32];
+            tmem_ld_32x32b_x32(taddr + c, p);  // (past the height: whatever is there, not stored)
+            tmem_ld_wait();
+            if (c + 64 >= height) release();
+            if constexpr (P::SPLIT > 1) {  // the part, rows of 128 columns, in the ring: it is done with
+#pragma unroll
+              for (int j = 0; j < 32; ++j)
+                *reinterpret_cast<uint32_t*>(smem + (c + j) * PART_ROW + (quarter * 32 + lane) * 4) = p[j];
+            } else {
+              store(c, p);
             }
-            group_sync(group);  // read before it is written again
           }
         }
         if (++acc == 2) { acc = 0; acc_phase ^= 1; }
@@ -1037,18 +1103,21 @@ cudaError_t choose(const Product16Args& a, int num_sms, cudaStream_t stream) {
   // 12.8).
   const int64_t few_tiles = most_tiles(a, FEW_ROWS, FEW_COLS);
   const int64_t blocks = (a.K + BK - 1) / BK;
-  if (blocks >= 16 && few_tiles <= few_at_once<Few<BT, 8>>())
+  // whether one accumulator will do for each of `split` parts of K
+  const int most_blocks = a.bf16 ? MOST_BLOCKS_BF16 : MOST_BLOCKS_FP16;
+  auto one_sum = [&](int split) { return (blocks + split - 1) / split <= most_blocks; };
+  if (blocks >= 16 && one_sum(8) && few_tiles <= few_at_once<Few<BT, 8>>())
     return launch_few<Few<BT, 8>>(a, few_tiles, num_sms, stream);
-  if (blocks >= 8 && few_tiles <= few_at_once<Few<BT, 4>>())
+  if (blocks >= 8 && one_sum(4) && few_tiles <= few_at_once<Few<BT, 4>>())
     return launch_few<Few<BT, 4>>(a, few_tiles, num_sms, stream);
-  if (blocks >= 4 && few_tiles <= few_at_once<Few<BT, 2>>())
+  if (blocks >= 4 && one_sum(2) && few_tiles <= few_at_once<Few<BT, 2>>())
     return launch_few<Few<BT, 2>>(a, few_tiles, num_sms, stream);
   // Up to 8 rows per group on average, most groups are one tile of 32 rows: less to load and to
   // set up than in tiles of pairs (64 groups of 1 row, 2048 x 2048: 81 us against 88; 16 of 8, 2048
   // x 4096: 45 and 48).  With more of them a few groups can hold many, and each reads its weights
   // once per 32 rows (4027 rows over 128 groups, the largest 753, 4096 x 2048: 422 us against 330;
   // 4096 rows in one of them 222 and 51; 16 rows in each 327 and 322).
-  if (a.M_total <= FEW_ROWS || a.M_total <= (int64_t)8 * a.E)
+  if (one_sum(1) && (a.M_total <= FEW_ROWS || a.M_total <= (int64_t)8 * a.E))
     return launch_few<Few<BT, 1>>(a, few_tiles, num_sms, stream);
   const int64_t units = num_sms / 2;
   // about how many tiles there are: the last of a group is half full
@@ -1076,13 +1145,14 @@ cudaError_t choose(const Product16Args& a, int num_sms, cudaStream_t stream) {
   const double c64 = 1.06 * cost(64, 1), c128 = 1.03 * cost(128, 1), c256 = cost(256, 1);
   const double c512 = cost(512, 1);
   const double low = c64 < c128 ? c64 : c128, high = c256 <= c512 ? c256 : c512;
-  const double least = low < high ? low : high;
+  const double least = !one_sum(1) ? c256 : low < high ? low : high;
   const int64_t most = most_tiles(a, 128, 256);
-  if (blocks >= 16 && cost(128, 4) < least && cost(128, 4) < cost(128, 2) &&
+  if (blocks >= 16 && one_sum(4) && cost(128, 4) < least && cost(128, 4) < cost(128, 2) &&
       most <= pairs_at_once<Pair<BT, 128, 4>>())
     return launch_pair<Pair<BT, 128, 4>>(a, num_sms, stream);
-  if (blocks >= 8 && cost(128, 2) < least && most <= pairs_at_once<Pair<BT, 128, 2>>())
+  if (blocks >= 8 && one_sum(2) && cost(128, 2) < least && most <= pairs_at_once<Pair<BT, 128, 2>>())
     return launch_pair<Pair<BT, 128, 2>>(a, num_sms, stream);
+  if (!one_sum(1)) return launch_pair<Pair<BT, 256, 1, CHUNK_BLOCKS>>(a, num_sms, stream);
   if (c256 == least) return launch_pair<Pair<BT, 256>>(a, num_sms, stream);
   if (c512 == least) return launch_pair<Pair<BT, 512>>(a, num_sms, stream);
   return c128 == least ? launch_pair<Pair<BT, 128>>(a, num_sms, stream)

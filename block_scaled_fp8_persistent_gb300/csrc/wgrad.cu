@@ -16,9 +16,9 @@
 // Sums: a chunk of rows accumulates in TMEM (fp8: the 128 rows of a scale block; 16-bit operands:
 // 512 rows), and the epilogue warps add the chunks into fp32 registers, scaled by sc[n] * sa[k].
 // The tensor core's additions do not round to nearest, and their errors add up: of 65536 rows in
-// one chunk the sum is off by 7.6e-5 of its norm, in chunks of 2048 by 2.1e-6, of 512 by 5e-7, as
-// a plain fp32 sum; chunks of 512 cost 3 % of the time of one.  Two chunks are in TMEM at a time,
-// so that the MMAs of the next run meanwhile.
+// one chunk the sum is off by 7.6e-5 of its norm, in chunks of 2048 by 2.1e-6, of 512 by 5e-7 (some 230
+// rows in one chunk 3.2e-7, where a sum that rounds is off by 1.4e-7); chunks of 512 cost 3 % of the
+// time of one.  Two chunks are in TMEM at a time, so that the MMAs of the next run meanwhile.
 //
 // What bounds it: 16-bit, the tensor core and the operands' way from L2 (65536 rows, 2048 x 4608:
 // 702 us, 1762 TFLOP/s with 144 tiles for 76 pairs; the loads alone 525) or, with few rows per

@@ -31,3 +31,33 @@ def test_wgrad8_waits_for_a_last_group_behind_a_second_of_whole_stages():
     bsfp8.bsfp8_grouped_wgrad(ones, ones, scales, scales, off, dB, rows, N, N, 2)
     _no_error()
     assert torch.all(dB[0] == M0) and torch.all(dB[1] == last)
+
+
+# ------------------------------------------------------------------------------ long sums
+@pytest.mark.parametrize("dtype", [BF16, FP16])
+@pytest.mark.parametrize("transposed", [False, True])
+@pytest.mark.parametrize("sizes,N,K", [
+    ([1], 64, 16384), ([1], 64, 131072), ([3, 0, 1], 136, 131080), ([1], 64, 1 << 20),
+    ([300], 512, 16384), ([300], 512, 65536), ([300], 512, 65600), ([300], 512, 262144), ([17, 0, 40, 1], 264, 1 << 18), ([300], 264, 1 << 20),
+    ([1000, 700, 1, 257], 1032, 16448), ([513, 90], 2048, 40968),
+], ids=str)
+def test_product_long_sums_of_one_sign(sizes, N, K, transposed, dtype):
+    """Terms of one sign, so that what an accumulator loses adds up.  An MMA of 16 loses at most one
+    unit of its accumulator's sum, 2^-23 T, and no accumulator takes more than 16384 of K for fp16
+    results, 131072 for bf16; chunks of 4096 are added with a rounding each."""
+    g = torch.Generator(device="cuda").manual_seed(N + K)
+    off = ref.offsets_of(sizes)
+    rows, E = int(off[-1]), len(sizes)
+    some = lambda *shape: (1 + torch.rand(*shape, device="cuda", generator=g))  # noqa: E731
+    A = (some(rows, K) * 2.0 ** -4).to(dtype)
+    B = (some(E, K, N) if transposed else some(E, N, K)).mul_(2.0 ** -8 if K < 1 << 18 else 2.0 ** -12).to(dtype)
+    C = torch.zeros(rows, N, device="cuda", dtype=dtype)
+    bsfp8.bs16_grouped_gemm(A, B, off.cuda(), C, rows, N, K, E, E, transposed=transposed)
+    _no_error()
+    for e, (r0, r1) in enumerate(zip(off.tolist(), off.tolist()[1:])):
+        W = B[e] if transposed else B[e].t()
+        want = sum(A[r0:r1, k: k + 8192].double() @ W[k: k + 8192].double() for k in range(0, K, 8192))
+        most = 16384 if dtype is FP16 else 131072
+        tol = want * ((min(K, most) / 16 + 2) * 2.0 ** -23 + K / 4096 * 2.0 ** -24)
+        off_by = (C[r0:r1].double() - want).abs()
+        assert torch.all(off_by <= tol + (want + tol) * ref.HALF[dtype]), float((off_by / want).max())
