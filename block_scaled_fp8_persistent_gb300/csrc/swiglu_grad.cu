@@ -16,11 +16,26 @@ namespace {
 
 constexpr int kPieceThreads = 256;
 
-// What is quantised is not rounded before.  The exponential is that of the forward operator
-// (its product with log2(e) is rounded: |g| 2^-24 relative); 1 - s costs |g| 2^-25 beside 1 in d_g.
-__device__ __forceinline__ float sigmoid(float g) {
-  return rcp_approx(1.0f + exp2_approx(g * -1.4426950408889634f));
-}
+// s and 1 - s.  What is quantised is not rounded before, and blockwise scales are fp32: there (EXACT)
+// exp(-g) is the library's, to 2 units, and 1 - s is exp(-g) s for g > 0, where the difference would
+// lose |g| 2^-25 beside 1.  Else the exponential is the forward's, 2^t of a rounded t, off by |g| 2^-24,
+// which goes whole into both gradients where g < 0: at most 5e-6, a hundredth of half a step of fp16
+// and less of bf16 and of the codes of 8 and 4 bits.  65536 rows of 2048, exact and not: blockwise with
+// d_h and act 297 us either way; d_h 220 and 212, mxfp8 223 and 210, act alone 148 and 132.
+template <bool EXACT>
+struct Sigmoid {
+  float s, rest;
+  __device__ __forceinline__ explicit Sigmoid(float g) {
+    if constexpr (EXACT) {
+      const float e = expf(-g);
+      s = rcp_approx(1.0f + e);
+      rest = g > 0.0f ? e * s : 1.0f - s;
+    } else {
+      s = rcp_approx(1.0f + exp2_approx(g * -1.4426950408889634f));
+      rest = 1.0f - s;
+    }
+  }
+};
 
 template <int XT>
 __device__ __forceinline__ void store16(void* p, int64_t at, const float (&v)[16]) {
@@ -51,9 +66,10 @@ __global__ void __launch_bounds__(kPieceThreads, 3) swiglu_backward_kernel(Swigl
     if (a.d_act) load16<XT>(a.d_act, t * a.N + (int64_t)i * 16, d);
 #pragma unroll
     for (int e = 0; e < 16; ++e) {
-      const float s = sigmoid(g[e]), silu = g[e] * s, ds = d[e] * s;
+      const Sigmoid<Q && FMT == Q_BLOCKWISE> of(g[e]);
+      const float silu = g[e] * of.s, ds = d[e] * of.s;
       act[e] = silu * u[e];
-      const float d_g = ds * u[e] * fmaf(g[e], 1.0f - s, 1.0f);
+      const float d_g = ds * u[e] * fmaf(g[e], of.rest, 1.0f);
       u[e] = d[e] * silu;
       g[e] = d_g;
     }

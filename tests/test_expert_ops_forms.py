@@ -61,3 +61,29 @@ def test_product_long_sums_of_one_sign(sizes, N, K, transposed, dtype):
         tol = want * ((min(K, most) / 16 + 2) * 2.0 ** -23 + K / 4096 * 2.0 ** -24)
         off_by = (C[r0:r1].double() - want).abs()
         assert torch.all(off_by <= tol + (want + tol) * ref.HALF[dtype]), float((off_by / want).max())
+
+
+# ------------------------------------------------------------------------------ SwiGLU's gradient in fp32
+@pytest.mark.parametrize("dtype", [BF16, FP16])
+def test_swiglu_backward_before_it_is_rounded(dtype):
+    """A block of 128 with one value that is not zero has the scale value / 448 in fp32: the gradient
+    before it is rounded.  In units of 2^-24, with u = d = 1: exp 4 (2 units in the last place), 1 + e
+    1, the reciprocal 2, so s 7; d_u two more for the product and 1 / 448: 9.  1 - s is e s (4 + 7 + 1)
+    or the difference (8 of it), with 1 in between and three roundings around it: 7 + 12 + 4 of d_g's
+    terms."""
+    g = torch.linspace(-80, 80, 64 * 512).to(dtype).view(512, 64)  # 512 rows of 64 blocks
+    rows, N = g.shape[0], 64 * 128
+    h = torch.zeros(rows, 2 * N, dtype=dtype)
+    d = torch.zeros(rows, N, dtype=dtype)
+    h[:, :N: 128], h[:, N:: 128], d[:, ::128] = g, 1.0, 1.0
+    q, scales = torch.zeros(rows, 2 * N, dtype=torch.uint8, device="cuda"), torch.zeros(2 * N // 128, rows, device="cuda")
+    bsfp8.bsmx_swiglu_backward(h.cuda(), d.cuda(), rows, N, q=q, scales=scales, format="blockwise")
+    _no_error()
+    d_g, d_u = (scales.t().double().cpu() * 448).chunk(2, dim=1)
+    x = g.double()
+    s, r = torch.special.expit(x), torch.special.expit(-x)
+    want_g, want_u, unit = (s * (1 + x * r)).abs(), (x * s).abs(), 2.0 ** -24
+    want_u = torch.where(x == 0, torch.full_like(x, 448.0), want_u)  # a block of zeros has scale 1
+    assert torch.all((d_u - want_u).abs() <= 9 * unit * want_u), float(((d_u - want_u).abs() / want_u).max() / unit)
+    off_by = (d_g - want_g).abs() / (s * (1 + x.abs() * r))
+    assert torch.all(off_by <= 23 * unit), float(off_by.max() / unit)
