@@ -23,6 +23,7 @@
 // In both: a TMA producer, an MMA thread (per 64 K four MMAs of K = 16 and one commit) and epilogue
 // warps that store one tile while the next accumulates in the other half of TMEM.
 #include "expert_ops.cuh"
+#include "operand_ring.h"
 #include "ptx.cuh"
 #include "sched.cuh"
 
@@ -484,10 +485,7 @@ struct Pair {
   static constexpr int HALVES = ROWS == 512 ? 2 : 1;  // of up to 256 rows
   static constexpr int BAND = 4096 / ROWS;
 };
-constexpr uint32_t UNIT = 4096;              // 32 rows of 128 bytes: what a stage of the ring counts in
-constexpr uint32_t RING = 51;                // units
-constexpr uint32_t W_UNITS = 4;              // a CTA's 128 weight rows
-constexpr uint32_t MAX_STAGES = 10;          // barriers: one more than the smallest stages that fit
+// (the operands' ring: operand_ring.h)
 constexpr uint32_t PAIR_EPI = RING * UNIT;
 constexpr int PAIR_THREADS = 352;  // warp 0 producer, 1 MMA thread, 2..9 epilogue, 10 plans tiles
 constexpr int PLAN_WARP = 10;
@@ -513,37 +511,12 @@ struct PairCtl {
 };
 constexpr uint32_t kPairSmem = PAIR_EPI + 2 * EPI_BUF + sizeof(PairCtl) + 1024;  // + alignment slack
 
-// The operands' ring.  A stage is as large as its tile needs it: the weights' units, and of each
-// half's rows as many as they fill, so that short tiles have more stages in flight (51 units: four
-// stages of 512 rows, six of 256, nine of 32).  Producer and MMA thread place stages by the same
-// rule: one behind the other, at the start where the end is too near.
-struct RingPlace {
-  uint32_t head = 0, slot = 0, phase = 0;
-  // start of a stage of `units`; the barriers' slot and phase are those of the members
-  __device__ uint32_t take(uint32_t units, uint32_t& skipped) {
-    const bool wraps = head + units > RING;
-    skipped = wraps ? RING - head : 0;
-    const uint32_t at = wraps ? 0 : head;
-    head = at + units;
-    return at;
-  }
-  __device__ void next() {
-    if (++slot == MAX_STAGES) { slot = 0; phase ^= 1; }
-  }
-};
-
 // Rows of half h of a tile as the MMA counts them: a multiple of 16, or 0.
 template <class P>
 __device__ __forceinline__ int half_height(const TileCoord& tc, int h) {
   constexpr int kMost = P::ROWS < 256 ? P::ROWS : 256;
   const int64_t left = tc.m_end - tc.m0 - 256 * h;
   return left >= kMost ? kMost : left <= 0 ? 0 : ((int)left + 15) / 16 * 16;
-}
-
-// Units of half h's rows in a stage: 128, 64 or 32 rows, the box of one load (several small ones
-// cost more than the rows they save: 64 groups of 160 rows 350 us with 3 of 32 rows, 313 with 128).
-__device__ __forceinline__ uint32_t half_units(int height) {
-  return height > 128 ? 4 : height > 64 ? 2 : height > 0 ? 1 : 0;
 }
 
 // Whether `ok` holds in all 128 threads of a group of the epilogue's warps, the same answer in each.
@@ -668,19 +641,13 @@ product16_pair_kernel(const __grid_constant__ CUtensorMap tmA,    // 128 rows of
       // Bands of row tiles keep their rows of A in L2 while B goes by.
       const uint64_t pol_a = l2_policy_evict_last(), pol_b = l2_policy_evict_normal();
       RingPlace ring;
-      uint32_t oldest = 0, oldest_phase = 0;      // the barrier of the oldest stage in the ring
-      uint32_t stages = 0, used = 0;              // in the ring: stages, units (and skipped ones)
-      uint64_t sizes = 0;                         // of the stages in the ring, the oldest's first
-      constexpr int kBits = 6;
+      RingFill fill;
       bool ok = true;
       auto free_oldest = [&](bool timed) {
-        if (timed ? !mbar_wait_timed(empty_bar(oldest), oldest_phase)
-                  : !mbar_wait_sleep(empty_bar(oldest), oldest_phase, abort))
+        if (timed ? !mbar_wait_timed(empty_bar(fill.oldest), fill.oldest_phase)
+                  : !mbar_wait_sleep(empty_bar(fill.oldest), fill.oldest_phase, abort))
           return false;
-        if (++oldest == MAX_STAGES) { oldest = 0; oldest_phase ^= 1; }
-        used -= (uint32_t)(sizes & ((1u << kBits) - 1));
-        sizes >>= kBits;
-        --stages;
+        fill.drop_oldest();
         return true;
       };
       for (bool have = first_tile(); ok && have; have = ok && next_tile(ok)) {
@@ -698,15 +665,12 @@ product16_pair_kernel(const __grid_constant__ CUtensorMap tmA,    // 128 rows of
         for (int kb = kb0; kb < kb1; ++kb) {
           uint32_t skipped;
           const uint32_t at = ring.take(units, skipped);
-          while (ok && (used + units + skipped > RING || stages + 1 == MAX_STAGES))
-            ok = free_oldest(false);
+          while (ok && !fill.fits(units + skipped)) ok = free_oldest(false);
           if (!ok) {
             give_up(args.err, abort);
             break;
           }
-          used += units + skipped;
-          sizes |= (uint64_t)(units + skipped) << (kBits * stages);
-          ++stages;
+          fill.put(units + skipped);
           const uint32_t w = base + at * UNIT;
           // both CTAs' bytes are counted on the leader's barrier
           const uint32_t bar = mapa_shared(full_bar(ring.slot), leader);
@@ -732,7 +696,7 @@ product16_pair_kernel(const __grid_constant__ CUtensorMap tmA,    // 128 rows of
       if (!ok) give_up(args.err, abort);
       // This CTA's last loads land, and the MMAs that read them end, before it can exit (after
       // an abort the first wait runs out, which is time enough for the loads).
-      while (stages > 0 && free_oldest(true)) {
+      while (fill.stages > 0 && free_oldest(true)) {
       }
     }
     __syncwarp();
