@@ -58,7 +58,7 @@ EXPORTED = ("bsfp8_grouped_gemm", "bsmxfp8_grouped_gemm", "bsfp8_grouped_gemm_id
             "bsmx_moe_sort_workspace", "bsmx_moe_sort", "bsmx_moe_combine",
             "bsmx_moe_combine_backward", "bs16_grouped_gemm", "bs16_grouped_wgrad",
             "bsfp8_grouped_wgrad", "bsfp8_quantize_columns", "bsmx_swiglu_backward",
-            "bsfp8_get_device_error", "bsfp8_check_wait_timeout", "bsfp8_status_string")
+            "bs16_grouped_gemm_plan", "bsfp8_grouped_wgrad_plan", "bsfp8_get_device_error", "bsfp8_check_wait_timeout", "bsfp8_status_string")
 
 
 class BsFp8Error(RuntimeError):
@@ -128,6 +128,10 @@ def load_library() -> ctypes.CDLL:
         lib.bsfp8_quantize_columns.restype = i32
         lib.bsmx_swiglu_backward.argtypes = [i32, i32, p, p, p, p, p, p, i64, i32, p]
         lib.bsmx_swiglu_backward.restype = i32
+        lib.bs16_grouped_gemm_plan.argtypes = [i32, i32, i64, i32, i32, i32, i32, p, p]
+        lib.bs16_grouped_gemm_plan.restype = i32
+        lib.bsfp8_grouped_wgrad_plan.argtypes = [i32, i32, i32, i64, i32, i32, i32, i32, i32, p]
+        lib.bsfp8_grouped_wgrad_plan.restype = i32
         lib.bsfp8_get_device_error.argtypes = [p, ctypes.POINTER(ctypes.c_int)]
         lib.bsfp8_get_device_error.restype = i32
         lib.bsfp8_check_wait_timeout.argtypes = [ctypes.c_int64, p]
@@ -445,6 +449,33 @@ def bsmx_swiglu_backward(h, d_act, rows: int, N: int, d_h=None, act=None, q=None
         _type(type), QUANT_FORMATS[format], h, d_act, d_h, act, q, scales, rows, N, stream)
     if st:
         raise BsFp8Error(st, "bsmx_swiglu_backward")
+
+
+def bs16_grouped_gemm_plan(M_total: int, N: int, K: int, num_groups: int, transposed: bool = False,
+                           type: str = "bf16", num_sms: int = 152, clusters=(76, 36, 15)) -> dict:
+    """The form that bs16_grouped_gemm launches for these sizes.  clusters: how many of 2, 4 and 8 CTAs
+    the device holds at once (host only; those of a GB300), or None: the current device is asked."""
+    out = (ctypes.c_int32 * 5)()
+    held = None if clusters is None else (ctypes.c_int32 * 3)(*clusters)
+    st = load_library().bs16_grouped_gemm_plan(TYPES[type], 1 if transposed else 0, M_total, N, K,
+                                               num_groups, num_sms, held, out)
+    if st != BSFP8_OK:
+        raise BsFp8Error(st, "bs16_grouped_gemm_plan")
+    return dict(zip(("tile_rows", "tile_cols", "ctas_per_tile", "k_shared_by", "k_chunk"), out))
+
+
+def bsfp8_grouped_wgrad_plan(M_total: int, N: int, K: int, num_experts: int, fp8: bool,
+                             out_type: str = "fp32", added: bool = False, num_sms: int = 152,
+                             clusters_of_8: int | None = 15) -> dict:
+    """The form of bsfp8_grouped_wgrad (fp8) or bs16_grouped_wgrad.  clusters_of_8: how many the device
+    holds at once (host only), or None: the current device is asked."""
+    out = (ctypes.c_int32 * 3)()
+    st = load_library().bsfp8_grouped_wgrad_plan(1 if fp8 else 0, TYPES[out_type], 1 if added else 0,
+                                                 M_total, N, K, num_experts, num_sms,
+                                                 -1 if clusters_of_8 is None else clusters_of_8, out)
+    if st != BSFP8_OK:
+        raise BsFp8Error(st, "bsfp8_grouped_wgrad_plan")
+    return {"stage_rows": out[0], "rows_shared_by": out[1], "stored_by_tma": bool(out[2])}
 
 
 def bsmxfp8_tmem_plan(block_k: int, epilogue_n: int, vec: int, overlap: bool) -> dict:

@@ -68,6 +68,23 @@ extern "C" bsfp8_status bs16_grouped_gemm(int type, int transposed, const void* 
       sms, stream));
 }
 
+extern "C" bsfp8_status bs16_grouped_gemm_plan(int type, int transposed, int64_t M_total, int N,
+                                               int K, int num_groups, int num_sms,
+                                               const int32_t* clusters, int32_t* out) {
+  if (!out) return BSFP8_ERR_NULL;
+  if (!half_type(type)) return BSFP8_ERR_FORMAT;
+  if (M_total < 1 || !grouped_rows_ok(M_total) || !matrix_ok(N, K, 8) || !groups_ok(num_groups) ||
+      num_sms < 2)
+    return BSFP8_ERR_SHAPE;
+  const Product16Plan p = plan_product16(
+      Product16Args{nullptr, nullptr, M_total, N, K, num_groups, num_groups, nullptr, nullptr,
+                    nullptr, nullptr, type == BSMX_BF16, transposed != 0},
+      num_sms, clusters);
+  const int32_t form[5] = {p.rows, p.cols, p.ctas, p.split, p.chunk};
+  for (int i = 0; i < 5; ++i) out[i] = form[i];
+  return BSFP8_OK;
+}
+
 extern "C" bsfp8_status bs16_grouped_wgrad(int type, int out_type, const void* dC, const void* A,
                                            const int32_t* group_offsets, const void* add, void* dB,
                                            int64_t M_total, int N, int K, int num_experts,
@@ -87,6 +104,28 @@ extern "C" bsfp8_status bsfp8_grouped_wgrad(int out_type, const void* dC, const 
   return wgrad(WgradArgs{group_offsets, M_total, N, K, num_experts, nullptr, dC, A, dc_scales,
                          a_scales, add, dB, out_type, true, false},
                128, stream);
+}
+
+extern "C" bsfp8_status bsfp8_grouped_wgrad_plan(int fp8, int out_type, int added,
+                                                 int64_t M_total, int N, int K, int num_experts,
+                                                 int num_sms, int clusters_of_8, int32_t* out) {
+  if (!out) return BSFP8_ERR_NULL;
+  if (out_type < BSMX_BF16 || out_type > BSMX_FP32) return BSFP8_ERR_FORMAT;
+  if (!grouped_rows_ok(M_total) || !matrix_ok(N, K, fp8 ? 128 : 8) || !groups_ok(num_experts) ||
+      num_sms < 2)
+    return BSFP8_ERR_SHAPE;
+  WgradArgs a{};
+  a.M_total = M_total;
+  a.N = N;
+  a.K = K;
+  a.E = num_experts;
+  a.out_type = out_type;
+  a.fp8 = fp8 != 0;
+  a.add = added ? &a : nullptr;  // (only whether there is one counts)
+  const WgradPlan p = plan_wgrad(a, num_sms, clusters_of_8);
+  const int32_t form[3] = {p.rows, p.split, p.staged};
+  for (int i = 0; i < 3; ++i) out[i] = form[i];
+  return BSFP8_OK;
 }
 
 extern "C" bsfp8_status bsfp8_quantize_columns(int x_type, const void* x,

@@ -44,6 +44,15 @@ struct Product16Args {
 };
 cudaError_t launch_product16(const Product16Args& a, int num_sms, cudaStream_t stream);
 
+// The form that a product is launched in: a tile, the CTAs that compute it, how many such units share
+// its K, and the K that is summed in one accumulator (0: each unit's whole part).  The sizes, type and
+// direction of `a` matter only.  clusters: of 2, 4 and 8 CTAs, that a device holds at once; nullptr: the
+// current one is asked.
+struct Product16Plan {
+  int rows, cols, ctas, split, chunk;
+};
+Product16Plan plan_product16(const Product16Args& a, int num_sms, const int32_t* clusters);
+
 // dB[e, n, k] = add[e, n, k] + sum over the rows m of group e of dC[m, n] A[m, k]; e4m3 operands
 // (fp8) have a scale for each block of 128 rows of a column.
 enum GradType : int { GRAD_BF16 = 0, GRAD_FP16 = 1, GRAD_FP32 = 2 };
@@ -64,6 +73,14 @@ struct WgradArgs {
   bool bf16;               // of 16-bit operands
 };
 cudaError_t launch_wgrad(const WgradArgs& a, int num_sms, cudaStream_t stream);
+
+// The form of a weight gradient: rows in a stage, pairs that share a tile's rows, and whether the
+// gradients are stored by TMA.  clusters: of 8 CTAs, that a device holds at once; negative: asked.
+struct WgradPlan {
+  int rows, split;
+  bool staged;
+};
+WgradPlan plan_wgrad(const WgradArgs& a, int num_sms, int64_t clusters);
 
 // q = e4m3(x / scale) in blocks of 128 rows of a column, counted from each group's first row.
 struct ColumnsArgs {

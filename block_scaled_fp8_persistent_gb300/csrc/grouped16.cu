@@ -1060,8 +1060,29 @@ int64_t pairs_at_once() {
   return clusters_at_once<product16_pair_kernel<P>>(2 * P::SPLIT, PAIR_THREADS, kPairSmem);
 }
 
+// How many clusters the device holds at once of a form whose K is shared `split` ways: those given (of
+// 2, 4 and 8 CTAs), or the current device's.
 template <bool BT>
-cudaError_t choose(const Product16Args& a, int num_sms, cudaStream_t stream) {
+struct AtOnce {
+  const int32_t* given;
+  int64_t few(int split) const {
+    if (given) return given[split == 2 ? 0 : split == 4 ? 1 : 2];
+    return split == 2   ? few_at_once<Few<BT, 2>>()
+           : split == 4 ? few_at_once<Few<BT, 4>>()
+                        : few_at_once<Few<BT, 8>>();
+  }
+  int64_t pairs(int split) const {
+    if (given) return given[split == 2 ? 1 : 2];
+    return split == 2 ? pairs_at_once<Pair<BT, 128, 2>>() : pairs_at_once<Pair<BT, 128, 4>>();
+  }
+};
+
+template <bool BT>
+Product16Plan choose(const Product16Args& a, int num_sms, const AtOnce<BT>& at_once) {
+  const auto few = [](int split) { return Product16Plan{FEW_ROWS, FEW_COLS, 1, split, 0}; };
+  const auto pair = [](int rows, int split, int chunk) {
+    return Product16Plan{rows, 256, 2, split, chunk};
+  };
   // A tile's K is shared where that leaves each of the tile's CTAs a part and an SM (a second round of
   // clusters costs more than sharing gains: 1000 rows, 512 x 2048, shared by four pairs 20.7 us, by two
   // 12.8).
@@ -1070,19 +1091,16 @@ cudaError_t choose(const Product16Args& a, int num_sms, cudaStream_t stream) {
   // whether one accumulator will do for each of `split` parts of K
   const int most_blocks = a.bf16 ? MOST_BLOCKS_BF16 : MOST_BLOCKS_FP16;
   auto one_sum = [&](int split) { return (blocks + split - 1) / split <= most_blocks; };
-  if (blocks >= 16 && one_sum(8) && few_tiles <= few_at_once<Few<BT, 8>>())
-    return launch_few<Few<BT, 8>>(a, few_tiles, num_sms, stream);
-  if (blocks >= 8 && one_sum(4) && few_tiles <= few_at_once<Few<BT, 4>>())
-    return launch_few<Few<BT, 4>>(a, few_tiles, num_sms, stream);
-  if (blocks >= 4 && one_sum(2) && few_tiles <= few_at_once<Few<BT, 2>>())
-    return launch_few<Few<BT, 2>>(a, few_tiles, num_sms, stream);
+  if (blocks >= 16 && one_sum(8) && few_tiles <= at_once.few(8)) return few(8);
+  if (blocks >= 8 && one_sum(4) && few_tiles <= at_once.few(4)) return few(4);
+  if (blocks >= 4 && one_sum(2) && few_tiles <= at_once.few(2)) return few(2);
   // Up to 8 rows per group on average, most groups are one tile of 32 rows: less to load and to
   // set up than in tiles of pairs (64 groups of 1 row, 2048 x 2048: 81 us against 88; 16 of 8, 2048
   // x 4096: 45 and 48).  With more of them a few groups can hold many, and each reads its weights
   // once per 32 rows (4027 rows over 128 groups, the largest 753, 4096 x 2048: 422 us against 330;
   // 4096 rows in one of them 222 and 51; 16 rows in each 327 and 322).
   if (one_sum(1) && (a.M_total <= FEW_ROWS || a.M_total <= (int64_t)8 * a.E))
-    return launch_few<Few<BT, 1>>(a, few_tiles, num_sms, stream);
+    return few(1);
   const int64_t units = num_sms / 2;
   // about how many tiles there are: the last of a group is half full
   auto tiles = [&](int rows) {
@@ -1112,22 +1130,47 @@ cudaError_t choose(const Product16Args& a, int num_sms, cudaStream_t stream) {
   const double least = !one_sum(1) ? c256 : low < high ? low : high;
   const int64_t most = most_tiles(a, 128, 256);
   if (blocks >= 16 && one_sum(4) && cost(128, 4) < least && cost(128, 4) < cost(128, 2) &&
-      most <= pairs_at_once<Pair<BT, 128, 4>>())
-    return launch_pair<Pair<BT, 128, 4>>(a, num_sms, stream);
-  if (blocks >= 8 && one_sum(2) && cost(128, 2) < least && most <= pairs_at_once<Pair<BT, 128, 2>>())
-    return launch_pair<Pair<BT, 128, 2>>(a, num_sms, stream);
-  if (!one_sum(1)) return launch_pair<Pair<BT, 256, 1, CHUNK_BLOCKS>>(a, num_sms, stream);
-  if (c256 == least) return launch_pair<Pair<BT, 256>>(a, num_sms, stream);
-  if (c512 == least) return launch_pair<Pair<BT, 512>>(a, num_sms, stream);
-  return c128 == least ? launch_pair<Pair<BT, 128>>(a, num_sms, stream)
-                       : launch_pair<Pair<BT, 64>>(a, num_sms, stream);
+      most <= at_once.pairs(4))
+    return pair(128, 4, 0);
+  if (blocks >= 8 && one_sum(2) && cost(128, 2) < least && most <= at_once.pairs(2))
+    return pair(128, 2, 0);
+  if (!one_sum(1)) return pair(256, 1, CHUNK_BLOCKS * BK);
+  return pair(c256 == least ? 256 : c512 == least ? 512 : c128 == least ? 128 : 64, 1, 0);
+}
+
+template <bool BT>
+cudaError_t launch_chosen(const Product16Args& a, int num_sms, cudaStream_t stream) {
+  const Product16Plan p = choose<BT>(a, num_sms, AtOnce<BT>{nullptr});
+  if (p.ctas == 1) {
+    const int64_t tiles = most_tiles(a, FEW_ROWS, FEW_COLS);
+    switch (p.split) {
+      case 8: return launch_few<Few<BT, 8>>(a, tiles, num_sms, stream);
+      case 4: return launch_few<Few<BT, 4>>(a, tiles, num_sms, stream);
+      case 2: return launch_few<Few<BT, 2>>(a, tiles, num_sms, stream);
+      default: return launch_few<Few<BT, 1>>(a, tiles, num_sms, stream);
+    }
+  }
+  if (p.chunk) return launch_pair<Pair<BT, 256, 1, CHUNK_BLOCKS>>(a, num_sms, stream);
+  if (p.split == 4) return launch_pair<Pair<BT, 128, 4>>(a, num_sms, stream);
+  if (p.split == 2) return launch_pair<Pair<BT, 128, 2>>(a, num_sms, stream);
+  switch (p.rows) {
+    case 512: return launch_pair<Pair<BT, 512>>(a, num_sms, stream);
+    case 256: return launch_pair<Pair<BT, 256>>(a, num_sms, stream);
+    case 128: return launch_pair<Pair<BT, 128>>(a, num_sms, stream);
+    default: return launch_pair<Pair<BT, 64>>(a, num_sms, stream);
+  }
 }
 
 }  // namespace g16
 
 cudaError_t launch_product16(const Product16Args& a, int num_sms, cudaStream_t stream) {
-  return a.transposed ? g16::choose<true>(a, num_sms, stream)
-                      : g16::choose<false>(a, num_sms, stream);
+  return a.transposed ? g16::launch_chosen<true>(a, num_sms, stream)
+                      : g16::launch_chosen<false>(a, num_sms, stream);
+}
+
+Product16Plan plan_product16(const Product16Args& a, int num_sms, const int32_t* clusters) {
+  return a.transposed ? g16::choose<true>(a, num_sms, g16::AtOnce<true>{clusters})
+                      : g16::choose<false>(a, num_sms, g16::AtOnce<false>{clusters});
 }
 
 }  // namespace bsfp8

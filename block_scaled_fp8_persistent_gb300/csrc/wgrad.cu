@@ -799,17 +799,19 @@ cudaError_t by_type(const WgradArgs& a, int num_sms, cudaStream_t stream) {
   }
 }
 
+using Split8 = Cfg<true, 128, 4, false, 4>;
+using Split16 = Cfg<false, 128, 3, false, 4>;
+
 }  // namespace wg
 
-cudaError_t launch_wgrad(const WgradArgs& a, int num_sms, cudaStream_t stream) {
+WgradPlan plan_wgrad(const WgradArgs& a, int num_sms, int64_t clusters) {
   // Few tiles and many rows: four pairs share a tile's rows (512 x 512: 8192 rows 54 -> 21 us; 304 x 416:
   // 1000 rows 12.6 -> 11.0, 3 groups of 900 12.4 -> 11.6, of 600 10.9 -> 11.5).
   const int64_t tiles = (int64_t)a.E * ((a.N + 255) / 256) * ((a.K + 255) / 256);
-  using Split8 = wg::Cfg<true, 128, 4, false, 4>;
-  using Split16 = wg::Cfg<false, 128, 3, false, 4>;
-  const bool split =
-      a.M_total >= (int64_t)768 * a.E &&
-      tiles <= (a.fp8 ? wg::at_once<Split8>() : wg::at_once<Split16>());
+  if (a.M_total >= (int64_t)768 * a.E) {
+    if (clusters < 0) clusters = a.fp8 ? wg::at_once<wg::Split8>() : wg::at_once<wg::Split16>();
+    if (tiles <= clusters) return WgradPlan{128, 4, false};
+  }
   // The gradients go out through shared memory and TMA, so that the epilogue takes up the next tile's
   // sums at once, or straight from the threads, in whole lines.  Which is faster was measured (32
   // experts of 2048 x 7168, us straight and by TMA):
@@ -823,20 +825,24 @@ cudaError_t launch_wgrad(const WgradArgs& a, int num_sms, cudaStream_t stream) {
   //     and 366), else straight (512 rows 380 and 391)
   const int64_t rounds = (tiles * 2 + num_sms - 1) / num_sms;
   const bool wide = a.out_type == GRAD_FP32;
-  if (a.fp8) {
-    if (split) return wg::by_type<Split8>(a, num_sms, stream);
-    const bool staged = !wide || (!a.add && (rounds <= 4 || a.M_total >= (int64_t)384 * a.E));
-    return staged ? wg::by_type<wg::Cfg<true, 128, 4, true>>(a, num_sms, stream)
-                  : wg::launch<wg::Cfg<true, 128, 4, false>, GRAD_FP32>(a, num_sms, stream);
-  }
-  if (split) return wg::by_type<Split16>(a, num_sms, stream);
   const bool long_groups = a.M_total >= (int64_t)384 * a.E;
-  const bool staged = a.add ? !wide : rounds <= 4 || (wide && long_groups);
-  if (long_groups)
-    return staged ? wg::by_type<wg::Cfg<false, 128, 3, true>>(a, num_sms, stream)
-                  : wg::by_type<wg::Cfg<false, 128, 3, false>>(a, num_sms, stream);
-  return staged ? wg::by_type<wg::Cfg<false, 64, 4, true>>(a, num_sms, stream)
-                : wg::by_type<wg::Cfg<false, 64, 4, false>>(a, num_sms, stream);
+  if (a.fp8) return WgradPlan{128, 1, !wide || (!a.add && (rounds <= 4 || long_groups))};
+  return WgradPlan{long_groups ? 128 : 64, 1, a.add ? !wide : rounds <= 4 || (wide && long_groups)};
+}
+
+cudaError_t launch_wgrad(const WgradArgs& a, int num_sms, cudaStream_t stream) {
+  const WgradPlan p = plan_wgrad(a, num_sms, -1);
+  if (a.fp8) {
+    if (p.split > 1) return wg::by_type<wg::Split8>(a, num_sms, stream);
+    return p.staged ? wg::by_type<wg::Cfg<true, 128, 4, true>>(a, num_sms, stream)
+                    : wg::launch<wg::Cfg<true, 128, 4, false>, GRAD_FP32>(a, num_sms, stream);
+  }
+  if (p.split > 1) return wg::by_type<wg::Split16>(a, num_sms, stream);
+  if (p.rows == 128)
+    return p.staged ? wg::by_type<wg::Cfg<false, 128, 3, true>>(a, num_sms, stream)
+                    : wg::by_type<wg::Cfg<false, 128, 3, false>>(a, num_sms, stream);
+  return p.staged ? wg::by_type<wg::Cfg<false, 64, 4, true>>(a, num_sms, stream)
+                  : wg::by_type<wg::Cfg<false, 64, 4, false>>(a, num_sms, stream);
 }
 
 }  // namespace bsfp8

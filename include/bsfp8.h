@@ -534,6 +534,28 @@ bsfp8_status bsfp8_blockwise_plan(int64_t M_total, int N, int num_experts, int n
                                   int32_t* out);
 
 /*
+ * The form that bs16_grouped_gemm launches for these sizes on a device with num_sms SMs: out[0] = tile
+ * rows, out[1] = tile columns, out[2] = CTAs per tile, out[3] = how many of these share a tile's K,
+ * out[4] = the K that is summed in one accumulator before it is added up in fp32 (0: each one's whole
+ * part).  `clusters`: how many clusters of 2, 4 and 8 CTAs the device holds at once, three numbers, with
+ * which the function is host only (a GB300: 76, 36, 15); NULL: the current device is asked.  A
+ * performance choice, but for the order and the accuracy of the sums.  Bad input as for the product
+ * itself; M_total >= 1.
+ */
+bsfp8_status bs16_grouped_gemm_plan(int type, int transposed, int64_t M_total, int N, int K,
+                                    int num_groups, int num_sms, const int32_t* clusters,
+                                    int32_t* out);
+
+/*
+ * The same of bs16_grouped_wgrad (fp8 == 0) and bsfp8_grouped_wgrad: out[0] = rows that are loaded at a
+ * time, out[1] = how many pairs of CTAs share a tile's rows, out[2] = 1 where the gradients are stored by
+ * TMA.  added: whether there is an `add`.  clusters_of_8: how many clusters of 8 CTAs the device holds
+ * at once (host only then); negative: the current device is asked.
+ */
+bsfp8_status bsfp8_grouped_wgrad_plan(int fp8, int out_type, int added, int64_t M_total, int N, int K,
+                                      int num_experts, int num_sms, int clusters_of_8, int32_t* out);
+
+/*
  * Kernel plan bsmxfp8_grouped_gemm (and its _ids / _prepacked forms) uses for M_total token
  * rows over num_experts row groups (host only, no GPU use; BSFP8_MX_KERNEL and BSFP8_MX_TN
  * are honoured as in the GEMM): out[0] = 0 for swap-AB tiles, 1 for CTA-pair 256 x 256 tiles,
