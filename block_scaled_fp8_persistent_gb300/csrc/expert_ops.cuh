@@ -164,32 +164,6 @@ int64_t clusters_at_once(int cluster, int threads, size_t smem) {
 // device side
 // ---------------------------------------------------------------------------------------
 
-// Groups of rows may end before M_total: offsets[0] == 0 <= offsets[1] <= .. <= offsets[E] <=
-// M_total.  One full warp checks them (and the expert ids, where there are any) and counts the
-// tiles of BM rows; every lane gets the status (0 or a device error code) and the count.
-template <int BM>
-__device__ __forceinline__ int check_groups(const int32_t* off, const int32_t* ids, int E,
-                                            int num_experts, int64_t M_total,
-                                            int64_t& row_tiles) {
-  const uint32_t lane = lane_id();
-  int good = 1, good_ids = 1;
-  long long tiles = 0;
-  for (int e = (int)lane; e < E; e += 32) {
-    const int a = off[e], b = off[e + 1];
-    if (a < 0 || b < a || b > M_total || (e == 0 && a != 0)) good = 0;
-    else tiles += ((int64_t)b - a + BM - 1) / BM;
-    if (ids) {
-      const int x = ids[e];
-      if (x < 0 || x >= num_experts) good_ids = 0;
-    }
-  }
-  for (int s = 16; s > 0; s >>= 1) tiles += __shfl_xor_sync(0xffffffffu, tiles, s);
-  row_tiles = tiles;
-  return !__all_sync(0xffffffffu, good)       ? DEV_BAD_OFFSETS
-         : !__all_sync(0xffffffffu, good_ids) ? DEV_BAD_EXPERT_IDS
-                                              : 0;
-}
-
 __device__ __forceinline__ void give_up(int* err, volatile int* abort) {
   atomicCAS(err, 0, (int)DEV_TIMEOUT);
   *abort = 1;

@@ -67,7 +67,8 @@ struct GroupList {
   int2 at[LISTED + 1];
 };
 
-// One full warp lists the groups, checks them and counts their tiles of BM rows (check_groups).
+// One full warp lists the groups, checks them (as check_offsets does, and the expert ids) and counts
+// their tiles of BM rows.
 template <int BM>
 __device__ __forceinline__ int list_groups(const Product16Args& a, GroupList& list, int64_t& row_tiles) {
   constexpr int kAhead = 4;  // loads of 32 groups each, under way together

@@ -15,7 +15,6 @@
 // columns 8 c.. of the rows i, i + 16, .., so that 16 (8) threads read 256 (128) bytes of a row
 // (16-bit) and write half as many.  Which rows those are the offsets say: block b of the scales belongs to the last
 // group e with offsets[e] / 128 + e <= b, which the threads count together, once for all tiles.
-#include <atomic>
 #include <cuda_fp16.h>
 
 #include "expert_ops.cuh"
@@ -109,7 +108,7 @@ __device__ __forceinline__ float2 pair(const Eight<XT>& x, int j) {
 
 template <int XT, bool GATHER>
 __global__ void __launch_bounds__(Tile<XT, GATHER>::THREADS, Tile<XT, GATHER>::RESIDENT)
-    columns_kernel(ColumnsArgs a, int blocks, int each, bool early) {
+    columns_kernel(ColumnsArgs a, int blocks, int each) {
   extern __shared__ __align__(16) uint8_t stages[];
   using T = Tile<XT, GATHER>;
   constexpr int STAGES = T::STAGES, kTileCols = T::COLS, kThreads = T::THREADS;
@@ -120,10 +119,15 @@ __global__ void __launch_bounds__(Tile<XT, GATHER>::THREADS, Tile<XT, GATHER>::R
   __shared__ __align__(16) float inverse[2][kTileCols];
   __shared__ int counts[kThreads / 32];
   const int stripe = blockIdx.x / blocks, b = blockIdx.x - stripe * blocks;
-  begin_early(early);
+  begin_early(true);  // its blocks move 24 KB and more
   // the groups whose first block is b or before it; a group's first block grows with the group
   int before = 0;
-  for (int e = threadIdx.x; e < a.E; e += kThreads) before += a.offsets[e] / kBlockRows + e <= b;
+  for (int e = threadIdx.x; e < a.E; e += kThreads) {
+    const int lo = a.offsets[e], hi = a.offsets[e + 1];
+    before += lo / kBlockRows + e <= b;
+    const bool good = lo >= 0 && lo <= hi && hi <= a.M_total && (e > 0 || lo == 0);
+    if (!good && blockIdx.x == 0) atomicCAS(a.err, 0, (int)DEV_BAD_OFFSETS);
+  }
 #pragma unroll
   for (int d = 16; d > 0; d /= 2) before += __shfl_xor_sync(0xffffffffu, before, d);
   if (threadIdx.x % 32 == 0) counts[threadIdx.x / 32] = before;
@@ -131,11 +135,6 @@ __global__ void __launch_bounds__(Tile<XT, GATHER>::THREADS, Tile<XT, GATHER>::R
   int e = -1;
 #pragma unroll
   for (int i = 0; i < kThreads / 32; ++i) e += counts[i];
-  if (blockIdx.x == 0 && threadIdx.x < 32) {
-    int64_t unused;
-    const int status = check_groups<1>(a.offsets, nullptr, a.E, a.E, a.M_total, unused);
-    if (status && threadIdx.x == 0) atomicCAS(a.err, 0, status);
-  }
   if (e < 0) return;
   const int64_t r0 = a.offsets[e], r1 = a.offsets[e + 1];
   const int64_t first = r0 + (b - (r0 / kBlockRows + e)) * (int64_t)kBlockRows;
@@ -266,22 +265,14 @@ cudaError_t columns_as(const ColumnsArgs& a, cudaStream_t stream) {
   // blocks, 32896 gathered rows of 512 17.0 -> 14.6 us, 6000 rows of 2176 in 60 groups 13.2 -> 10.1).
   using T = Tile<XT, GATHER>;
   constexpr int kSmem = T::STAGES * T::STAGE_BYTES;
-  static std::atomic<bool> attr_set[64];  // per device; several host threads may launch
-  int dev = 0;
-  cudaGetDevice(&dev);
-  if (dev >= 64 || !attr_set[dev].load(std::memory_order_acquire)) {
-    const cudaError_t e = cudaFuncSetAttribute(columns_kernel<XT, GATHER>,
-                                               cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
-    if (e != cudaSuccess) return e;
-    if (dev < 64) attr_set[dev].store(true, std::memory_order_release);
-  }
+  const cudaError_t e = allow_smem<columns_kernel<XT, GATHER>>(kSmem);
+  if (e != cudaSuccess) return e;
   const int64_t blocks = a.M_total / kBlockRows + a.E;
   const int tiles = a.K / T::COLS;
   const int64_t most = blocks * tiles < 8000 ? 900 : 2500, want = (most + blocks - 1) / blocks;
   const int each = (int)((tiles + want - 1) / want);
   const dim3 grid((unsigned)(blocks * ((tiles + each - 1) / each)));
-  const bool early = starts_early(grid, (int64_t)kBlockRows * T::COLS * 3 * each);
-  return launch(columns_kernel<XT, GATHER>, grid, T::THREADS, kSmem, early, stream, 1, a, (int)blocks, each, early);
+  return launch(columns_kernel<XT, GATHER>, grid, T::THREADS, kSmem, true, stream, 1, a, (int)blocks, each);
 }
 
 }  // namespace

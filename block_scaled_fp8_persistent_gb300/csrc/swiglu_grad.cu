@@ -49,9 +49,8 @@ __device__ __forceinline__ void store16(void* p, int64_t at, const float (&v)[16
 }
 
 template <int FMT, int XT, bool Q>
-__global__ void __launch_bounds__(kPieceThreads, 3) swiglu_backward_kernel(SwigluBackwardArgs a,
-                                                                           bool early) {
-  begin_early(early);
+__global__ void __launch_bounds__(kPieceThreads, 3) swiglu_backward_kernel(SwigluBackwardArgs a) {
+  begin_early(true);  // its blocks move 32 KB and more
   const int items = a.N / 16;
   const int64_t p = (int64_t)blockIdx.x * kPieceThreads + threadIdx.x;
   const int64_t t = p / items;
@@ -94,9 +93,7 @@ template <int FMT, int XT, bool Q>
 cudaError_t swiglu_backward_as(const SwigluBackwardArgs& a, cudaStream_t stream) {
   const int64_t pieces = a.rows * (a.N / 16);
   const dim3 grid((unsigned)((pieces + kPieceThreads - 1) / kPieceThreads));
-  const int each = 16 * (6 + (a.d_h ? 4 : 0) + (a.act ? 2 : 0) + (Q ? 2 : 0));
-  const bool early = starts_early(grid, (int64_t)kPieceThreads * each);
-  return launch(swiglu_backward_kernel<FMT, XT, Q>, grid, kPieceThreads, 0, early, stream, 1, a, early);
+  return launch(swiglu_backward_kernel<FMT, XT, Q>, grid, kPieceThreads, 0, true, stream, 1, a);
 }
 
 template <int FMT>

@@ -114,6 +114,17 @@ constexpr uint32_t smem_bytes() {
   return C::SMEM_CTL + sizeof(Ctl<C>) + 1024;  // + alignment slack
 }
 
+// Groups of rows may end before M_total: offsets[0] == 0 <= offsets[1] <= .. <= offsets[E] <=
+// M_total.  One full warp checks them; every lane gets the status (0 or a device error code).
+__device__ __forceinline__ int check_offsets(const int32_t* off, int E, int64_t M_total) {
+  int good = 1;
+  for (int e = (int)lane_id(); e < E; e += 32) {
+    const int a = off[e], b = off[e + 1];
+    if (a < 0 || b < a || b > M_total || (e == 0 && a != 0)) good = 0;
+  }
+  return __all_sync(0xffffffffu, good) ? 0 : DEV_BAD_OFFSETS;
+}
+
 // Tiles are numbered expert by expert, inside one in bands of 8 column tiles of dC, whose columns
 // of dC and A stay in L2 while the band's tiles are in flight.  An expert without rows has tiles
 // too: its gradient is written.  A role walks the tiles `stride` apart; the walk is a few integers
@@ -337,8 +348,7 @@ wgrad_kernel(const __grid_constant__ CUtensorMap tmC, const __grid_constant__ CU
   }
   wait_for_previous();
   if (warp == 2) {
-    int64_t unused;
-    const int status = check_groups<1>(args.offsets, nullptr, args.E, args.E, args.M_total, unused);
+    const int status = check_offsets(args.offsets, args.E, args.M_total);
     if (lane == 0) {
       ctl->valid = status == 0;
       if (status && blockIdx.x == 0) atomicCAS(args.err, 0, status);
