@@ -138,7 +138,7 @@ extern "C" bsfp8_status bsfp8_quantize_columns(int x_type, const void* x,
     return BSFP8_ERR_NULL;
   if (!grouped_rows_ok(M_total) || !rows_ok(x_rows) || K < 128 || K % 128 != 0 || K > (1 << 22) ||
       !groups_ok(num_groups) || top_k < 1 || top_k > 64 ||
-      (!slot_of_row && (top_k != 1 || x_rows != M_total)))
+      (M_total > 0 && !slot_of_row && (top_k != 1 || x_rows != M_total)))
     return BSFP8_ERR_SHAPE;
   if (!aligned(x, 16) || !aligned(q, 16) || !aligned(scales, 16) || !aligned(slot_of_row, 4) ||
       !aligned(group_offsets, 4))

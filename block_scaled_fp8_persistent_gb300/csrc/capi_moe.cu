@@ -43,7 +43,7 @@ extern "C" bsfp8_status bsmx_quantize(int format, int x_type, const void* x,
   if (!format_ok(format) || x_type < BSMX_BF16 || x_type > BSMX_FP32) return BSFP8_ERR_FORMAT;
   if (rows > 0 && (!x || !q || !scales)) return BSFP8_ERR_NULL;
   if (!width_ok(K) || !slots_ok(rows, top_k) || !rows_ok(out_rows) ||
-      (!row_of_slot && (top_k != 1 || out_rows != rows)))
+      (rows > 0 && !row_of_slot && (top_k != 1 || out_rows != rows)))
     return BSFP8_ERR_SHAPE;
   if (!aligned(x, 16) || !operand_aligned(format, q, scales) || !aligned(row_of_slot, 4))
     return BSFP8_ERR_ALIGN;

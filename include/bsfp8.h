@@ -475,8 +475,8 @@ bsfp8_status bsfp8_grouped_wgrad(int out_type, const void* dC, const void* A,
  *                     x [x_rows, K]; zeros where it is negative.  A row >= x_rows counts as zeros
  *                     and is recorded as BSFP8_ERR_DEVICE_ROWS.
  * x is of x_type (a bsmx_type).  Rows of q behind the last group and rows of scales that no block
- * has are left as they are.  K is a multiple of 128, at most 2^22; 1 <= top_k <= 64; x, q and
- * scales 16-byte aligned.
+ * has are left as they are; M_total == 0 is a no-op (slot_of_row may be NULL).  K is a multiple of
+ * 128, at most 2^22; 1 <= top_k <= 64; x, q and scales 16-byte aligned.
  */
 bsfp8_status bsfp8_quantize_columns(int x_type, const void* x, const int32_t* slot_of_row,
                                     int top_k, const int32_t* group_offsets, void* q,

@@ -1,5 +1,8 @@
 """The experts' operators in the forms that their rules choose for ordinary sizes, and in loops that
 are long enough to turn: against 64 bits, with the tolerances of test_expert_ops.py."""
+import os
+import sys
+
 import pytest
 import torch
 
@@ -8,6 +11,8 @@ import expert_forms as forms
 import expert_reference as ref
 
 pytestmark = pytest.mark.gpu
+
+sys.path.insert(0, os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "examples"))
 
 BF16, FP16, FP32 = torch.bfloat16, torch.float16, torch.float32
 
@@ -267,3 +272,17 @@ def test_same_bits_every_time_in_long_loops():
     _no_error()
     for later in runs[1:]:
         assert all(torch.equal(a, b) for a, b in zip(runs[0], later))
+
+
+# ------------------------------------------------------------------------------ a step of no tokens
+@pytest.mark.parametrize("fmt", ["bf16", "blockwise"])
+def test_step_without_tokens(fmt):
+    import moe_training
+    y, ids, weights, gate_up, down, d_out = moe_training.random_step(4, 256, 128, 3, 2)
+    experts = moe_training.TrainedExperts(gate_up, down, 2, fmt, max_rows=4)
+    experts.d_gate_up.fill_(1.5)
+    out, kept = experts.forward(y[:0], ids[:0], weights[:0])
+    d_y, d_weights = experts.backward(d_out[:0], kept)
+    _no_error()
+    assert out.shape == d_y.shape == (0, 256) and d_weights.shape == (0, 2)
+    assert torch.all(experts.d_gate_up == 1.5) and torch.all(experts.d_down == 0)

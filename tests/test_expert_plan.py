@@ -65,3 +65,14 @@ def test_refusals():
         bsfp8.bs16_grouped_gemm_plan(10, 12, 64, 1)
     with pytest.raises(bsfp8.BsFp8Error):
         bsfp8.bsfp8_grouped_wgrad_plan(10, 64, 64, 1, fp8=True)
+
+
+def test_gathering_no_rows_is_no_error():
+    """An empty map's address is NULL: with no rows that is not a map that is missing.  (Past the checks
+    the call wants a device.)"""
+    lib, FAKE = bsfp8.load_library(), 1 << 20
+    columns = lambda M, k: lib.bsfp8_quantize_columns(0, FAKE, None, k, FAKE, FAKE, FAKE, M, 4, 256, 2, None)  # noqa: E731
+    quantize = lambda rows, k: lib.bsmx_quantize(3, 0, FAKE, None, k, FAKE, FAKE, rows, 4, 256, None)  # noqa: E731
+    for call in (columns, quantize):
+        assert call(0, 8) != SHAPE and call(0, 1) != SHAPE
+        assert call(2, 8) == SHAPE and call(2, 1) == SHAPE and call(0, 0) == SHAPE
