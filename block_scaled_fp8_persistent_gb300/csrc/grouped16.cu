@@ -17,9 +17,9 @@
 //   clusters of CTAs share a tile's K and add up their parts through distributed shared memory.
 //   more rows: the tensor core, and the way from L2 to it.  A CTA pair takes 256 columns x up to 512
 //   rows; the rows are the MMA's N, which goes by 16, so that a group's last rows cost what they are.
-//   8192^3: 560 us, 1960 TFLOP/s (a library product 557).
-//   4096 rows over 7 uneven groups, 4096 x 7168: 144-168 us, the tensor cores busy 90 % of the time
-//   that the SMs are (181 in long runs, under the power cap).
+//   8192^3: 563 us, 1950 TFLOP/s (a library product 557).
+//   8 groups of 512 rows, 4096 x 7168: 153 us, the tensor cores busy 90 % of the time that the SMs
+//   are; uneven groups of 4096 rows in long runs, under the power cap, 181.
 // In both: a TMA producer, an MMA thread (per 64 K four MMAs of K = 16 and one commit) and epilogue
 // warps that store one tile while the next accumulates in the other half of TMEM.
 #include "expert_ops.cuh"
@@ -774,7 +774,8 @@ product16_pair_kernel(const __grid_constant__ CUtensorMap tmA,    // 128 rows of
     // ----------------------------------- plan ------------------------------------
     // Every pair follows the same plan, each for itself: the tiles in their order, each to the pair
     // that is done first by what tiles cost.  (One of every `stride` to each, as many pairs got more
-    // of the full ones: 7 groups of 585 rows, 4096 x 7168, 190 us, so 174.)  In 82 clocks per unit of 4 KB of operands, or 2 per row of MMAs.
+    // of the full ones: 7 groups of 585 rows, 4096 x 7168, 190 us, so 170-181.)  In 82 clocks per unit
+    // of 4 KB of operands, or 2 per row of MMAs.
     if (P::SPLIT == 1 && total_tiles > tile_stride) {
       const uint32_t mine = (uint32_t)tile0, pairs = (uint32_t)tile_stride;
       const uint32_t kb = (uint32_t)KB;
@@ -1114,7 +1115,7 @@ Product16Plan choose(const Product16Args& a, int num_sms, const AtOnce<BT>& at_o
   // than pairs the last ones leave some pairs idle, for half a tile or, of 512 rows, one.  Where little
   // is between them the higher ones: groups of many rows read their weights less often.  With each
   // height, us: 64 groups of 260 rows, 7168 x 2048: 496 in tiles of 256 and 400 of 512; 7 of 585, 4096 x
-  // 7168: 235 of 128, 174 of 256, 220 of 512; 8177 rows over 128 groups, the largest 1517, 4096 x 2048:
+  // 7168: 235 of 128, 170-181 of 256, 220 of 512; 8177 rows over 128 groups, the largest 1517, 4096 x 2048:
   // 367 of 128, 345 of 256; 545 rows, 3000 x 1256: 18.9 of 64, 13.3 of 128, 14.7 of 256; 128 rows, 4096
   // x 4096: 21.4, shared by two pairs 16.8; 1000 rows, 512 x 2048: 13.6, by two 12.8.
   auto cost = [&](int rows, int split) {

@@ -13,8 +13,9 @@
 // A block of threads takes the 128 rows of a scale block and walks over tiles of 128 or 64 columns, the
 // next ones under way (cp.async; a thread reads back what it copied itself): thread (i, c) the 8
 // columns 8 c.. of the rows i, i + 16, .., so that 16 (8) threads read 256 (128) bytes of a row
-// (16-bit) and write half as many.  Which rows those are the offsets say: block b of the scales belongs to the last
-// group e with offsets[e] / 128 + e <= b, which the threads count together, once for all tiles.
+// (16-bit) and write half as many.  Which rows those are the offsets say: block b of the scales belongs
+// to the last group e with offsets[e] / 128 + e <= b, which the threads count together, once for all
+// tiles; the first block reports offsets that are no partition.
 #include <cuda_fp16.h>
 
 #include "expert_ops.cuh"

@@ -3,8 +3,8 @@
 //   d_u = d g s,   d_g = d u s (1 + g (1 - s))
 //
 // written in 16 bits and / or quantised as the A of the products that follow, and act itself.  Bound
-// by HBM: a thread reads 16 elements of each of g, u and d once and writes what is made of them (32768
-// rows of 4096 with d_h, act and blockwise d_h: 297 us, 6.4 TB/s).  Straight pieces, no loop: three
+// by HBM: a thread reads 16 elements of each of g, u and d once and writes what is made of them (65536
+// rows of 2048 with d_h, act and blockwise d_h: 297 us, 6.4 TB/s).  Straight pieces, no loop: three
 // blocks of 256 threads to an SM hold their 48 values without spilling, and the rest is other blocks'.
 #include "moe_ops.cuh"
 #include "pieces.cuh"
